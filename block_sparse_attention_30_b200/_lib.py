@@ -17,7 +17,7 @@ STATUS_NAMES = {
 }
 
 # (name, restype, argtypes) for every entry point of include/vsa.h
-_i, _sz, _p = ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p
+_i, _ll, _sz, _p = ctypes.c_int, ctypes.c_longlong, ctypes.c_size_t, ctypes.c_void_p
 _SHAPE = [_i] * 9                       # B, heads, head_dim, T, H, W, tt, th, tw
 SIGNATURES = {
     "vsa_status_string": (ctypes.c_char_p, [_i]),
@@ -35,6 +35,8 @@ SIGNATURES = {
     "vsa_quantize_qk_e4m3": (_i, [_p] * 6 + _SHAPE + [_p]),
     "vsa_sparse_attn_fwd_e4m3": (_i, [_p] * 7 + _SHAPE + [_i, _p, _sz, _p]),
     "vsa_sparse_linear_attn_fwd_e4m3": (_i, [_p] * 10 + _SHAPE + [_i, _p, _sz, _p]),
+    "vsa_packed_attn_workspace_bytes": (_sz, [_i] * 6),
+    "vsa_packed_attn_fwd": (_i, [_p, _ll] * 3 + [_p, _p] + [_p, _ll] + [_p, _p] + [_i] * 7 + [_p, _sz, _p]),
     "vsa_device_status": (_i, [_p, _p]),
     "vsa_select_blocks_noalloc": (_i, [_p, _p] + _SHAPE + [_i, _p, _p]),
     "vsa_selftest_wait_timeout": (_i, [_p, _sz, ctypes.c_uint, _p]),

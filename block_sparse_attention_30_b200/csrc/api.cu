@@ -12,6 +12,7 @@
 #include "common.cuh"
 #include "fine_attn.h"
 #include "linear.h"
+#include "packed.h"
 #include "quant.h"
 #include "select.h"
 #include "tiles.h"
@@ -22,6 +23,8 @@ namespace {
 constexpr size_t kStatusBytes = 256;     // status block at the start of the workspace
 
 bool aligned16(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+bool aligned4(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 vsa_status check_shape(int B, int heads, int d, int T, int H, int W, int tt, int th, int tw) {
     switch (vsa::shape_error(B, heads, d, T, H, W, tt, th, tw)) {
@@ -89,6 +92,29 @@ bool encode_grid_map_u8(CUtensorMap* m, const void* base, const vsa::Grid& g) {
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, const_cast<void*>(base), dims, strides, box, es,
               CU_TENSOR_MAP_INTERLEAVE_NONE, g.d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// A packed [rows][heads][d] operand: rows at least heads*d elements apart, in
+// steps of 16 bytes (TMA), below the tensor map's 2^40-byte limit.  A tensor
+// without rows needs no address.
+bool packed_ok(const void* p, long long stride, int rows, int heads, int d) {
+    if (rows == 0) return true;
+    return aligned16(p) && stride >= (long long)heads * d && stride % 8 == 0 && stride < (1ll << 38);
+}
+
+vsa::PackedTensor packed(const void* p, long long stride, int rows, int heads, int d) {
+    // the stride of a single row is not used; give the maps a valid one
+    return {const_cast<void*>(p), rows > 1 ? stride : (long long)heads * d};
+}
+
+vsa_status check_packed(int total_q, int total_k, int n_seq, int heads_q, int heads_kv, int d) {
+    if (total_q < 0 || total_k < 0 || n_seq < 1 || heads_q < 1 || heads_kv < 1 || d < 1) return VSA_ERR_INVALID_ARGUMENT;
+    if (heads_q % heads_kv) return VSA_ERR_INVALID_ARGUMENT;
+    if (d != 64 && d != 128) return VSA_ERR_UNSUPPORTED;
+    if (heads_q / heads_kv > 128) return VSA_ERR_UNSUPPORTED;
+    if (total_q >= (1 << 30) || total_k >= (1 << 30) || n_seq >= (1 << 24) || heads_q >= (1 << 16)) return VSA_ERR_UNSUPPORTED;
+    if (vsa::packed_work_items({n_seq, total_q, total_k, heads_q, heads_kv, d}) > 0x7fffffffll) return VSA_ERR_UNSUPPORTED;
+    return VSA_OK;
 }
 
 vsa_status from_cuda(cudaError_t e) { return e == cudaSuccess ? VSA_OK : VSA_ERR_CUDA; }
@@ -420,6 +446,46 @@ vsa_status vsa_sparse_linear_attn_fwd_e4m3(const uint8_t* q8, const uint8_t* k8,
                                             (cudaStream_t)stream);
     if (e != cudaSuccess) return from_cuda(e);
     return from_cuda(vsa::launch_fine(a, (cudaStream_t)stream));
+}
+
+size_t vsa_packed_attn_workspace_bytes(int total_q, int total_k, int n_seq, int heads_q, int heads_kv,
+                                       int head_dim) {
+    if (check_packed(total_q, total_k, n_seq, heads_q, heads_kv, head_dim) != VSA_OK) return 0;
+    const vsa::PackedShape sh{n_seq, total_q, total_k, heads_q, heads_kv, head_dim};
+    const size_t f = vsa::packed_fwd_scratch_bytes(sh), b = vsa::packed_bwd_scratch_bytes(sh);
+    return kStatusBytes + (f > b ? f : b);
+}
+
+vsa_status vsa_packed_attn_fwd(const vsa_bf16* q, long long q_stride, const vsa_bf16* k, long long k_stride,
+                               const vsa_bf16* v, long long v_stride, const int32_t* cu_q, const int32_t* cu_k,
+                               vsa_bf16* out, long long out_stride, float* out_f32, float* lse, int total_q,
+                               int total_k, int n_seq, int heads_q, int heads_kv, int head_dim, int causal,
+                               void* workspace, size_t workspace_bytes, vsa_stream_t stream) {
+    vsa_status s = check_packed(total_q, total_k, n_seq, heads_q, heads_kv, head_dim);
+    if (s != VSA_OK) return s;
+    if (!packed_ok(q, q_stride, total_q, heads_q, head_dim) || !packed_ok(k, k_stride, total_k, heads_kv, head_dim) ||
+        !packed_ok(v, v_stride, total_k, heads_kv, head_dim) || !packed_ok(out, out_stride, total_q, heads_q, head_dim))
+        return VSA_ERR_INVALID_ARGUMENT;
+    if (!aligned4(cu_q) || !aligned4(cu_k)) return VSA_ERR_INVALID_ARGUMENT;
+    if ((out_f32 && !aligned16(out_f32)) || (lse && !aligned16(lse))) return VSA_ERR_INVALID_ARGUMENT;
+    if (!aligned16(workspace)) return VSA_ERR_WORKSPACE;
+    vsa::PackedArgs a{};
+    a.s = {n_seq, total_q, total_k, heads_q, heads_kv, head_dim};
+    if (workspace_bytes < kStatusBytes + vsa::packed_fwd_scratch_bytes(a.s)) return VSA_ERR_WORKSPACE;
+    if (total_q == 0) return VSA_OK;
+    a.q = packed(q, q_stride, total_q, heads_q, head_dim);
+    a.k = packed(k, k_stride, total_k, heads_kv, head_dim);
+    a.v = packed(v, v_stride, total_k, heads_kv, head_dim);
+    a.out = packed(out, out_stride, total_q, heads_q, head_dim);
+    a.cu_q = cu_q;
+    a.cu_k = cu_k;
+    a.out32 = out_f32;
+    a.lse = lse;
+    a.causal = causal != 0;
+    a.scratch = static_cast<uint8_t*>(workspace) + kStatusBytes;
+    a.status = static_cast<int*>(workspace);
+    if (!(a.enc = encode_fn())) return VSA_ERR_CUDA;
+    return from_cuda(vsa::launch_packed_fwd(a, (cudaStream_t)stream));
 }
 
 vsa_status vsa_device_status(void* workspace, vsa_stream_t stream) {

@@ -1,0 +1,71 @@
+// packed.h -- internal launch interface of the operators over packed
+// sequences: causal softmax attention with grouped heads (packed_attn.cu,
+// packed_bwd.cu) and linear attention with a decay per head (decay_attn.cu,
+// decay_step.cu).
+#pragma once
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+#include <cstdint>
+
+namespace vsa {
+
+// One bf16 tensor [rows][heads][d]: heads and features contiguous, rows
+// `stride` elements apart.
+struct PackedTensor {
+    void* p;
+    long long stride;
+};
+
+struct PackedShape {
+    int n_seq, total_q, total_k, heads_q, heads_kv, d;
+    int group() const { return heads_q / heads_kv; }
+};
+
+struct PackedArgs {
+    PackedShape s;
+    PackedTensor q, k, v, out, dout, dq, dk, dv;
+    const int32_t* cu_q;         // [n_seq + 1]
+    const int32_t* cu_k;
+    float* out32;                // [total_q][heads_q][d] or null
+    float* lse;                  // [heads_q][total_q] or null
+    int causal;
+    uint8_t* scratch;            // behind the workspace's status block
+    int* status;
+    PFN_cuTensorMapEncodeTiled_v12000 enc;
+};
+
+// 3-D map {d, heads, rows} of a packed tensor; box {64, box_heads, box_rows},
+// 128-byte swizzle; rows past the end read as zeros.
+bool encode_packed_map(CUtensorMap* m, const PackedTensor& t, int rows, int heads, int d, int box_heads,
+                       int box_rows, PFN_cuTensorMapEncodeTiled_v12000 enc);
+
+long long packed_work_items(const PackedShape& s);   // CTAs of one share, at most 2^31 - 1
+int packed_splits(const PackedShape& s);
+size_t packed_fwd_scratch_bytes(const PackedShape& s);
+size_t packed_bwd_scratch_bytes(const PackedShape& s);
+cudaError_t launch_packed_fwd(const PackedArgs& a, cudaStream_t stream);
+cudaError_t launch_packed_bwd(const PackedArgs& a, cudaStream_t stream);
+
+struct DecayArgs {
+    int n_seq, total, heads, d;
+    PackedTensor q, k, v, out, dout, dq, dk, dv;
+    const float* log_decay;      // [heads]
+    const int32_t* cu;           // [n_seq + 1]
+    const float* state_in;       // [n_seq][heads][d][d] or null
+    float* state_out;            // or null
+    const float* dstate_out;     // or null
+    float* dstate_in;            // or null
+    float scale;
+    uint8_t* scratch;
+    int* status;
+    PFN_cuTensorMapEncodeTiled_v12000 enc;
+};
+
+size_t decay_scratch_bytes(int n_seq, int total, int heads, int d);
+cudaError_t launch_decay_fwd(const DecayArgs& a, cudaStream_t stream);
+cudaError_t launch_decay_bwd(const DecayArgs& a, cudaStream_t stream);
+cudaError_t launch_decay_step(const DecayArgs& a, int batch, const float* state, float* state_out,
+                              cudaStream_t stream);
+
+}  // namespace vsa

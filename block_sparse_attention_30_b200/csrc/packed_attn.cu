@@ -1,0 +1,508 @@
+// packed_attn.cu -- causal softmax attention over packed sequences with
+// grouped heads on sm_100a (no counterpart on the pages, whose attention is
+// bidirectional over one grid; this is the dense, causal form that a model
+// generating clip after clip, or conditioned on prompts of different lengths,
+// needs next to the block-sparse pass).
+//
+// Per query token i of a sequence with nq queries and nk keys, and query head
+// h of the group that shares kv head h / G:
+//     O_i = sum_j p_ij v_j,   p_ij = softmax over j <= i + nk - nq of
+//     q_i.k_j / sqrt(d)      (j < nk without the causal mask);
+// a row that sees no key gives O = 0 and lse = -inf.
+//
+// One CTA owns two tiles of 128 rows of one kv head; a row is a (token, head
+// of the group) pair, token-major, so the group's heads share every K and V
+// tile that is loaded, and a single new token fills G rows of a tile instead
+// of one.  Per block of 128 keys:
+//   * warp 8 (one lane) brings Q once and the K and V blocks through one ring
+//     of TMA stages, last block first (the masked ones come first, the rest
+//     of the walk needs no mask);
+//   * warp 9 (one lane) issues S = Q K^T (M = 128, N = 128) for each tile
+//     into TMEM and, once the softmax has written P as bf16 over S,
+//     O += P V (A = P from TMEM): the tensor cores work on one tile while the
+//     other is in its softmax;
+//   * warps 0-3 and 4-7 (one tile each, one row per thread) do the online
+//     softmax in the exp2 domain with fp32 statistics; O is rescaled in TMEM
+//     only when a row maximum grows by more than 2^8 (P stays below 256, far
+//     from overflow).  P is rounded to bf16 for the tensor cores (2^-8
+//     relative at most per weight, as much as the rounding of the output); the row
+//     sum adds the fp32 weights, so lse is good to fp32.
+// The rows of a K/V tile behind the sequence's last key belong to another
+// sequence.  Scores there are masked by selection, whatever they are; V rows
+// there are overwritten with zeros before P V (0 x NaN would not be 0).
+#include <algorithm>
+#include <cmath>
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math_constants.h>
+
+#include "common.cuh"
+#include "packed.cuh"
+#include "packed.h"
+#include "sm100.cuh"
+#include "softmax_step.cuh"
+
+namespace vsa {
+using namespace sm100;
+
+template <int D>
+struct PackCfg {
+    static constexpr int NCH = D / 64;                   // 64-feature chunks
+    static constexpr int CHUNK = 128 * 128;              // 128 rows of one chunk (bf16)
+    static constexpr int TILE = NCH * CHUNK;             // 128 rows of one tensor
+    static constexpr int NST = D == 128 ? 5 : 10;        // K/V ring stages
+    static constexpr int BAR_OFF = (2 + NST) * TILE;
+    static constexpr int SMEM = BAR_OFF + 512;
+    static constexpr int THREADS = 384;                  // 3 warpgroups, 168 registers a thread at launch
+    static constexpr int REG_LOAD = 72, REG_SOFT = 216;  // 128 * 72 + 256 * 216 = 384 * 168
+    static constexpr int TMEM_COLS = 512;
+    static constexpr int S_COL = 0;                      // S / P of tile w at 128 w
+    static constexpr int O_COL = 256;                    // O of tile w at 256 + D w
+};
+static_assert(PackCfg<128>::SMEM <= 232448 && PackCfg<64>::SMEM <= 232448, "shared memory");
+
+template <int D>
+struct PackBars {
+    uint64_t q_full[2];
+    uint64_t full[PackCfg<D>::NST], empty[PackCfg<D>::NST];
+    uint64_t s_full[2], p_full[2], o_full[2];
+    uint64_t mma_done;                   // every MMA of the CTA finished
+    uint32_t tmem_base;
+    int abort;
+};
+static_assert(sizeof(PackBars<64>) <= 512, "barrier block");
+
+// What one CTA works on: rows of the tile pair and its key blocks.
+struct PackWork {
+    int seq;             // -1: nothing
+    int q0, nq;          // the sequence's first query row and query count
+    int k0, nk;
+    int tok[2];          // first token (within the sequence) of each tile
+    int nb[2];           // key blocks each tile needs (0: none visible)
+    int lo, hi;          // this CTA's share of the blocks [lo, hi)
+};
+
+// Keys that query token i of the sequence sees.
+__device__ __forceinline__ int seen_keys(int i, int nq, int nk, int causal) {
+    return causal ? max(0, min(nk, i + 1 + nk - nq)) : nk;
+}
+
+__device__ __forceinline__ PackWork pack_work(const int32_t* __restrict__ cu_q, const int32_t* __restrict__ cu_k,
+                                              const PackedShape& s, int tok_per_tile, int tiles, int t, int causal,
+                                              int n_splits, int split, int* status) {
+    PackWork w;
+    const SeqTile at = find_tile(cu_q, s.n_seq, s.total_q, 2 * tok_per_tile, tiles - 1 - t, status);
+    w.seq = at.seq;
+    if (at.seq < 0) return w;
+    const SeqRange q = seq_range(cu_q, at.seq, s.total_q, status), k = seq_range(cu_k, at.seq, s.total_k, status);
+    w.q0 = q.begin; w.nq = q.len; w.k0 = k.begin; w.nk = k.len;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        w.tok[x] = (2 * at.tile + x) * tok_per_tile;
+        // the tile's last token sees the most keys
+        const int last = min(w.tok[x] + tok_per_tile, w.nq) - 1;
+        w.nb[x] = w.tok[x] < w.nq ? (seen_keys(last, w.nq, w.nk, causal) + 127) / 128 : 0;
+    }
+    const int nb = max(w.nb[0], w.nb[1]);
+    const int per = (nb + n_splits - 1) / n_splits;
+    w.lo = min(nb, split * per);
+    w.hi = min(nb, w.lo + per);
+    return w;
+}
+
+template <int D>
+__global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
+packed_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                  const __grid_constant__ CUtensorMap mv, const PackedShape sh, const int tok_per_tile,
+                  const int tiles, const int32_t* __restrict__ cu_q, const int32_t* __restrict__ cu_k,
+                  const int causal, const float scale_log2, __nv_bfloat16* __restrict__ out,
+                  const long long out_stride, float* __restrict__ out32, float* __restrict__ lse,
+                  const int n_splits, float* __restrict__ part_o, float* __restrict__ part_lse, int* status) {
+    using C = PackCfg<D>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    if (smem_u32(smem) & 1023) {
+        if (threadIdx.x == 0) report(status, kStatusMisaligned);
+        return;
+    }
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int group = sh.heads_q / sh.heads_kv;
+    const int kvh = blockIdx.x % sh.heads_kv;
+    const int split = blockIdx.y;
+    const PackWork w = pack_work(cu_q, cu_k, sh, tok_per_tile, tiles, blockIdx.x / sh.heads_kv, causal, n_splits, split,
+                                 status);
+    if (w.seq < 0) return;                               // uniform over the CTA
+    uint8_t* sQ = smem;
+    uint8_t* ring = smem + 2 * C::TILE;
+    PackBars<D>* bars = reinterpret_cast<PackBars<D>*>(smem + C::BAR_OFF);
+    volatile int* abort_flag = &bars->abort;
+    if (tid == 0) {
+        bars->abort = 0;
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(&bars->q_full[x], 1);
+            mbar_init(&bars->s_full[x], 1);
+            mbar_init(&bars->p_full[x], 128);
+            mbar_init(&bars->o_full[x], 1);
+        }
+        for (int x = 0; x < C::NST; ++x) { mbar_init(&bars->full[x], 1); mbar_init(&bars->empty[x], 1); }
+        mbar_init(&bars->mma_done, 1);
+        fence_barrier_init();
+    }
+    if (warp == 9) { tmem_alloc(&bars->tmem_base, C::TMEM_COLS); tmem_relinquish(); }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tbase = bars->tmem_base;
+    auto fail = [&]() { *abort_flag = 1; report(status, kStatusTimeout); };
+    const int n = w.hi - w.lo;                           // blocks hi - 1 down to lo: step t is block hi - 1 - t
+    // tile x takes part from step first[x] on
+    const int first[2] = {max(0, w.hi - w.nb[0]), max(0, w.hi - w.nb[1])};
+
+    if (warp >= 8) {
+      reg_dec<C::REG_LOAD>();
+      if (warp == 8) {
+        if (lane == 0) {
+            // ------------------------------------------------------ loads
+            // ring item 2 t is K of step t, item 2 t + 1 its V
+            bool q_issued[2] = {false, false};
+            for (int x = 0; x < 2 && n > 0; ++x) {
+                if (w.tok[x] >= w.nq) continue;
+                mbar_arrive_expect_tx(&bars->q_full[x], C::NCH * tok_per_tile * group * 128);
+                for (int c = 0; c < C::NCH; ++c)
+                    tma_load_3d(sQ + x * C::TILE + c * C::CHUNK, &mq, &bars->q_full[x], 64 * c, kvh * group,
+                                w.q0 + w.tok[x]);
+                q_issued[x] = true;
+            }
+            int issued = 0;
+            for (int i = 0; i < 2 * n; ++i) {
+                const int st = i % C::NST;
+                if (i >= C::NST && !mbar_wait(&bars->empty[st], ((i / C::NST) - 1) & 1, abort_flag)) { fail(); break; }
+                const int row = w.k0 + 128 * (w.hi - 1 - (i >> 1));
+                const CUtensorMap* map = (i & 1) ? &mv : &mk;
+                mbar_arrive_expect_tx(&bars->full[st], C::TILE);
+                for (int c = 0; c < C::NCH; ++c)
+                    tma_load_3d(ring + st * C::TILE + c * C::CHUNK, map, &bars->full[st], 64 * c, kvh, row);
+                ++issued;
+            }
+            if (*abort_flag) {
+                // drain: every load must land before the CTA's shared memory is given up
+                for (int x = 0; x < 2; ++x) if (q_issued[x]) wait_noabort(&bars->q_full[x], 0);
+                for (int i = max(0, issued - C::NST); i < issued; ++i)
+                    wait_noabort(&bars->full[i % C::NST], (i / C::NST) & 1);
+            }
+        }
+      } else if (warp == 9) {
+        if (lane == 0 && n > 0) {
+            // ------------------------------------------------------- MMAs
+            const uint32_t id_s = idesc_bf16_f32(128, 128, false, false);
+            const uint32_t id_o = idesc_bf16_f32(128, D, false, true);
+            const uint32_t q_addr = smem_u32(sQ), r_addr = smem_u32(ring);
+            auto item = [&](int i) { return mma_wait(&bars->full[i % C::NST], (i / C::NST) & 1, abort_flag); };
+            auto issue_s = [&](int x, int t) {
+                const uint32_t a0 = q_addr + x * C::TILE, b0 = r_addr + ((2 * t) % C::NST) * C::TILE;
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t o = (kk >> 2) * C::CHUNK + (kk & 3) * 32;
+                    mma_bf16_ss(tbase + C::S_COL + 128 * x, smem_desc_sw128(a0 + o, 16, 1024),
+                                smem_desc_sw128(b0 + o, 16, 1024), id_s, kk > 0);
+                }
+                mma_commit(&bars->s_full[x]);
+            };
+            auto issue_o = [&](int x, int t) {
+                const uint32_t b0 = r_addr + ((2 * t + 1) % C::NST) * C::TILE;
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)               // 16 keys per MMA
+                    mma_bf16_ts(tbase + C::O_COL + D * x, tbase + C::S_COL + 128 * x + kk * 8,
+                                smem_desc_sw128(b0 + kk * 2048, C::CHUNK, 1024), id_o, t > first[x] || kk > 0);
+            };
+            bool ok = true;
+            for (int x = 0; x < 2 && ok; ++x)
+                if (first[x] < n) ok = mma_wait(&bars->q_full[x], 0, abort_flag);
+            // step t: P V of step t, then S of step t + 1 over the same columns
+            // (MMAs of one thread run in issue order); step -1 has only the S
+            for (int t = -1; t < n && ok; ++t) {
+                bool have_k = false, have_v = false;
+                for (int x = 0; x < 2 && ok; ++x) {
+                    if (t >= first[x] && t >= 0) {
+                        if (!have_v) { ok = item(2 * t + 1); have_v = true; }
+                        if (!ok || !(ok = mma_wait(&bars->p_full[x], (t - first[x]) & 1, abort_flag))) break;
+                        tc_fence_after();
+                        issue_o(x, t);
+                        if (t == n - 1) mma_commit(&bars->o_full[x]);
+                    }
+                    if (t + 1 >= first[x] && t + 1 < n) {
+                        if (!have_k) { ok = item(2 * t + 2); have_k = true; }
+                        if (!ok) break;
+                        tc_fence_after();
+                        issue_s(x, t + 1);
+                    }
+                }
+                if (!ok) break;
+                if (t >= 0) mma_commit(&bars->empty[(2 * t + 1) % C::NST]);
+                if (t + 1 < n) mma_commit(&bars->empty[(2 * t + 2) % C::NST]);
+            }
+            if (!ok) fail();
+            mma_commit(&bars->mma_done);
+            wait_noabort(&bars->mma_done, 0);
+        }
+      }
+    } else {
+        reg_inc<C::REG_SOFT>();
+        // ------------------------------------------------------- softmax
+        const int x = warp >> 2;                         // tile
+        const int r = tid & 127;                         // row of the tile
+        const int tok = w.tok[x] + r / group;            // token within the sequence
+        const bool valid = r < tok_per_tile * group && tok < w.nq;
+        const int head = kvh * group + r % group;
+        const int lim = valid ? seen_keys(tok, w.nq, w.nk, causal) : 0;
+        const int lim_min = seen_keys(w.tok[x], w.nq, w.nk, causal);   // of the tile's first token: the smallest
+        const uint32_t lane_base = tbase + ((uint32_t)(32 * (warp & 3)) << 16);
+        const uint32_t tS = lane_base + C::S_COL + 128 * x, tO = lane_base + C::O_COL + D * x;
+        float m_run = -CUDART_INF_F, l_run = 0.f;
+        bool ok = true;
+        const int f = first[x];
+        for (int t = f; t < n; ++t) {
+            const int key0 = 128 * (w.hi - 1 - t);
+            if (key0 + 128 > w.nk) {
+                // the sequence's last, partial block (step 0): zero V's rows behind it
+                if (!__all_sync(0xffffffffu, mbar_wait(&bars->full[(2 * t + 1) % C::NST], ((2 * t + 1) / C::NST) & 1, abort_flag))) { ok = false; break; }
+                uint8_t* v = ring + ((2 * t + 1) % C::NST) * C::TILE;
+                const int z0 = w.nk - key0;
+                for (int u = r; u < (128 - z0) * 8 * C::NCH; u += 128)
+                    *reinterpret_cast<uint4*>(v + (u % C::NCH) * C::CHUNK + z0 * 128 + (u / C::NCH) * 16) = make_uint4(0, 0, 0, 0);
+                fence_proxy_async_smem();
+            }
+            if (!__all_sync(0xffffffffu, mbar_wait(&bars->s_full[x], (t - f) & 1, abort_flag))) { ok = false; break; }
+            tc_fence_after();
+            float s[128];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(tS + 32 * c, *reinterpret_cast<float(*)[32]>(&s[32 * c]));
+            tmem_wait_ld();
+            if (key0 + 128 > lim_min) {                  // uniform over the tile
+                const int seen = lim - key0;
+#pragma unroll
+                for (int e = 0; e < 128; ++e)
+                    if (e >= seen) s[e] = -CUDART_INF_F;
+            }
+            float m0 = s[0], m1 = s[1], m2 = s[2], m3 = s[3];
+#pragma unroll
+            for (int e = 4; e < 124; e += 8) {
+                m0 = max3f(m0, s[e], s[e + 1]);
+                m1 = max3f(m1, s[e + 2], s[e + 3]);
+                m2 = max3f(m2, s[e + 4], s[e + 5]);
+                m3 = max3f(m3, s[e + 6], s[e + 7]);
+            }
+            m0 = max3f(m0, s[124], s[125]);
+            m1 = max3f(m1, s[126], s[127]);
+            const float mx = fmaxf(max3f(m0, m1, m2), m3) * scale_log2;
+            const bool raise = mx > m_run + 8.f;
+            const float alpha = raise ? ex2(m_run - mx) : 1.f;   // 0 from -inf
+            if (raise) m_run = mx;
+            l_run *= alpha;
+            // P V of the step before is finished (s_full was committed behind
+            // it), so O can be rescaled here; step f has no O yet
+            if (t > f && __any_sync(0xffffffffu, raise)) {
+#pragma unroll
+                for (int c = 0; c < D; c += 32) {
+                    float o[32];
+                    tmem_ld_32x32b_x32(tO + c, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] *= alpha;
+                    tmem_st_32x32b_x32f(tO + c, o);
+                }
+            }
+            const float m_sub = m_run == -CUDART_INF_F ? 0.f : m_run;
+            const uint64_t sc2 = f32x2(scale_log2, scale_log2), nm2 = f32x2(-m_sub, -m_sub);
+            uint64_t acc0 = 0, acc1 = 0;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t pk[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    float t0, t1;
+                    unf32x2(fma_f32x2(f32x2(s[32 * c + 2 * e], s[32 * c + 2 * e + 1]), sc2, nm2), t0, t1);
+                    const float p0 = ex2(t0), p1 = ex2(t1);
+                    pk[e] = pack_bf16x2(p0, p1);
+                    if (e & 1) acc1 = add_f32x2(acc1, f32x2(p0, p1));
+                    else acc0 = add_f32x2(acc0, f32x2(p0, p1));
+                }
+                tmem_st_32x32b_x16(tS + 16 * c, pk);
+            }
+            float a0, a1, b0, b1;
+            unf32x2(acc0, a0, a1);
+            unf32x2(acc1, b0, b1);
+            l_run += (a0 + a1) + (b0 + b1);
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(&bars->p_full[x]);
+        }
+        if (ok && f < n && !__all_sync(0xffffffffu, mbar_wait(&bars->o_full[x], 0, abort_flag))) ok = false;
+        if (!ok) fail();
+        if (ok) {
+            tc_fence_after();
+            const bool none = l_run == 0.f;               // the row saw no key (of this share)
+            const float inv = none ? 0.f : 1.f / l_run;
+            const float row_lse = none ? -CUDART_INF_F : m_run + log2f(l_run);
+            const long long row = (long long)w.q0 + tok;
+            if (n_splits > 1) {
+                // partial result of this share, joined by combine_kernel
+                if (valid) part_lse[((long long)split * sh.heads_q + head) * sh.total_q + row] = row_lse;
+                float* po = part_o + (((long long)split * sh.total_q + row) * sh.heads_q + head) * D;
+#pragma unroll
+                for (int c = 0; c < D; c += 32) {
+                    float o[32];
+                    if (f < n) { tmem_ld_32x32b_x32(tO + c, o); tmem_wait_ld(); }
+                    if (valid && !none) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            *reinterpret_cast<float4*>(po + c + e) = make_float4(o[e] * inv, o[e + 1] * inv, o[e + 2] * inv, o[e + 3] * inv);
+                    }
+                }
+            } else {
+                if (valid && lse) lse[(long long)head * sh.total_q + row] = row_lse;
+#pragma unroll
+                for (int c = 0; c < D; c += 32) {
+                    float o[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = 0.f;
+                    if (f < n) { tmem_ld_32x32b_x32(tO + c, o); tmem_wait_ld(); }
+                    if (valid) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = none ? 0.f : o[e] * inv;
+                        __nv_bfloat16* po = out + row * out_stride + (long long)head * D + c;
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8)
+                            *reinterpret_cast<uint4*>(po + e) = make_uint4(pack_bf16x2(o[e], o[e + 1]), pack_bf16x2(o[e + 2], o[e + 3]),
+                                                                           pack_bf16x2(o[e + 4], o[e + 5]), pack_bf16x2(o[e + 6], o[e + 7]));
+                        if (out32) {
+                            float* p32 = out32 + (row * sh.heads_q + head) * D + c;
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4)
+                                *reinterpret_cast<float4*>(p32 + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                        }
+                    }
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 9) tmem_dealloc(tbase, C::TMEM_COLS);
+}
+
+// Joins the shares of a split key axis: out = sum_s 2^(lse_s - m) O_s / sum_s 2^(lse_s - m), m the largest lse_s.
+// One CTA per tile pair and kv head as in the kernel before it, D / 4 threads per row.
+template <int D>
+__global__ void __launch_bounds__(256)
+packed_combine_kernel(const PackedShape sh, const int tok_per_tile, const int tiles, const int32_t* __restrict__ cu_q,
+                      const int n_splits, const float* __restrict__ part_o, const float* __restrict__ part_lse,
+                      __nv_bfloat16* __restrict__ out, const long long out_stride, float* __restrict__ out32,
+                      float* __restrict__ lse, int* status) {
+    constexpr int TPR = D / 4;
+    const int group = sh.heads_q / sh.heads_kv;
+    const int kvh = blockIdx.x % sh.heads_kv;
+    const SeqTile at = find_tile(cu_q, sh.n_seq, sh.total_q, 2 * tok_per_tile, tiles - 1 - blockIdx.x / sh.heads_kv, status);
+    if (at.seq < 0) return;
+    const SeqRange q = seq_range(cu_q, at.seq, sh.total_q, status);
+    const int tok0 = at.tile * 2 * tok_per_tile;
+    const int rows = min(2 * tok_per_tile, q.len - tok0) * group;
+    const int f = threadIdx.x % TPR * 4;
+    for (int r = threadIdx.x / TPR + blockIdx.y * (256 / TPR); r < rows; r += 256 / TPR * gridDim.y) {
+        const long long row = (long long)q.begin + tok0 + r / group;
+        const int head = kvh * group + r % group;
+        float m = -CUDART_INF_F;
+        for (int s = 0; s < n_splits; ++s) m = fmaxf(m, __ldg(part_lse + ((long long)s * sh.heads_q + head) * sh.total_q + row));
+        float sum = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int s = 0; s < n_splits; ++s) {
+            const float l = __ldg(part_lse + ((long long)s * sh.heads_q + head) * sh.total_q + row);
+            if (l == -CUDART_INF_F) continue;            // the share saw no key: its O was not written
+            const float w = ex2(l - m);
+            const float4 p = __ldg(reinterpret_cast<const float4*>(part_o + (((long long)s * sh.total_q + row) * sh.heads_q + head) * D + f));
+            sum += w;
+            o.x = fmaf(w, p.x, o.x); o.y = fmaf(w, p.y, o.y); o.z = fmaf(w, p.z, o.z); o.w = fmaf(w, p.w, o.w);
+        }
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        o.x *= inv; o.y *= inv; o.z *= inv; o.w *= inv;
+        *reinterpret_cast<uint2*>(out + row * out_stride + (long long)head * D + f) = make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+        if (out32) *reinterpret_cast<float4*>(out32 + (row * sh.heads_q + head) * D + f) = o;
+        if (lse && f == 0) lse[(long long)head * sh.total_q + row] = sum == 0.f ? -CUDART_INF_F : m + log2f(sum);
+    }
+}
+
+bool encode_packed_map(CUtensorMap* m, const PackedTensor& t, int rows, int heads, int d, int box_heads,
+                       int box_rows, PFN_cuTensorMapEncodeTiled_v12000 enc) {
+    cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)rows};
+    cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)t.stride * 2};
+    cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
+    cuuint32_t es[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, t.p, dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Upper bound of the tile pairs of 2 x (128 / group) tokens that the
+// sequences are cut into (their lengths are device data).
+static long long pair_bound(const PackedShape& s) {
+    return (long long)s.total_q / (2 * (128 / s.group())) + s.n_seq;
+}
+
+long long packed_work_items(const PackedShape& s) { return pair_bound(s) * s.heads_kv; }
+
+// Shares the key axis is split into: 1 when the tile pairs fill the GPU.
+// The host knows the average key length only.
+int packed_splits(const PackedShape& s) {
+    const long long items = packed_work_items(s);
+    const long long blocks = ((long long)s.total_k / s.n_seq + 127) / 128;     // of an average sequence
+    if (items >= 2 * 148 || blocks < 4) return 1;
+    return (int)std::max<long long>(1, std::min<long long>({(4 * 148 + items - 1) / items, blocks / 2, 64}));
+}
+
+size_t packed_fwd_scratch_bytes(const PackedShape& s) {
+    const int n = packed_splits(s);
+    return n > 1 ? (size_t)n * s.total_q * s.heads_q * (s.d + 1) * sizeof(float) : 0;
+}
+
+template <int D>
+static cudaError_t launch_packed_fwd_impl(const PackedArgs& a, cudaStream_t stream) {
+    using C = PackCfg<D>;
+    // set on every call: a cache by device would need a lock to be re-entrant
+    cudaError_t e = cudaFuncSetAttribute(packed_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    const int group = a.s.group(), tok = 128 / group;
+    const long long tiles = pair_bound(a.s);
+    // without keys nothing is read from k and v: any valid address will do for their maps
+    const PackedTensor kk = a.s.total_k ? a.k : a.q, vv = a.s.total_k ? a.v : a.q;
+    CUtensorMap mq, mk, mv;
+    if (!encode_packed_map(&mq, a.q, a.s.total_q, a.s.heads_q, D, group, tok, a.enc) ||
+        !encode_packed_map(&mk, kk, std::max(1, a.s.total_k), a.s.heads_kv, D, 1, 128, a.enc) ||
+        !encode_packed_map(&mv, vv, std::max(1, a.s.total_k), a.s.heads_kv, D, 1, 128, a.enc))
+        return cudaErrorInvalidValue;
+    const int n = packed_splits(a.s);
+    float* part_o = reinterpret_cast<float*>(a.scratch);
+    float* part_lse = part_o + (size_t)n * a.s.total_q * a.s.heads_q * D;
+    const float scale_log2 = 1.4426950408889634f / sqrtf((float)D);
+    packed_fwd_kernel<D><<<dim3((unsigned)(tiles * a.s.heads_kv), n), C::THREADS, C::SMEM, stream>>>(
+        mq, mk, mv, a.s, tok, (int)tiles, a.cu_q, a.cu_k, a.causal, scale_log2,
+        static_cast<__nv_bfloat16*>(a.out.p), a.out.stride, a.out32, a.lse, n, part_o, part_lse, a.status);
+    if (n > 1) {
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+        const int rows = 2 * tok * group, per = 256 / (D / 4);
+        const int gy = std::min((rows + per - 1) / per, 8);
+        packed_combine_kernel<D><<<dim3((unsigned)(tiles * a.s.heads_kv), gy), 256, 0, stream>>>(
+            a.s, tok, (int)tiles, a.cu_q, n, part_o, part_lse, static_cast<__nv_bfloat16*>(a.out.p), a.out.stride,
+            a.out32, a.lse, a.status);
+    }
+    return cudaGetLastError();
+}
+
+cudaError_t launch_packed_fwd(const PackedArgs& a, cudaStream_t stream) {
+    return a.s.d == 128 ? launch_packed_fwd_impl<128>(a, stream) : launch_packed_fwd_impl<64>(a, stream);
+}
+
+}  // namespace vsa
+namespace vsa { size_t packed_bwd_scratch_bytes(const PackedShape& s) { return 0; } }

@@ -115,6 +115,17 @@ __device__ __forceinline__ bool wait_noabort(uint64_t* bar, uint32_t parity) {
     return true;
 }
 
+// Move registers between the warpgroups of a CTA (every warp of a warpgroup
+// executes it; the shares must add up to no more than the launch's total).
+template <int N>
+__device__ __forceinline__ void reg_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void reg_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // Order this thread's generic-proxy shared-memory writes before later
 // async-proxy (tensor core / TMA) reads of the same bytes.
 __device__ __forceinline__ void fence_proxy_async_smem() {

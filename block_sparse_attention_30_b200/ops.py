@@ -161,6 +161,68 @@ def vsa_sparse_linear_attn_fwd_e4m3(q8, k8, q_scale, k_scale, q, v, block_idx, l
         _stream(stream)))
 
 
+# ------------------------------------------------------- packed sequences
+
+def new_workspace_bytes(nbytes, device="cuda", stream=None):
+    """Allocate (torch) and initialise a workspace of `nbytes` bytes."""
+    with torch.cuda.device(device):
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        _lib.check("vsa_workspace_init", _lib.lib().vsa_workspace_init(ws.data_ptr(), nbytes, _stream(stream)))
+    return ws
+
+
+def _rows(x, heads=None, d=None, total=None):
+    """A packed bf16 [total, heads, d] tensor -> (pointer, row stride)."""
+    assert x.dtype == torch.bfloat16 and x.is_cuda and x.dim() == 3, "expected a bf16 [total, heads, d] CUDA tensor"
+    t, h, n = x.shape
+    assert (heads is None or h == heads) and (d is None or n == d) and (total is None or t == total), tuple(x.shape)
+    assert t == 0 or ((n == 1 or x.stride(2) == 1) and (h == 1 or x.stride(1) == n)), \
+        "heads and features must be contiguous"
+    return x.data_ptr(), x.stride(0) if t > 1 else h * n
+
+
+def _borders(cu):
+    assert cu.dtype == torch.int32 and cu.is_cuda and cu.dim() == 1 and cu.is_contiguous() and cu.numel() >= 2, \
+        "expected int32 [n_seq + 1] sequence borders"
+    return cu.data_ptr(), cu.numel() - 1
+
+
+def _f32(x, shape):
+    if x is None:
+        return None
+    assert x.dtype == torch.float32 and x.is_cuda and x.is_contiguous() and tuple(x.shape) == tuple(shape), \
+        f"expected a contiguous fp32 tensor of shape {tuple(shape)}"
+    return x.data_ptr()
+
+
+def _same_device(*tensors):
+    dev = {x.device for x in tensors if x is not None}
+    assert len(dev) == 1, f"tensors on several devices: {sorted(map(str, dev))}"
+    return torch.cuda.device(dev.pop())
+
+
+def vsa_packed_attn_workspace_bytes(total_q, total_k, n_seq, heads_q, heads_kv, head_dim) -> int:
+    return _lib.lib().vsa_packed_attn_workspace_bytes(total_q, total_k, n_seq, heads_q, heads_kv, head_dim)
+
+
+def vsa_packed_attn_fwd(q, k, v, cu_q, cu_k, out, workspace, causal=True, out_f32=None, lse=None, stream=None):
+    """Softmax attention over packed sequences with grouped heads.
+
+    q, out: bf16 [total_q, heads_q, d]; k, v: bf16 [total_k, heads_kv, d] (rows
+    may be strided: slices of a fused projection); cu_q, cu_k: int32 borders.
+    Query i of a sequence sees keys up to i + nk - nq (causal) or all of them.
+    out_f32 [total_q, heads_q, d] and lse [heads_q, total_q] (fp32) are
+    written if given; the backward needs both."""
+    (tq, hq, d), (tk, hk) = q.shape, k.shape[:2]
+    n = _borders(cu_q)[1]
+    assert _borders(cu_k)[1] == n, "cu_q and cu_k describe different numbers of sequences"
+    with _same_device(q, k, v, cu_q, cu_k, out, workspace, out_f32, lse):
+        _lib.check("vsa_packed_attn_fwd", _lib.lib().vsa_packed_attn_fwd(
+            *_rows(q), *_rows(k, hk, d), *_rows(v, hk, d, tk), cu_q.data_ptr(), cu_k.data_ptr(), *_rows(out, hq, d, tq),
+            _f32(out_f32, (tq, hq, d)), _f32(lse, (hq, tq)), tq, tk, n, hq, hk, d, int(bool(causal)),
+            workspace.data_ptr(), workspace.numel(), _stream(stream)))
+
+
 def vsa_device_status(workspace, stream=None) -> int:
     """Synchronise and return the device status code (0 = VSA_OK)."""
     return _lib.lib().vsa_device_status(workspace.data_ptr(), _stream(stream))

@@ -270,6 +270,57 @@ vsa_status vsa_sparse_linear_attn_fwd_e4m3(const uint8_t* q8, const uint8_t* k8,
                                            int topk, void* workspace, size_t workspace_bytes,
                                            vsa_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Operators over packed sequences (no counterpart on the pages, whose
+ * attention is bidirectional over one grid): the dense causal softmax branch
+ * and a causal linear branch with a decay per head, for models that generate
+ * clip after clip or are conditioned on prompts of different lengths.
+ *
+ * Conventions on top of the ones above
+ *  - Tokens of all sequences lie one after another: a tensor is bf16
+ *    [total][heads][d], heads and features contiguous, rows `*_stride`
+ *    elements apart (>= heads*d, a multiple of 8; so slices of one fused
+ *    projection can be passed as they are).  head_dim 64 or 128.
+ *  - cu[n_seq + 1] (int32, device memory, 4-byte aligned) holds the borders:
+ *    sequence i has rows cu[i] .. cu[i+1] - 1; lengths of 0 are allowed.
+ *    Rows before cu[0] and from cu[n_seq] on belong to no sequence: they are
+ *    not read into any result, and outputs there are left as they were.
+ *    Borders that do not ascend within [0, total] are recorded as
+ *    VSA_ERR_DEVICE_CHECK, and a sequence between two such borders is taken
+ *    as empty.
+ *  - One sequence's values never reach another one's results, whatever they
+ *    are (NaN and Inf too).  Within a sequence the products run over tiles
+ *    of 128 tokens, so a NaN or Inf in k or v (in any tensor, for the
+ *    gradients) may also reach results that the mask hides it from.
+ *  - total below 2^30, n_seq below 2^24, heads below 2^16.  A tensor without
+ *    rows (total == 0) may be NULL.
+ * ------------------------------------------------------------------------- */
+
+/* Bytes of workspace vsa_packed_attn_fwd and vsa_packed_attn_bwd need for
+ * these shapes: the status block, then fp32 partial results where the key
+ * axis is split (few query tiles), or the backward's row terms.  0 for
+ * invalid shapes. */
+size_t vsa_packed_attn_workspace_bytes(int total_q, int total_k, int n_seq, int heads_q, int heads_kv,
+                                       int head_dim);
+
+/* Softmax attention over packed sequences with grouped heads: query head h
+ * reads kv head h / (heads_q / heads_kv).  For query token i of a sequence of
+ * nq queries (cu_q) and nk keys (cu_k),
+ *     out_i = sum_j p_ij v_j,  p_ij = softmax_j(q_i.k_j / sqrt(d))
+ * over j <= i + nk - nq (causal != 0; the last query sees every key) or all j
+ * (causal == 0); fp32 online softmax, bf16 tensor-core products.  A query
+ * that sees no key gives 0.  nq < nk is a continued prompt, nq == 1 a single
+ * new token over a cache of keys.
+ * out_f32 ([total_q][heads_q][d]) and lse ([heads_q][total_q], log2 of the
+ * normaliser of the scaled scores as in vsa_sparse_attn_fwd_train, -inf
+ * for a query that sees no key) may be NULL; the backward needs both.
+ * heads_q a multiple of heads_kv, at most 128 query heads per kv head. */
+vsa_status vsa_packed_attn_fwd(const vsa_bf16* q, long long q_stride, const vsa_bf16* k, long long k_stride,
+                               const vsa_bf16* v, long long v_stride, const int32_t* cu_q, const int32_t* cu_k,
+                               vsa_bf16* out, long long out_stride, float* out_f32, float* lse, int total_q,
+                               int total_k, int n_seq, int heads_q, int heads_kv, int head_dim, int causal,
+                               void* workspace, size_t workspace_bytes, vsa_stream_t stream);
+
 /* Self-test of the device failure path (no counterpart on the pages): a
  * one-warp kernel waits on a barrier nobody arrives at, gives up after
  * `limit_cycles` SM clock cycles exactly as the library's kernels do, and
