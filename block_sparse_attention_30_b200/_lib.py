@@ -37,6 +37,7 @@ SIGNATURES = {
     "vsa_sparse_linear_attn_fwd_e4m3": (_i, [_p] * 10 + _SHAPE + [_i, _p, _sz, _p]),
     "vsa_packed_attn_workspace_bytes": (_sz, [_i] * 6),
     "vsa_packed_attn_fwd": (_i, [_p, _ll] * 3 + [_p, _p] + [_p, _ll] + [_p, _p] + [_i] * 7 + [_p, _sz, _p]),
+    "vsa_packed_attn_bwd": (_i, [_p, _ll] * 3 + [_p] + [_p, _ll] + [_p] * 3 + [_p, _ll] * 3 + [_i] * 7 + [_p, _sz, _p]),
     "vsa_device_status": (_i, [_p, _p]),
     "vsa_select_blocks_noalloc": (_i, [_p, _p] + _SHAPE + [_i, _p, _p]),
     "vsa_selftest_wait_timeout": (_i, [_p, _sz, ctypes.c_uint, _p]),

@@ -113,7 +113,8 @@ vsa_status check_packed(int total_q, int total_k, int n_seq, int heads_q, int he
     if (d != 64 && d != 128) return VSA_ERR_UNSUPPORTED;
     if (heads_q / heads_kv > 128) return VSA_ERR_UNSUPPORTED;
     if (total_q >= (1 << 30) || total_k >= (1 << 30) || n_seq >= (1 << 24) || heads_q >= (1 << 16)) return VSA_ERR_UNSUPPORTED;
-    if (vsa::packed_work_items({n_seq, total_q, total_k, heads_q, heads_kv, d}) > 0x7fffffffll) return VSA_ERR_UNSUPPORTED;
+    const vsa::PackedShape sh{n_seq, total_q, total_k, heads_q, heads_kv, d};
+    if (vsa::packed_work_items(sh) > 0x7fffffffll || vsa::packed_bwd_work_items(sh) > 0x7fffffffll) return VSA_ERR_UNSUPPORTED;
     return VSA_OK;
 }
 
@@ -486,6 +487,47 @@ vsa_status vsa_packed_attn_fwd(const vsa_bf16* q, long long q_stride, const vsa_
     a.status = static_cast<int*>(workspace);
     if (!(a.enc = encode_fn())) return VSA_ERR_CUDA;
     return from_cuda(vsa::launch_packed_fwd(a, (cudaStream_t)stream));
+}
+
+vsa_status vsa_packed_attn_bwd(const vsa_bf16* q, long long q_stride, const vsa_bf16* k, long long k_stride,
+                               const vsa_bf16* v, long long v_stride, const float* out_f32, const vsa_bf16* dout,
+                               long long dout_stride, const int32_t* cu_q, const int32_t* cu_k, const float* lse,
+                               vsa_bf16* dq, long long dq_stride, vsa_bf16* dk, long long dk_stride, vsa_bf16* dv,
+                               long long dv_stride, int total_q, int total_k, int n_seq, int heads_q, int heads_kv,
+                               int head_dim, int causal, void* workspace, size_t workspace_bytes,
+                               vsa_stream_t stream) {
+    vsa_status s = check_packed(total_q, total_k, n_seq, heads_q, heads_kv, head_dim);
+    if (s != VSA_OK) return s;
+    if (!packed_ok(q, q_stride, total_q, heads_q, head_dim) || !packed_ok(k, k_stride, total_k, heads_kv, head_dim) ||
+        !packed_ok(v, v_stride, total_k, heads_kv, head_dim) ||
+        !packed_ok(dout, dout_stride, total_q, heads_q, head_dim) ||
+        !packed_ok(dq, dq_stride, total_q, heads_q, head_dim) ||
+        !packed_ok(dk, dk_stride, total_k, heads_kv, head_dim) ||
+        !packed_ok(dv, dv_stride, total_k, heads_kv, head_dim))
+        return VSA_ERR_INVALID_ARGUMENT;
+    if (!aligned4(cu_q) || !aligned4(cu_k)) return VSA_ERR_INVALID_ARGUMENT;
+    if (total_q > 0 && (!aligned16(out_f32) || !aligned16(lse))) return VSA_ERR_INVALID_ARGUMENT;
+    if (!aligned16(workspace)) return VSA_ERR_WORKSPACE;
+    vsa::PackedArgs a{};
+    a.s = {n_seq, total_q, total_k, heads_q, heads_kv, head_dim};
+    if (workspace_bytes < kStatusBytes + vsa::packed_bwd_scratch_bytes(a.s)) return VSA_ERR_WORKSPACE;
+    if (total_q == 0 && total_k == 0) return VSA_OK;
+    a.q = packed(q, q_stride, total_q, heads_q, head_dim);
+    a.k = packed(k, k_stride, total_k, heads_kv, head_dim);
+    a.v = packed(v, v_stride, total_k, heads_kv, head_dim);
+    a.dout = packed(dout, dout_stride, total_q, heads_q, head_dim);
+    a.dq = packed(dq, dq_stride, total_q, heads_q, head_dim);
+    a.dk = packed(dk, dk_stride, total_k, heads_kv, head_dim);
+    a.dv = packed(dv, dv_stride, total_k, heads_kv, head_dim);
+    a.cu_q = cu_q;
+    a.cu_k = cu_k;
+    a.out32 = const_cast<float*>(out_f32);
+    a.lse = const_cast<float*>(lse);
+    a.causal = causal != 0;
+    a.scratch = static_cast<uint8_t*>(workspace) + kStatusBytes;
+    a.status = static_cast<int*>(workspace);
+    if (!(a.enc = encode_fn())) return VSA_ERR_CUDA;
+    return from_cuda(vsa::launch_packed_bwd(a, (cudaStream_t)stream));
 }
 
 vsa_status vsa_device_status(void* workspace, vsa_stream_t stream) {

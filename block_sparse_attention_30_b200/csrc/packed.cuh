@@ -24,6 +24,11 @@ __device__ __forceinline__ SeqRange seq_range(const int32_t* __restrict__ cu, in
     return {a, b - a};
 }
 
+// Keys that query token i of the sequence sees.
+__device__ __forceinline__ int seen_keys(int i, int nq, int nk, int causal) {
+    return causal ? max(0, min(nk, i + 1 + nk - nq)) : nk;
+}
+
 struct SeqTile {
     int seq;     // -1: past the last tile
     int tile;    // tile within the sequence

@@ -41,6 +41,7 @@ bool encode_packed_map(CUtensorMap* m, const PackedTensor& t, int rows, int head
                        int box_rows, PFN_cuTensorMapEncodeTiled_v12000 enc);
 
 long long packed_work_items(const PackedShape& s);   // CTAs of one share, at most 2^31 - 1
+long long packed_bwd_work_items(const PackedShape& s);   // of the backward's largest launch
 int packed_splits(const PackedShape& s);
 size_t packed_fwd_scratch_bytes(const PackedShape& s);
 size_t packed_bwd_scratch_bytes(const PackedShape& s);

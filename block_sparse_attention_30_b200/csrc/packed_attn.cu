@@ -84,11 +84,6 @@ struct PackWork {
     int lo, hi;          // this CTA's share of the blocks [lo, hi)
 };
 
-// Keys that query token i of the sequence sees.
-__device__ __forceinline__ int seen_keys(int i, int nq, int nk, int causal) {
-    return causal ? max(0, min(nk, i + 1 + nk - nq)) : nk;
-}
-
 __device__ __forceinline__ PackWork pack_work(const int32_t* __restrict__ cu_q, const int32_t* __restrict__ cu_k,
                                               const PackedShape& s, int tok_per_tile, int tiles, int t, int causal,
                                               int n_splits, int split, int* status) {
@@ -505,4 +500,3 @@ cudaError_t launch_packed_fwd(const PackedArgs& a, cudaStream_t stream) {
 }
 
 }  // namespace vsa
-namespace vsa { size_t packed_bwd_scratch_bytes(const PackedShape& s) { return 0; } }

@@ -1,0 +1,629 @@
+// packed_bwd.cu -- gradients of the softmax attention over packed sequences
+// (packed_attn.cu) on sm_100a.
+//
+// With P_ij = 2^(q_i.k_j log2(e)/sqrt(d) - lse_i) recomputed from the
+// forward's lse, and the output gradient dO:
+//     dV_j = sum_i P_ij dO_i,      dP_ij = dO_i.v_j,   D_i = dO_i.O_i,
+//     dS_ij = P_ij (dP_ij - D_i),  dQ_i = sum_j dS_ij k_j / sqrt(d),
+//     dK_j = sum_i dS_ij q_i / sqrt(d),
+// the sums over i running over every query head of the group as well.
+//
+// Three launches, no atomics (the same call gives the same bits):
+//   row_terms_kernel  (lse, D) of every packed row, D from the forward's fp32
+//                  output (the bf16 one's rounding would enter dQ as
+//                  -dD sum_j P_j k_j, which does not shrink with dQ when the
+//                  keys share a large common component);
+//   dq_kernel      one CTA per 128 rows of one kv head ((token, head of the
+//                  group) pairs, as in the forward), walking its key blocks:
+//                  S = Q K^T, dP = dO V^T, dQ += dS K;
+//   dkdv_kernel    one CTA per 128 keys of one kv head, walking the blocks of
+//                  128 rows that see them: S^T = K Q^T, dP^T = V dO^T,
+//                  dV += P^T dO, dK += dS^T Q.  The rows of a block include
+//                  the group's heads, so the sum over shared heads is part of
+//                  the products.
+// 7 products instead of the 5 of a single kernel, which would have to add dQ
+// with atomics.  P and dS are rounded to bf16 for the products (2^-8 relative
+// at most per weight); everything else, sums included, is fp32.
+//
+// TMEM holds S twice (dQ) or once (dK/dV), dP once and the accumulators: 512
+// columns.  The tensor cores always have a product that does not wait for the
+// softmax of the current block: dQ alternates dP of block j+1, dQ of block j
+// and S of block j+2; dK/dV runs dV of block j and S^T of block j+1 while dS
+// is formed, and dK of block j and dP^T of block j+1 while the next weights
+// are.  Eight warps do the elementwise part, each row shared by two threads
+// (64 columns each).
+// Rows of a tile behind the sequence's end are masked by selection in the
+// scores and overwritten with zeros in shared memory before they enter a
+// product as its inner dimension (0 x NaN would not be 0).
+#include <algorithm>
+#include <cmath>
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math_constants.h>
+
+#include "common.cuh"
+#include "packed.cuh"
+#include "packed.h"
+#include "sm100.cuh"
+
+namespace vsa {
+using namespace sm100;
+
+// ------------------------------------------------------------------ row terms
+// terms[kv head][token][head of the group] = (lse, D), lse = +inf where the
+// row saw no key (its weights are then 2^-inf = 0).  D/8 threads per row.
+template <int D>
+__global__ void __launch_bounds__(256)
+row_terms_kernel(const float* __restrict__ o, const __nv_bfloat16* __restrict__ dout, const long long dout_stride,
+                 const float* __restrict__ lse, const int total, const int heads, const int group,
+                 float2* __restrict__ terms) {
+    constexpr int TPR = D / 8;
+    const long long id = (long long)blockIdx.x * (256 / TPR) + threadIdx.x / TPR;
+    const int f = threadIdx.x % TPR * 8;
+    const bool in = id < (long long)total * heads;
+    const long long tok = in ? id / heads : 0;
+    const int h = in ? (int)(id % heads) : 0;
+    float acc = 0.f;
+    if (in) {
+        const float4 a = __ldg(reinterpret_cast<const float4*>(o + (tok * heads + h) * D + f));
+        const float4 b = __ldg(reinterpret_cast<const float4*>(o + (tok * heads + h) * D + f + 4));
+        const uint4 g = __ldg(reinterpret_cast<const uint4*>(dout + tok * dout_stride + (long long)h * D + f));
+        const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        const uint32_t y[4] = {g.x, g.y, g.z, g.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            acc = fmaf(x[2 * e], __uint_as_float(y[e] << 16), acc);
+            acc = fmaf(x[2 * e + 1], __uint_as_float(y[e] & 0xffff0000u), acc);
+        }
+    }
+#pragma unroll
+    for (int m = TPR / 2; m > 0; m >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, m);
+    if (in && f == 0) {
+        const float l = __ldg(lse + (long long)h * total + tok);
+        terms[((long long)(h / group) * total + tok) * group + h % group] = make_float2(l == -CUDART_INF_F ? CUDART_INF_F : l, acc);
+    }
+}
+
+template <int D>
+struct PackBwdCfg {
+    static constexpr int NCH = D / 64;
+    static constexpr int CHUNK = 128 * 128;
+    static constexpr int TILE = NCH * CHUNK;
+    static constexpr int BAR_OFF = 7 * TILE;             // (dK/dV uses 6 tiles; its row terms lie in the 7th)
+    static constexpr int SMEM = BAR_OFF + 512;
+    static constexpr int THREADS = 320;                  // 8 elementwise warps, loads, MMAs
+};
+static_assert(PackBwdCfg<128>::SMEM <= 232448, "shared memory");
+
+// (lse, D, last key seen) of a block's 128 rows, each kind in a row of its own:
+// the keys' threads read four rows at a time, the same ones in every thread.
+struct RowTerms {
+    float lse[128], delta[128];
+    int last[128];
+};
+
+struct PackBwdBars {
+    uint64_t own_full;                   // the CTA's own tiles
+    uint64_t x_full[3], x_empty[3];      // K blocks | Q blocks (2)
+    uint64_t y_full[2], y_empty[2];      // V blocks | dO blocks
+    uint64_t s_full[2], dp_full, p_ready, ds_ready, mma_done;
+    uint32_t tmem_base;
+    int abort;
+};
+
+__device__ __forceinline__ void bwd_bars_init(PackBwdBars* b) {
+    b->abort = 0;
+    mbar_init(&b->own_full, 1);
+    for (int x = 0; x < 3; ++x) { mbar_init(&b->x_full[x], 1); mbar_init(&b->x_empty[x], 1); }
+    for (int x = 0; x < 2; ++x) { mbar_init(&b->y_full[x], 1); mbar_init(&b->y_empty[x], 1); mbar_init(&b->s_full[x], 1); }
+    mbar_init(&b->dp_full, 1);
+    mbar_init(&b->p_ready, 256);
+    mbar_init(&b->ds_ready, 256);
+    mbar_init(&b->mma_done, 1);
+    fence_barrier_init();
+}
+
+// acc (+)= A B^T, both tiles of 128 rows in shared memory, K-major.
+template <int D>
+__device__ __forceinline__ void mma_scores(uint32_t acc, uint32_t a, uint32_t b) {
+    constexpr uint32_t id = idesc_bf16_f32(128, 128, false, false);
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t o = (kk >> 2) * PackBwdCfg<D>::CHUNK + (kk & 3) * 32;
+        mma_bf16_ss(acc, smem_desc_sw128(a + o, 16, 1024), smem_desc_sw128(b + o, 16, 1024), id, kk > 0);
+    }
+}
+
+// acc (+)= T X: T 128 x 128 bf16 in TMEM (columns 0-63 of its inner dimension
+// at t, 64-127 at t + 64), X a tile of 128 rows x D in shared memory.
+template <int D>
+__device__ __forceinline__ void mma_weighted(uint32_t acc, uint32_t t, uint32_t x, bool accumulate) {
+    constexpr uint32_t id = idesc_bf16_f32(128, D, false, true);
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk)
+        mma_bf16_ts(acc, t + (kk >> 2) * 64 + (kk & 3) * 8, smem_desc_sw128(x + kk * 2048, PackBwdCfg<D>::CHUNK, 1024), id,
+                    accumulate || kk > 0);
+}
+
+// Rows [from, 128) of a tile become zeros (256 threads).
+template <int D>
+__device__ __forceinline__ void zero_rows(uint8_t* tile, int from, int tid) {
+    constexpr int NCH = PackBwdCfg<D>::NCH;
+    for (int u = tid; u < (128 - from) * 8 * NCH; u += 256)
+        *reinterpret_cast<uint4*>(tile + (u % NCH) * PackBwdCfg<D>::CHUNK + from * 128 + (u / NCH) * 16) = make_uint4(0, 0, 0, 0);
+}
+
+// Half a row (D/2 features) of an accumulator, times `scale`, as bf16; zeros
+// where the accumulator was never written.
+template <int D>
+__device__ __forceinline__ void store_grad(uint32_t acc, bool written, float scale, __nv_bfloat16* dst, bool valid) {
+#pragma unroll
+    for (int c = 0; c < D / 2; c += 32) {
+        float o[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = 0.f;
+        if (written) { tmem_ld_32x32b_x32(acc + c, o); tmem_wait_ld(); }
+        if (valid) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 8)
+                *reinterpret_cast<uint4*>(dst + c + e) =
+                    make_uint4(pack_bf16x2(o[e] * scale, o[e + 1] * scale), pack_bf16x2(o[e + 2] * scale, o[e + 3] * scale),
+                               pack_bf16x2(o[e + 4] * scale, o[e + 5] * scale), pack_bf16x2(o[e + 6] * scale, o[e + 7] * scale));
+        }
+    }
+}
+
+// ------------------------------------------------------------------------ dQ
+template <int D>
+__global__ void __launch_bounds__(PackBwdCfg<D>::THREADS, 1)
+packed_dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                 const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mg, const PackedShape sh,
+                 const int tok_per_tile, const int tiles, const int32_t* __restrict__ cu_q,
+                 const int32_t* __restrict__ cu_k, const int causal, const float scale_log2, const float scale,
+                 const float2* __restrict__ terms, __nv_bfloat16* __restrict__ dq, const long long dq_stride,
+                 int* status) {
+    using C = PackBwdCfg<D>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    if (smem_u32(smem) & 1023) {
+        if (threadIdx.x == 0) report(status, kStatusMisaligned);
+        return;
+    }
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int group = sh.heads_q / sh.heads_kv;
+    const int kvh = blockIdx.x % sh.heads_kv;
+    // the last tiles of a sequence see the most keys: they start first
+    const SeqTile at = find_tile(cu_q, sh.n_seq, sh.total_q, tok_per_tile, tiles - 1 - blockIdx.x / sh.heads_kv, status);
+    if (at.seq < 0) return;
+    const SeqRange qr = seq_range(cu_q, at.seq, sh.total_q, status), kr = seq_range(cu_k, at.seq, sh.total_k, status);
+    const int tok0 = at.tile * tok_per_tile;
+    const int n = (seen_keys(min(tok0 + tok_per_tile, qr.len) - 1, qr.len, kr.len, causal) + 127) / 128;   // key blocks
+    uint8_t* sQ = smem;
+    uint8_t* sG = smem + C::TILE;
+    uint8_t* sK = smem + 2 * C::TILE;                    // 3 slots: a K block is read by S and, two steps later, by dQ
+    uint8_t* sV = smem + 5 * C::TILE;                    // 2 slots
+    PackBwdBars* bars = reinterpret_cast<PackBwdBars*>(smem + C::BAR_OFF);
+    volatile int* abort_flag = &bars->abort;
+    if (tid == 0) bwd_bars_init(bars);
+    if (warp == 9) { tmem_alloc(&bars->tmem_base, 512); tmem_relinquish(); }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tbase = bars->tmem_base;
+    const uint32_t tDP = tbase + 256, tAcc = tbase + 384;     // S of block j at 128 (j & 1)
+    auto fail = [&]() { *abort_flag = 1; report(status, kStatusTimeout); };
+
+    if (warp == 8) {
+        if (lane == 0 && n > 0) {
+            mbar_arrive_expect_tx(&bars->own_full, 2 * C::NCH * tok_per_tile * group * 128);
+            for (int c = 0; c < C::NCH; ++c) {
+                tma_load_3d(sQ + c * C::CHUNK, &mq, &bars->own_full, 64 * c, kvh * group, qr.begin + tok0);
+                tma_load_3d(sG + c * C::CHUNK, &mg, &bars->own_full, 64 * c, kvh * group, qr.begin + tok0);
+            }
+            int done = 0;
+            for (int t = 0; t < n; ++t) {
+                const int x = t % 3, y = t & 1;
+                if (t >= 3 && !mbar_wait(&bars->x_empty[x], (t / 3 - 1) & 1, abort_flag)) { fail(); break; }
+                mbar_arrive_expect_tx(&bars->x_full[x], C::TILE);
+                for (int c = 0; c < C::NCH; ++c)
+                    tma_load_3d(sK + x * C::TILE + c * C::CHUNK, &mk, &bars->x_full[x], 64 * c, kvh, kr.begin + 128 * t);
+                if (t >= 2 && !mbar_wait(&bars->y_empty[y], (t / 2 - 1) & 1, abort_flag)) {
+                    wait_noabort(&bars->x_full[x], (t / 3) & 1);
+                    fail();
+                    break;
+                }
+                mbar_arrive_expect_tx(&bars->y_full[y], C::TILE);
+                for (int c = 0; c < C::NCH; ++c)
+                    tma_load_3d(sV + y * C::TILE + c * C::CHUNK, &mv, &bars->y_full[y], 64 * c, kvh, kr.begin + 128 * t);
+                ++done;
+            }
+            if (*abort_flag) {
+                // drain: every load must land before the shared memory is given up
+                wait_noabort(&bars->own_full, 0);
+                for (int t = max(0, done - 3); t < done; ++t) wait_noabort(&bars->x_full[t % 3], (t / 3) & 1);
+                for (int t = max(0, done - 2); t < done; ++t) wait_noabort(&bars->y_full[t & 1], (t / 2) & 1);
+            }
+        }
+    } else if (warp == 9) {
+        if (lane == 0 && n > 0) {
+            const uint32_t q = smem_u32(sQ), g = smem_u32(sG), k = smem_u32(sK), v = smem_u32(sV);
+            auto issue_s = [&](int t) {
+                if (!mma_wait(&bars->x_full[t % 3], (t / 3) & 1, abort_flag)) return false;
+                tc_fence_after();
+                mma_scores<D>(tbase + 128 * (t & 1), q, k + (t % 3) * C::TILE);
+                mma_commit(&bars->s_full[t & 1]);
+                return true;
+            };
+            auto issue_dp = [&](int t) {
+                if (!mma_wait(&bars->y_full[t & 1], (t / 2) & 1, abort_flag)) return false;
+                tc_fence_after();
+                mma_scores<D>(tDP, g, v + (t & 1) * C::TILE);
+                mma_commit(&bars->dp_full);
+                mma_commit(&bars->y_empty[t & 1]);
+                return true;
+            };
+            bool ok = mma_wait(&bars->own_full, 0, abort_flag) && issue_s(0) && issue_dp(0) && (n < 2 || issue_s(1));
+            for (int t = 0; t < n && ok; ++t) {
+                ok = mma_wait(&bars->ds_ready, t & 1, abort_flag);
+                if (!ok) break;
+                tc_fence_after();
+                if (t + 1 < n && !(ok = issue_dp(t + 1))) break;
+                mma_weighted<D>(tAcc, tbase + 128 * (t & 1), k + (t % 3) * C::TILE, t > 0);
+                mma_commit(&bars->x_empty[t % 3]);
+                if (t + 2 < n) ok = issue_s(t + 2);
+            }
+            if (!ok) fail();
+            mma_commit(&bars->mma_done);
+            wait_noabort(&bars->mma_done, 0);
+        }
+    } else {
+        const int r = 32 * (warp & 3) + lane, hf = warp >> 2;     // row, half of the columns
+        const int tok = tok0 + r / group;
+        const bool valid = r < tok_per_tile * group && tok < qr.len;
+        const int lim = valid ? seen_keys(tok, qr.len, kr.len, causal) : 0;
+        const int lim_min = seen_keys(tok0, qr.len, kr.len, causal);
+        const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
+        float2 ld = make_float2(0.f, 0.f);
+        if (valid) ld = __ldg(terms + ((long long)kvh * sh.total_q + qr.begin + tok) * group + r % group);
+        bool ok = true;
+        for (int t = 0; t < n; ++t) {
+            if (128 * t + 128 > kr.len) {                // the last, partial block: K's rows behind the sequence
+                if (!__all_sync(0xffffffffu, mbar_wait(&bars->x_full[t % 3], (t / 3) & 1, abort_flag))) { ok = false; break; }
+                zero_rows<D>(sK + (t % 3) * C::TILE, kr.len - 128 * t, tid);
+                fence_proxy_async_smem();
+            }
+            const uint32_t tS = tbase + lane_base + 128 * (t & 1) + 64 * hf;
+            if (!__all_sync(0xffffffffu, mbar_wait(&bars->s_full[t & 1], (t >> 1) & 1, abort_flag))) { ok = false; break; }
+            tc_fence_after();
+            float p[64];
+            tmem_ld_32x32b_x32(tS, *reinterpret_cast<float(*)[32]>(&p[0]));
+            tmem_ld_32x32b_x32(tS + 32, *reinterpret_cast<float(*)[32]>(&p[32]));
+            tmem_wait_ld();
+            if (128 * t + 128 > lim_min) {
+                const int seen = lim - 128 * t - 64 * hf;
+#pragma unroll
+                for (int e = 0; e < 64; ++e) p[e] = e < seen ? ex2(fmaf(p[e], scale_log2, -ld.x)) : 0.f;
+            } else {
+#pragma unroll
+                for (int e = 0; e < 64; ++e) p[e] = ex2(fmaf(p[e], scale_log2, -ld.x));
+            }
+            if (!__all_sync(0xffffffffu, mbar_wait(&bars->dp_full, t & 1, abort_flag))) { ok = false; break; }
+            tc_fence_after();
+            const bool masked = 128 * t + 128 > lim_min;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                float dp[32];
+                tmem_ld_32x32b_x32(tDP + lane_base + 64 * hf + 32 * c, dp);
+                tmem_wait_ld();
+                uint32_t pk[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    float d0 = p[32 * c + 2 * e] * (dp[2 * e] - ld.y), d1 = p[32 * c + 2 * e + 1] * (dp[2 * e + 1] - ld.y);
+                    if (masked) {                        // dP of a masked place may be anything
+                        const int seen = lim - 128 * t - 64 * hf - 32 * c;
+                        d0 = 2 * e < seen ? d0 : 0.f;
+                        d1 = 2 * e + 1 < seen ? d1 : 0.f;
+                    }
+                    pk[e] = pack_bf16x2(d0, d1);
+                }
+                tmem_st_32x32b_x16(tS + 16 * c, pk);     // dS over S: this thread's 64 columns in 32
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(&bars->ds_ready);
+        }
+        if (ok && n > 0 && !__all_sync(0xffffffffu, mbar_wait(&bars->mma_done, 0, abort_flag))) ok = false;
+        if (!ok) fail();
+        if (ok) {
+            tc_fence_after();
+            store_grad<D>(tAcc + lane_base + hf * (D / 2), n > 0, scale,
+                          dq + ((long long)qr.begin + tok) * dq_stride + (long long)(kvh * group + r % group) * D + hf * (D / 2), valid);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 9) tmem_dealloc(tbase, 512);
+}
+
+// --------------------------------------------------------------------- dK, dV
+template <int D>
+__global__ void __launch_bounds__(PackBwdCfg<D>::THREADS, 1)
+packed_dkdv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                   const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mg, const PackedShape sh,
+                   const int tok_per_tile, const int32_t* __restrict__ cu_q, const int32_t* __restrict__ cu_k,
+                   const int causal, const float scale_log2, const float scale, const float2* __restrict__ terms,
+                   __nv_bfloat16* __restrict__ dk, const long long dk_stride, __nv_bfloat16* __restrict__ dv,
+                   const long long dv_stride, int* status) {
+    using C = PackBwdCfg<D>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    if (smem_u32(smem) & 1023) {
+        if (threadIdx.x == 0) report(status, kStatusMisaligned);
+        return;
+    }
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int group = sh.heads_q / sh.heads_kv;
+    const int kvh = blockIdx.x % sh.heads_kv;
+    // the first tiles of a sequence are seen by the most queries: they start first
+    const SeqTile at = find_tile(cu_k, sh.n_seq, sh.total_k, 128, blockIdx.x / sh.heads_kv, status);
+    if (at.seq < 0) return;
+    const SeqRange qr = seq_range(cu_q, at.seq, sh.total_q, status), kr = seq_range(cu_k, at.seq, sh.total_k, status);
+    const int key0 = 128 * at.tile;
+    const int rows = tok_per_tile * group;               // rows of a block in use
+    // first query token that sees key0, and the blocks from its on
+    const int tok_first = causal ? max(0, key0 + qr.len - kr.len) : 0;
+    const int b0 = tok_first / tok_per_tile;
+    const int n = max(0, (qr.len + tok_per_tile - 1) / tok_per_tile - b0);
+    uint8_t* sK = smem;
+    uint8_t* sV = smem + C::TILE;
+    uint8_t* sQ = smem + 2 * C::TILE;                    // 2 slots
+    uint8_t* sG = smem + 4 * C::TILE;                    // 2 slots
+    RowTerms* sT = reinterpret_cast<RowTerms*>(smem + 6 * C::TILE);   // of the even and the odd blocks
+    PackBwdBars* bars = reinterpret_cast<PackBwdBars*>(smem + C::BAR_OFF);
+    volatile int* abort_flag = &bars->abort;
+    if (tid == 0) bwd_bars_init(bars);
+    if (warp == 9) { tmem_alloc(&bars->tmem_base, 512); tmem_relinquish(); }
+    if (rows < 128 && tid < 256) {
+        // rows that no load writes (a group that does not divide 128): zeros
+        for (int x = 0; x < 4; ++x) zero_rows<D>(sQ + x * C::TILE, rows, tid);
+        fence_proxy_async_smem();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tbase = bars->tmem_base;
+    const uint32_t tS = tbase, tDP = tbase + 128, tDV = tbase + 256, tDK = tbase + 384;
+    auto fail = [&]() { *abort_flag = 1; report(status, kStatusTimeout); };
+
+    if (warp == 8) {
+        if (lane == 0 && n > 0) {
+            mbar_arrive_expect_tx(&bars->own_full, 2 * C::TILE);
+            for (int c = 0; c < C::NCH; ++c) {
+                tma_load_3d(sK + c * C::CHUNK, &mk, &bars->own_full, 64 * c, kvh, kr.begin + key0);
+                tma_load_3d(sV + c * C::CHUNK, &mv, &bars->own_full, 64 * c, kvh, kr.begin + key0);
+            }
+            int done = 0;
+            for (int t = 0; t < n; ++t) {
+                const int x = t & 1;
+                // one barrier frees a slot's Q and dO: dK of step t - 2, the last product to read them
+                if (t >= 2 && !mbar_wait(&bars->x_empty[x], (t / 2 - 1) & 1, abort_flag)) { fail(); break; }
+                const int row = qr.begin + (b0 + t) * tok_per_tile;
+                mbar_arrive_expect_tx(&bars->x_full[x], C::NCH * rows * 128);
+                for (int c = 0; c < C::NCH; ++c)
+                    tma_load_3d(sQ + x * C::TILE + c * C::CHUNK, &mq, &bars->x_full[x], 64 * c, kvh * group, row);
+                mbar_arrive_expect_tx(&bars->y_full[x], C::NCH * rows * 128);
+                for (int c = 0; c < C::NCH; ++c)
+                    tma_load_3d(sG + x * C::TILE + c * C::CHUNK, &mg, &bars->y_full[x], 64 * c, kvh * group, row);
+                ++done;
+            }
+            if (*abort_flag) {
+                wait_noabort(&bars->own_full, 0);
+                for (int t = max(0, done - 2); t < done; ++t) {
+                    wait_noabort(&bars->x_full[t & 1], (t / 2) & 1);
+                    wait_noabort(&bars->y_full[t & 1], (t / 2) & 1);
+                }
+            }
+        }
+    } else if (warp == 9) {
+        if (lane == 0 && n > 0) {
+            const uint32_t k = smem_u32(sK), v = smem_u32(sV), q = smem_u32(sQ), g = smem_u32(sG);
+            auto issue_s = [&](int t) {
+                if (!mma_wait(&bars->x_full[t & 1], (t / 2) & 1, abort_flag)) return false;
+                tc_fence_after();
+                mma_scores<D>(tS, k, q + (t & 1) * C::TILE);
+                mma_commit(&bars->s_full[0]);
+                return true;
+            };
+            auto issue_dp = [&](int t) {
+                if (!mma_wait(&bars->y_full[t & 1], (t / 2) & 1, abort_flag)) return false;
+                tc_fence_after();
+                mma_scores<D>(tDP, v, g + (t & 1) * C::TILE);
+                mma_commit(&bars->dp_full);
+                return true;
+            };
+            bool ok = mma_wait(&bars->own_full, 0, abort_flag) && issue_s(0) && issue_dp(0);
+            for (int t = 0; t < n && ok; ++t) {
+                if (!(ok = mma_wait(&bars->p_ready, t & 1, abort_flag))) break;
+                tc_fence_after();
+                mma_weighted<D>(tDV, tS, g + (t & 1) * C::TILE, t > 0);
+                if (t + 1 < n && !(ok = issue_s(t + 1))) break;
+                if (!(ok = mma_wait(&bars->ds_ready, t & 1, abort_flag))) break;
+                tc_fence_after();
+                mma_weighted<D>(tDK, tDP, q + (t & 1) * C::TILE, t > 0);
+                mma_commit(&bars->x_empty[t & 1]);
+                if (t + 1 < n) ok = issue_dp(t + 1);
+            }
+            if (!ok) fail();
+            mma_commit(&bars->mma_done);
+            wait_noabort(&bars->mma_done, 0);
+        }
+    } else {
+        const int r = 32 * (warp & 3) + lane, hf = warp >> 2;     // key of the tile, half of the query rows
+        const int key = key0 + r;
+        const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
+        // weights of a row that is not there are 2^-inf = 0
+        float row_lse = CUDART_INF_F, row_delta = 0.f;
+        int row_last = -1;
+        auto fetch = [&](int t) {
+            const int tok = (b0 + t) * tok_per_tile + tid / group;
+            row_lse = CUDART_INF_F; row_delta = 0.f; row_last = -1;
+            if (tid < rows && tok < qr.len) {
+                const float2 ld = __ldg(terms + ((long long)kvh * sh.total_q + qr.begin + tok) * group + tid % group);
+                row_lse = ld.x;
+                row_delta = ld.y;
+                row_last = seen_keys(tok, qr.len, kr.len, causal) - 1;
+            }
+        };
+        if (tid < 128 && n > 0) fetch(0);
+        bool ok = true;
+        // A wait that gave up leaves `ok` false in its warp, which then walks on
+        // through the barriers below without working.
+        for (int t = 0; t < n; ++t) {
+            RowTerms& tr = sT[t & 1];
+            if (tid < 128) {
+                tr.lse[tid] = row_lse; tr.delta[tid] = row_delta; tr.last[tid] = row_last;
+                if (t + 1 < n) fetch(t + 1);
+            }
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+            if (!ok) continue;
+            const int tok0 = (b0 + t) * tok_per_tile;
+            const bool tail = tok0 + tok_per_tile > qr.len;
+            // keys hidden from the block's first token, or rows behind the sequence
+            const bool masked = tail || seen_keys(tok0, qr.len, kr.len, causal) < min(key0 + 128, kr.len);
+            if (tail) {
+                bool here = mbar_wait(&bars->x_full[t & 1], (t / 2) & 1, abort_flag);
+                here = here && mbar_wait(&bars->y_full[t & 1], (t / 2) & 1, abort_flag);
+                if (!__all_sync(0xffffffffu, here)) { ok = false; continue; }
+                zero_rows<D>(sQ + (t & 1) * C::TILE, (qr.len - tok0) * group, tid);
+                zero_rows<D>(sG + (t & 1) * C::TILE, (qr.len - tok0) * group, tid);
+                fence_proxy_async_smem();
+            }
+            if (!__all_sync(0xffffffffu, mbar_wait(&bars->s_full[0], t & 1, abort_flag))) { ok = false; continue; }
+            tc_fence_after();
+            float p[64];
+            tmem_ld_32x32b_x32(tS + lane_base + 64 * hf, *reinterpret_cast<float(*)[32]>(&p[0]));
+            tmem_ld_32x32b_x32(tS + lane_base + 64 * hf + 32, *reinterpret_cast<float(*)[32]>(&p[32]));
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 64; e += 4) {
+                const float4 l = *reinterpret_cast<const float4*>(&tr.lse[64 * hf + e]);
+                p[e] = ex2(fmaf(p[e], scale_log2, -l.x));
+                p[e + 1] = ex2(fmaf(p[e + 1], scale_log2, -l.y));
+                p[e + 2] = ex2(fmaf(p[e + 2], scale_log2, -l.z));
+                p[e + 3] = ex2(fmaf(p[e + 3], scale_log2, -l.w));
+            }
+            if (masked) {
+#pragma unroll
+                for (int e = 0; e < 64; ++e) p[e] = key <= tr.last[64 * hf + e] ? p[e] : 0.f;
+            }
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                uint32_t pk[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) pk[e] = pack_bf16x2(p[32 * c + 2 * e], p[32 * c + 2 * e + 1]);
+                tmem_st_32x32b_x16(tS + lane_base + 64 * hf + 16 * c, pk);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(&bars->p_ready);
+            if (!__all_sync(0xffffffffu, mbar_wait(&bars->dp_full, t & 1, abort_flag))) { ok = false; continue; }
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                float dp[32];
+                tmem_ld_32x32b_x32(tDP + lane_base + 64 * hf + 32 * c, dp);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) {
+                    const float4 x = *reinterpret_cast<const float4*>(&tr.delta[64 * hf + 32 * c + e]);
+                    dp[e] = p[32 * c + e] * (dp[e] - x.x);
+                    dp[e + 1] = p[32 * c + e + 1] * (dp[e + 1] - x.y);
+                    dp[e + 2] = p[32 * c + e + 2] * (dp[e + 2] - x.z);
+                    dp[e + 3] = p[32 * c + e + 3] * (dp[e + 3] - x.w);
+                }
+                if (masked) {                            // dP of a masked place may be anything
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) dp[e] = key <= tr.last[64 * hf + 32 * c + e] ? dp[e] : 0.f;
+                }
+                uint32_t pk[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) pk[e] = pack_bf16x2(dp[2 * e], dp[2 * e + 1]);
+                tmem_st_32x32b_x16(tDP + lane_base + 64 * hf + 16 * c, pk);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(&bars->ds_ready);
+        }
+        if (ok && n > 0 && !__all_sync(0xffffffffu, mbar_wait(&bars->mma_done, 0, abort_flag))) ok = false;
+        if (!ok) fail();
+        if (ok) {
+            tc_fence_after();
+            const bool valid = key < kr.len;
+            const long long row = (long long)kr.begin + key;
+            store_grad<D>(tDV + lane_base + hf * (D / 2), n > 0, 1.f, dv + row * dv_stride + (long long)kvh * D + hf * (D / 2), valid);
+            store_grad<D>(tDK + lane_base + hf * (D / 2), n > 0, scale, dk + row * dk_stride + (long long)kvh * D + hf * (D / 2), valid);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 9) tmem_dealloc(tbase, 512);
+}
+
+// --------------------------------------------------------------------- launch
+long long packed_bwd_work_items(const PackedShape& s) {
+    const long long q = (long long)s.total_q / (128 / s.group()) + s.n_seq, k = (long long)s.total_k / 128 + s.n_seq;
+    return std::max(std::max(q, k) * s.heads_kv, ((long long)s.total_q * s.heads_q * s.d + 2047) / 2048);
+}
+
+size_t packed_bwd_scratch_bytes(const PackedShape& s) {
+    return (size_t)s.total_q * s.heads_q * sizeof(float2);
+}
+
+template <int D>
+static cudaError_t launch_packed_bwd_impl(const PackedArgs& a, cudaStream_t stream) {
+    using C = PackBwdCfg<D>;
+    const PackedShape& s = a.s;
+    const int group = s.group(), tok = 128 / group;
+    cudaError_t e = cudaFuncSetAttribute(packed_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(packed_dkdv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    float2* terms = reinterpret_cast<float2*>(a.scratch);
+    // a side without rows is never loaded: any valid address will do for its maps
+    void* any = s.total_q ? a.q.p : a.k.p;
+    const PackedTensor none_q{any, (long long)s.heads_q * D}, none_k{any, (long long)s.heads_kv * D};
+    const int rq = std::max(1, s.total_q), rk = std::max(1, s.total_k);
+    CUtensorMap mq, mk, mv, mg;
+    if (!encode_packed_map(&mq, s.total_q ? a.q : none_q, rq, s.heads_q, D, group, tok, a.enc) ||
+        !encode_packed_map(&mg, s.total_q ? a.dout : none_q, rq, s.heads_q, D, group, tok, a.enc) ||
+        !encode_packed_map(&mk, s.total_k ? a.k : none_k, rk, s.heads_kv, D, 1, 128, a.enc) ||
+        !encode_packed_map(&mv, s.total_k ? a.v : none_k, rk, s.heads_kv, D, 1, 128, a.enc))
+        return cudaErrorInvalidValue;
+    const float scale = 1.f / sqrtf((float)D), scale_log2 = 1.4426950408889634f * scale;
+    if (s.total_q) {
+        const long long rows = (long long)s.total_q * s.heads_q;
+        row_terms_kernel<D><<<(unsigned)((rows + 2048 / D - 1) / (2048 / D)), 256, 0, stream>>>(
+            a.out32, static_cast<const __nv_bfloat16*>(a.dout.p), a.dout.stride, a.lse, s.total_q, s.heads_q, group, terms);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        const int tiles = s.total_q / tok + s.n_seq;
+        packed_dq_kernel<D><<<(unsigned)(tiles * s.heads_kv), C::THREADS, C::SMEM, stream>>>(
+            mq, mk, mv, mg, s, tok, tiles, a.cu_q, a.cu_k, a.causal, scale_log2, scale, terms,
+            static_cast<__nv_bfloat16*>(a.dq.p), a.dq.stride, a.status);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
+    if (s.total_k) {
+        const int tiles = s.total_k / 128 + s.n_seq;
+        packed_dkdv_kernel<D><<<(unsigned)(tiles * s.heads_kv), C::THREADS, C::SMEM, stream>>>(
+            mq, mk, mv, mg, s, tok, a.cu_q, a.cu_k, a.causal, scale_log2, scale, terms,
+            static_cast<__nv_bfloat16*>(a.dk.p), a.dk.stride, static_cast<__nv_bfloat16*>(a.dv.p), a.dv.stride, a.status);
+        e = cudaGetLastError();
+    }
+    return e;
+}
+
+cudaError_t launch_packed_bwd(const PackedArgs& a, cudaStream_t stream) {
+    return a.s.d == 128 ? launch_packed_bwd_impl<128>(a, stream) : launch_packed_bwd_impl<64>(a, stream);
+}
+
+}  // namespace vsa

@@ -223,6 +223,20 @@ def vsa_packed_attn_fwd(q, k, v, cu_q, cu_k, out, workspace, causal=True, out_f3
             workspace.data_ptr(), workspace.numel(), _stream(stream)))
 
 
+def vsa_packed_attn_bwd(q, k, v, out_f32, dout, cu_q, cu_k, lse, dq, dk, dv, workspace, causal=True, stream=None):
+    """Gradients of vsa_packed_attn_fwd, written into dq, dk, dv (bf16, shaped
+    as q, k, v; rows may be strided); out_f32 and lse are the forward's."""
+    (tq, hq, d), (tk, hk) = q.shape, k.shape[:2]
+    n = _borders(cu_q)[1]
+    assert _borders(cu_k)[1] == n, "cu_q and cu_k describe different numbers of sequences"
+    with _same_device(q, k, v, out_f32, dout, cu_q, cu_k, lse, dq, dk, dv, workspace):
+        _lib.check("vsa_packed_attn_bwd", _lib.lib().vsa_packed_attn_bwd(
+            *_rows(q), *_rows(k, hk, d), *_rows(v, hk, d, tk), _f32(out_f32, (tq, hq, d)), *_rows(dout, hq, d, tq),
+            cu_q.data_ptr(), cu_k.data_ptr(), _f32(lse, (hq, tq)), *_rows(dq, hq, d, tq), *_rows(dk, hk, d, tk),
+            *_rows(dv, hk, d, tk), tq, tk, n, hq, hk, d, int(bool(causal)), workspace.data_ptr(), workspace.numel(),
+            _stream(stream)))
+
+
 def vsa_device_status(workspace, stream=None) -> int:
     """Synchronise and return the device status code (0 = VSA_OK)."""
     return _lib.lib().vsa_device_status(workspace.data_ptr(), _stream(stream))

@@ -321,6 +321,21 @@ vsa_status vsa_packed_attn_fwd(const vsa_bf16* q, long long q_stride, const vsa_
                                int total_k, int n_seq, int heads_q, int heads_kv, int head_dim, int causal,
                                void* workspace, size_t workspace_bytes, vsa_stream_t stream);
 
+/* Gradients of vsa_packed_attn_fwd.  out_f32 and lse are that call's, with the
+ * same causal flag and borders; dout is the gradient of its output.
+ *     dv_j = sum_i p_ij dout_i,  ds_ij = p_ij (dout_i.v_j - dout_i.out_i),
+ *     dq_i = sum_j ds_ij k_j / sqrt(d),  dk_j = sum_i ds_ij q_i / sqrt(d),
+ * dk and dv summed over the query heads of a group too (in fp32, in a fixed
+ * order: the same call gives the same bits).  p and ds are rounded to bf16
+ * for the products.  dq, dk, dv must not overlap the inputs or one another. */
+vsa_status vsa_packed_attn_bwd(const vsa_bf16* q, long long q_stride, const vsa_bf16* k, long long k_stride,
+                               const vsa_bf16* v, long long v_stride, const float* out_f32, const vsa_bf16* dout,
+                               long long dout_stride, const int32_t* cu_q, const int32_t* cu_k, const float* lse,
+                               vsa_bf16* dq, long long dq_stride, vsa_bf16* dk, long long dk_stride, vsa_bf16* dv,
+                               long long dv_stride, int total_q, int total_k, int n_seq, int heads_q, int heads_kv,
+                               int head_dim, int causal, void* workspace, size_t workspace_bytes,
+                               vsa_stream_t stream);
+
 /* Self-test of the device failure path (no counterpart on the pages): a
  * one-warp kernel waits on a barrier nobody arrives at, gives up after
  * `limit_cycles` SM clock cycles exactly as the library's kernels do, and
