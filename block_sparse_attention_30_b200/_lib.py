@@ -18,6 +18,7 @@ STATUS_NAMES = {
 
 # (name, restype, argtypes) for every entry point of include/vsa.h
 _i, _ll, _sz, _p = ctypes.c_int, ctypes.c_longlong, ctypes.c_size_t, ctypes.c_void_p
+_f = ctypes.c_float
 _SHAPE = [_i] * 9                       # B, heads, head_dim, T, H, W, tt, th, tw
 SIGNATURES = {
     "vsa_status_string": (ctypes.c_char_p, [_i]),
@@ -38,6 +39,10 @@ SIGNATURES = {
     "vsa_packed_attn_workspace_bytes": (_sz, [_i] * 6),
     "vsa_packed_attn_fwd": (_i, [_p, _ll] * 3 + [_p, _p] + [_p, _ll] + [_p, _p] + [_i] * 7 + [_p, _sz, _p]),
     "vsa_packed_attn_bwd": (_i, [_p, _ll] * 3 + [_p] + [_p, _ll] + [_p] * 3 + [_p, _ll] * 3 + [_i] * 7 + [_p, _sz, _p]),
+    "vsa_decay_attn_workspace_bytes": (_sz, [_i] * 4),
+    "vsa_decay_attn_fwd": (_i, [_p, _ll] * 3 + [_p] * 4 + [_p, _ll, _f] + [_i] * 4 + [_p, _sz, _p]),
+    "vsa_decay_attn_bwd": (_i, [_p, _ll] * 4 + [_p] * 4 + [_p, _ll] * 3 + [_p, _f] + [_i] * 4 + [_p, _sz, _p]),
+    "vsa_decay_attn_step": (_i, [_p, _ll] * 3 + [_p] * 3 + [_p, _ll, _f] + [_i] * 3 + [_p]),
     "vsa_device_status": (_i, [_p, _p]),
     "vsa_select_blocks_noalloc": (_i, [_p, _p] + _SHAPE + [_i, _p, _p]),
     "vsa_selftest_wait_timeout": (_i, [_p, _sz, ctypes.c_uint, _p]),

@@ -118,6 +118,17 @@ vsa_status check_packed(int total_q, int total_k, int n_seq, int heads_q, int he
     return VSA_OK;
 }
 
+vsa_status check_decay(int total, int n_seq, int heads, int d) {
+    if (total < 0 || n_seq < 1 || heads < 1 || d < 1) return VSA_ERR_INVALID_ARGUMENT;
+    if (d != 64 && d != 128) return VSA_ERR_UNSUPPORTED;
+    if (total >= (1 << 30) || n_seq >= (1 << 24) || heads >= (1 << 16)) return VSA_ERR_UNSUPPORTED;
+    if (vsa::decay_work_items(n_seq, total, heads) > 0x7fffffffll) return VSA_ERR_UNSUPPORTED;
+    return VSA_OK;
+}
+
+// An fp32 state that may be absent.
+bool state_ok(const float* p) { return p == nullptr || aligned16(p); }
+
 vsa_status from_cuda(cudaError_t e) { return e == cudaSuccess ? VSA_OK : VSA_ERR_CUDA; }
 
 }  // namespace
@@ -528,6 +539,116 @@ vsa_status vsa_packed_attn_bwd(const vsa_bf16* q, long long q_stride, const vsa_
     a.status = static_cast<int*>(workspace);
     if (!(a.enc = encode_fn())) return VSA_ERR_CUDA;
     return from_cuda(vsa::launch_packed_bwd(a, (cudaStream_t)stream));
+}
+
+size_t vsa_decay_attn_workspace_bytes(int total, int n_seq, int heads, int head_dim) {
+    if (check_decay(total, n_seq, heads, head_dim) != VSA_OK) return 0;
+    return kStatusBytes + vsa::decay_scratch_bytes(n_seq, total, heads, head_dim);
+}
+
+vsa_status vsa_decay_attn_fwd(const vsa_bf16* q, long long q_stride, const vsa_bf16* k, long long k_stride,
+                              const vsa_bf16* v, long long v_stride, const float* log_decay, const int32_t* cu,
+                              const float* state_in, float* state_out, vsa_bf16* out, long long out_stride,
+                              float scale, int total, int n_seq, int heads, int head_dim, void* workspace,
+                              size_t workspace_bytes, vsa_stream_t stream) {
+    vsa_status s = check_decay(total, n_seq, heads, head_dim);
+    if (s != VSA_OK) return s;
+    if (!packed_ok(q, q_stride, total, heads, head_dim) || !packed_ok(k, k_stride, total, heads, head_dim) ||
+        !packed_ok(v, v_stride, total, heads, head_dim) || !packed_ok(out, out_stride, total, heads, head_dim))
+        return VSA_ERR_INVALID_ARGUMENT;
+    if (!aligned4(log_decay) || !aligned4(cu) || !state_ok(state_in) || !state_ok(state_out))
+        return VSA_ERR_INVALID_ARGUMENT;
+    if (state_out && state_in == state_out) return VSA_ERR_INVALID_ARGUMENT;
+    if (!aligned16(workspace)) return VSA_ERR_WORKSPACE;
+    if (workspace_bytes < kStatusBytes + vsa::decay_scratch_bytes(n_seq, total, heads, head_dim)) return VSA_ERR_WORKSPACE;
+    vsa::DecayArgs a{};
+    a.n_seq = n_seq;
+    a.total = total;
+    a.heads = heads;
+    a.d = head_dim;
+    a.q = packed(q, q_stride, total, heads, head_dim);
+    a.k = packed(k, k_stride, total, heads, head_dim);
+    a.v = packed(v, v_stride, total, heads, head_dim);
+    a.out = packed(out, out_stride, total, heads, head_dim);
+    a.log_decay = log_decay;
+    a.cu = cu;
+    a.state_in = state_in;
+    a.state_out = state_out;
+    a.scale = scale;
+    a.scratch = static_cast<uint8_t*>(workspace) + kStatusBytes;
+    a.status = static_cast<int*>(workspace);
+    if (!(a.enc = encode_fn())) return VSA_ERR_CUDA;
+    return from_cuda(vsa::launch_decay_fwd(a, (cudaStream_t)stream));
+}
+
+vsa_status vsa_decay_attn_bwd(const vsa_bf16* q, long long q_stride, const vsa_bf16* k, long long k_stride,
+                              const vsa_bf16* v, long long v_stride, const vsa_bf16* dout, long long dout_stride,
+                              const float* log_decay, const int32_t* cu, const float* state_in,
+                              const float* dstate_out, vsa_bf16* dq, long long dq_stride, vsa_bf16* dk,
+                              long long dk_stride, vsa_bf16* dv, long long dv_stride, float* dstate_in, float scale,
+                              int total, int n_seq, int heads, int head_dim, void* workspace,
+                              size_t workspace_bytes, vsa_stream_t stream) {
+    vsa_status s = check_decay(total, n_seq, heads, head_dim);
+    if (s != VSA_OK) return s;
+    if (!packed_ok(q, q_stride, total, heads, head_dim) || !packed_ok(k, k_stride, total, heads, head_dim) ||
+        !packed_ok(v, v_stride, total, heads, head_dim) || !packed_ok(dout, dout_stride, total, heads, head_dim) ||
+        !packed_ok(dq, dq_stride, total, heads, head_dim) || !packed_ok(dk, dk_stride, total, heads, head_dim) ||
+        !packed_ok(dv, dv_stride, total, heads, head_dim))
+        return VSA_ERR_INVALID_ARGUMENT;
+    if (!aligned4(log_decay) || !aligned4(cu) || !state_ok(state_in) || !state_ok(dstate_out) || !state_ok(dstate_in))
+        return VSA_ERR_INVALID_ARGUMENT;
+    if (dstate_in && dstate_in == dstate_out) return VSA_ERR_INVALID_ARGUMENT;
+    if (!aligned16(workspace)) return VSA_ERR_WORKSPACE;
+    if (workspace_bytes < kStatusBytes + vsa::decay_scratch_bytes(n_seq, total, heads, head_dim)) return VSA_ERR_WORKSPACE;
+    vsa::DecayArgs a{};
+    a.n_seq = n_seq;
+    a.total = total;
+    a.heads = heads;
+    a.d = head_dim;
+    a.q = packed(q, q_stride, total, heads, head_dim);
+    a.k = packed(k, k_stride, total, heads, head_dim);
+    a.v = packed(v, v_stride, total, heads, head_dim);
+    a.dout = packed(dout, dout_stride, total, heads, head_dim);
+    a.dq = packed(dq, dq_stride, total, heads, head_dim);
+    a.dk = packed(dk, dk_stride, total, heads, head_dim);
+    a.dv = packed(dv, dv_stride, total, heads, head_dim);
+    a.log_decay = log_decay;
+    a.cu = cu;
+    a.state_in = state_in;
+    a.dstate_out = dstate_out;
+    a.dstate_in = dstate_in;
+    a.scale = scale;
+    a.scratch = static_cast<uint8_t*>(workspace) + kStatusBytes;
+    a.status = static_cast<int*>(workspace);
+    if (!(a.enc = encode_fn())) return VSA_ERR_CUDA;
+    return from_cuda(vsa::launch_decay_bwd(a, (cudaStream_t)stream));
+}
+
+vsa_status vsa_decay_attn_step(const vsa_bf16* q, long long q_stride, const vsa_bf16* k, long long k_stride,
+                               const vsa_bf16* v, long long v_stride, const float* log_decay, const float* state,
+                               float* state_out, vsa_bf16* out, long long out_stride, float scale, int batch,
+                               int heads, int head_dim, vsa_stream_t stream) {
+    vsa_status s = check_decay(batch, 1, heads, head_dim);
+    if (s != VSA_OK) return s;
+    if ((long long)batch * heads > 0x7fffffffll) return VSA_ERR_UNSUPPORTED;
+    if (batch == 0) return VSA_OK;
+    if (!packed_ok(q, q_stride, batch, heads, head_dim) || !packed_ok(k, k_stride, batch, heads, head_dim) ||
+        !packed_ok(v, v_stride, batch, heads, head_dim) || !packed_ok(out, out_stride, batch, heads, head_dim))
+        return VSA_ERR_INVALID_ARGUMENT;
+    if (!aligned4(log_decay) || !aligned16(state) || !aligned16(state_out)) return VSA_ERR_INVALID_ARGUMENT;
+    vsa::DecayStepArgs a{};
+    a.batch = batch;
+    a.heads = heads;
+    a.d = head_dim;
+    a.q = packed(q, q_stride, batch, heads, head_dim);
+    a.k = packed(k, k_stride, batch, heads, head_dim);
+    a.v = packed(v, v_stride, batch, heads, head_dim);
+    a.out = packed(out, out_stride, batch, heads, head_dim);
+    a.log_decay = log_decay;
+    a.state = state;
+    a.state_out = state_out;
+    a.scale = scale;
+    return from_cuda(vsa::launch_decay_step(a, (cudaStream_t)stream));
 }
 
 vsa_status vsa_device_status(void* workspace, vsa_stream_t stream) {

@@ -1,0 +1,804 @@
+// decay_attn.cu -- linear attention with a decay per head over packed
+// sequences, chunked form and its gradient, on sm_100a (the causal counterpart
+// of the linear branch, whose state sums over the whole grid: here token t
+// only sees the tokens before it, and less of them the further back they lie).
+//
+// Per sequence and head, with lam = exp(log_decay) and an outer product per token:
+//     S_t = lam S_(t-1) + k_t^T v_t,     o_t = scale q_t S_t.
+// One general pass serves the forward and the three gradients:
+//     out_i = sum_j lam^|i-j| (a_i.b_j) c_j    (j <= i, or j >= i walking
+//             backwards in time)  + lam^(..) a_i X,   X the state before the
+//             chunk, b^T c summed with its decays:
+//     out: a, b, c = q, k, v;   dq: dout, v, k (the same state, transposed);
+//     dv:  k, q, dout and dk: v, dout, q backwards in time (state: the
+//          gradient of S, transposed for dk).
+//
+// Tokens go in chunks of 128.  A sequence is cut into segments (a rule on the
+// sizes, see segment_chunks), and three launches compute
+//   decay_state_kernel  each segment's own contribution to the state at its
+//                       border: (b w)^T c with w = lam^(tokens to the border),
+//                       one GEMM with the tokens as its inner dimension;
+//   decay_scan_kernel   the states at the borders, border after border;
+//   decay_out_kernel    one CTA per segment and head walks its chunks with the
+//                       state in TMEM: per chunk
+//                         scores A B^T, times lam^|i-j|, as bf16 P;
+//                         O1 = P C, O2 = A X, out = O1 + lam^(..) O2;
+//                         X = lam^128 X + (B w)^T C.
+// Sequences of one segment need the last launch alone.
+//
+// The state is fp32 throughout (TMEM, scratch, outputs).  The weighted operand
+// of its update is split into bf16 hi + lo (2^-17 relative), so the update is
+// good to about fp32; the state is rounded to bf16 only as the operand of A X
+// and P only as the operand of P C (2^-8 relative at most, as much as
+// the rounding of the output).
+//
+// At d = 64 hi and lo are the two halves of one M = 128 operand: the state's
+// hi part lies in TMEM lanes 0-63 and its lo part in lanes 64-127, A X runs
+// over both, and they are added when the state leaves the kernel.
+#include <algorithm>
+#include <cmath>
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "common.cuh"
+#include "packed.cuh"
+#include "packed.h"
+#include "sm100.cuh"
+
+namespace vsa {
+using namespace sm100;
+
+// One scan over the sequences: a kind of output.
+struct DecayPass {
+    CUtensorMap a, b, c;
+    __nv_bfloat16* out;
+    long long out_stride;
+    const float* first;          // [n_seq][heads][d][d]: the state the walk starts with, or null (zeros)
+    float* last;                 // the state it ends with, or null
+    const float* border;         // [slots][heads][d][d]: the states between segments
+    int back;                    // walk backwards in time
+    int trans;                   // the states in memory are c^T b
+    float w_scale, p_scale, s_scale;   // factors of b^T c in the state, of P, and of A X
+};
+
+struct DecayPasses {
+    DecayPass p[3];
+};
+
+struct DecayShape {
+    int n_seq, total, heads, seg;      // seg: tokens of a segment, a multiple of 128
+};
+
+// log2(lam); below 2^-1024 a decay is a plain 0 (and lam^0 stays 1)
+__device__ __forceinline__ float decay_log2(const float* __restrict__ log_decay, int head) {
+    const float x = __ldg(log_decay + head) * 1.4426950408889634f;
+    return x < -1024.f ? -1024.f : x;
+}
+
+// Where a segment lies, and its border's place in the scratch: the borders
+// start full segments, whose starts are `seg` rows apart at least.
+struct Segment {
+    int seq, begin, len;         // first row and rows of the segment
+    bool first, last;            // of its sequence
+};
+
+__device__ __forceinline__ Segment find_segment(const int32_t* __restrict__ cu, const DecayShape& s, int t, int* status) {
+    Segment g{-1, 0, 0, false, false};
+    const SeqTile at = find_tile(cu, s.n_seq, s.total, s.seg, t, status, 1);
+    if (at.seq < 0) return g;
+    const SeqRange r = seq_range(cu, at.seq, s.total, status);
+    const int off = at.tile * s.seg;
+    g.seq = at.seq;
+    g.begin = r.begin + off;
+    g.len = min(s.seg, r.len - off);
+    g.first = off == 0;
+    g.last = off + s.seg >= r.len;
+    return g;
+}
+
+// bf16 pairs x times w as hi + lo.
+__device__ __forceinline__ void split_pair(uint32_t x, float w, uint32_t& hi, uint32_t& lo) {
+    const float x0 = __uint_as_float(x << 16) * w, x1 = __uint_as_float(x & 0xffff0000u) * w;
+    hi = pack_bf16x2(x0, x1);
+    lo = pack_bf16x2(x0 - __uint_as_float(hi << 16), x1 - __uint_as_float(hi & 0xffff0000u));
+}
+
+// ---------------------------------------------------------------- border sums
+template <int D>
+struct DecStateCfg {
+    static constexpr int NCH = D / 64;
+    static constexpr int CHUNK = 64 * 128;               // 64 tokens of one 64-feature chunk
+    static constexpr int TILE = NCH * CHUNK;
+    static constexpr int STAGE = 3 * TILE;               // b (hi in its place), c, lo
+    static constexpr int NST = D == 128 ? 4 : 8;
+    static constexpr int BAR_OFF = NST * STAGE;
+    static constexpr int SMEM = BAR_OFF + 512;
+    static constexpr int THREADS = 288;                  // 8 transform warps, loads and MMAs
+};
+
+template <int D>
+struct DecStateBars {
+    uint64_t full[DecStateCfg<D>::NST], ready[DecStateCfg<D>::NST], done[DecStateCfg<D>::NST];
+    uint64_t mma_done;
+    uint32_t tmem_base;
+    int abort;
+};
+static_assert(sizeof(DecStateBars<64>) <= 512, "barrier block");
+
+struct DecayStateArgs {
+    CUtensorMap b[2], c[2];
+    float* border[2];
+    int back[2];
+    float w_scale[2];
+};
+
+// grid (segments x heads, kinds of state).  Forward in time the sum of segment
+// s goes to the border behind it, backwards that of segment s + 1.
+template <int D>
+__global__ void __launch_bounds__(DecStateCfg<D>::THREADS, 1)
+decay_state_kernel(const __grid_constant__ DecayStateArgs args, const DecayShape sh, const int32_t* __restrict__ cu,
+                   const float* __restrict__ log_decay, int* status) {
+    using C = DecStateCfg<D>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    if (smem_u32(smem) & 1023) {
+        if (threadIdx.x == 0) report(status, kStatusMisaligned);
+        return;
+    }
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int head = blockIdx.x % sh.heads, kind = blockIdx.y, back = args.back[kind];
+    const Segment g = find_segment(cu, sh, blockIdx.x / sh.heads, status);
+    if (g.seq < 0 || (back ? g.first : g.last)) return;
+    DecStateBars<D>* bars = reinterpret_cast<DecStateBars<D>*>(smem + C::BAR_OFF);
+    volatile int* abort_flag = &bars->abort;
+    if (tid == 0) {
+        bars->abort = 0;
+        for (int x = 0; x < C::NST; ++x) { mbar_init(&bars->full[x], 1); mbar_init(&bars->ready[x], 256); mbar_init(&bars->done[x], 1); }
+        mbar_init(&bars->mma_done, 1);
+        fence_barrier_init();
+    }
+    if (warp == 8) { tmem_alloc(&bars->tmem_base, 128); tmem_relinquish(); }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tbase = bars->tmem_base;
+    auto fail = [&]() { *abort_flag = 1; report(status, kStatusTimeout); };
+    const int n = (g.len + 63) / 64;
+    if (warp == 8) {
+        if (lane == 0) {
+            constexpr uint32_t id = idesc_bf16_f32(128, D, true, true);
+            int issued = 0;
+            auto load = [&](int t) {
+                uint8_t* st = smem + (t % C::NST) * C::STAGE;
+                uint64_t* bar = &bars->full[t % C::NST];
+                mbar_arrive_expect_tx(bar, 2 * C::TILE);
+                for (int c = 0; c < C::NCH; ++c) {
+                    tma_load_3d(st + c * C::CHUNK, &args.b[kind], bar, 64 * c, head, g.begin + 64 * t);
+                    tma_load_3d(st + C::TILE + c * C::CHUNK, &args.c[kind], bar, 64 * c, head, g.begin + 64 * t);
+                }
+                ++issued;
+            };
+            for (int t = 0; t < min(n, C::NST); ++t) load(t);
+            bool ok = true;
+            for (int t = 0; t < n && ok; ++t) {
+                // the stage of step t - 1 refills while step t's products run
+                if (!(ok = mma_wait(&bars->ready[t % C::NST], (t / C::NST) & 1, abort_flag))) break;
+                tc_fence_after();
+                const uint32_t s0 = smem_u32(smem + (t % C::NST) * C::STAGE);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {         // 16 tokens per MMA
+                    const uint64_t c = smem_desc_sw128(s0 + C::TILE + kk * 2048, C::CHUNK, 1024);
+                    if (D == 128) {
+                        mma_bf16_ss(tbase, smem_desc_sw128(s0 + kk * 2048, C::CHUNK, 1024), c, id, t > 0 || kk > 0);
+                        mma_bf16_ss(tbase, smem_desc_sw128(s0 + 2 * C::TILE + kk * 2048, C::CHUNK, 1024), c, id, 1);
+                    } else {
+                        mma_bf16_ss(tbase, smem_desc_sw128(s0 + kk * 2048, 2 * C::TILE, 1024), c, id, t > 0 || kk > 0);
+                    }
+                }
+                mma_commit(&bars->done[t % C::NST]);
+                if (t >= 1 && t - 1 + C::NST < n) {
+                    if (!(ok = mma_wait(&bars->done[(t - 1) % C::NST], ((t - 1) / C::NST) & 1, abort_flag))) break;
+                    load(t - 1 + C::NST);
+                }
+            }
+            if (!ok) {
+                fail();
+                for (int t = max(0, issued - C::NST); t < issued; ++t) wait_noabort(&bars->full[t % C::NST], (t / C::NST) & 1);
+            }
+            mma_commit(&bars->mma_done);
+            wait_noabort(&bars->mma_done, 0);
+        }
+    } else {
+        const float l2 = decay_log2(log_decay, head), w0 = args.w_scale[kind];
+        bool ok = true;
+        for (int t = 0; t < n; ++t) {
+            if (!__all_sync(0xffffffffu, mbar_wait(&bars->full[t % C::NST], (t / C::NST) & 1, abort_flag))) { ok = false; break; }
+            uint8_t* st = smem + (t % C::NST) * C::STAGE;
+#pragma unroll
+            for (int u = tid; u < C::TILE / 16; u += 256) {
+                const int r = 64 * t + (u & 511) / 8;    // token of the segment
+                uint4 x = *reinterpret_cast<const uint4*>(st + u * 16), lo;
+                if (r < g.len) {
+                    const float w = w0 * ex2((float)(back ? r + 1 : g.len - 1 - r) * l2);
+                    split_pair(x.x, w, x.x, lo.x);
+                    split_pair(x.y, w, x.y, lo.y);
+                    split_pair(x.z, w, x.z, lo.z);
+                    split_pair(x.w, w, x.w, lo.w);
+                } else {                                 // another sequence's rows
+                    x = lo = make_uint4(0, 0, 0, 0);
+                    *reinterpret_cast<uint4*>(st + C::TILE + u * 16) = x;
+                }
+                *reinterpret_cast<uint4*>(st + u * 16) = x;
+                *reinterpret_cast<uint4*>(st + 2 * C::TILE + u * 16) = lo;
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(&bars->ready[t % C::NST]);
+        }
+        if (ok && !__all_sync(0xffffffffu, mbar_wait(&bars->mma_done, 0, abort_flag))) ok = false;
+        if (!ok) fail();
+        tc_fence_after();
+        const int row = 32 * (warp & 3) + lane, hf = warp >> 2;   // feature of b (d = 64: of hi, lo), half of c's
+        const long long slot = (back ? g.begin - sh.seg : g.begin) / sh.seg;
+        float* dst = args.border[kind] + (slot * sh.heads + head) * D * D;
+        float x[D / 2];
+        if (ok) {
+#pragma unroll
+            for (int c = 0; c < D / 2; c += 32)
+                tmem_ld_32x32b_x32(tbase + ((uint32_t)(32 * (warp & 3)) << 16) + hf * (D / 2) + c, *reinterpret_cast<float(*)[32]>(&x[c]));
+            tmem_wait_ld();
+        }
+        if (D == 64) {
+            // every product has finished: stage 0 holds the lo part for the hi part's threads
+            float* half = reinterpret_cast<float*>(smem) + hf * 32 * 64 + (row & 63);
+            if (ok && row >= 64) {
+#pragma unroll
+                for (int c = 0; c < 32; ++c) half[c * 64] = x[c];
+            }
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+            if (ok && row < 64) {
+#pragma unroll
+                for (int c = 0; c < 32; ++c) x[c] += half[c * 64];
+            }
+        }
+        if (ok && row < D) {
+#pragma unroll
+            for (int c = 0; c < D / 2; c += 4)
+                *reinterpret_cast<float4*>(dst + (long long)row * D + hf * (D / 2) + c) = make_float4(x[c], x[c + 1], x[c + 2], x[c + 3]);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 8) tmem_dealloc(tbase, 128);
+}
+
+struct DecayScanArgs {
+    float* border[2];
+    const float* first[2];
+    int back[2];
+};
+
+// Border sums -> states at the borders, in place.  grid (sequences x heads,
+// D^2 / 1024, kinds of state), 4 elements per thread.
+template <int D>
+__global__ void __launch_bounds__(256)
+decay_scan_kernel(const DecayScanArgs args, const DecayShape sh, const int32_t* __restrict__ cu,
+                  const float* __restrict__ log_decay, int* status) {
+    const int head = blockIdx.x % sh.heads, seq = blockIdx.x / sh.heads, kind = blockIdx.z;
+    const SeqRange r = seq_range(cu, seq, sh.total, status);
+    const int n = (r.len + sh.seg - 1) / sh.seg - 1;     // borders
+    if (n < 1) return;
+    const int e = (blockIdx.y * 256 + threadIdx.x) * 4;
+    const float l2 = decay_log2(log_decay, head);
+    const int back = args.back[kind];
+    const float full = ex2((float)sh.seg * l2);
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (args.first[kind]) s = __ldg(reinterpret_cast<const float4*>(args.first[kind] + ((long long)seq * sh.heads + head) * D * D + e));
+    const int tail = r.len - n * sh.seg;                 // tokens of the last segment
+    float* base = args.border[kind] + (long long)head * D * D + e;
+    constexpr int AHEAD = 8;
+    for (int i0 = 0; i0 < n; i0 += AHEAD) {
+        float4 u[AHEAD];
+        float4* p[AHEAD];
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) {
+            const int b = back ? n - 1 - i0 - j : i0 + j;          // border b lies behind segment b
+            if (i0 + j < n) {
+                p[j] = reinterpret_cast<float4*>(base + ((long long)r.begin + (long long)b * sh.seg) / sh.seg * sh.heads * D * D);
+                u[j] = *p[j];
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) {
+            if (i0 + j >= n) break;
+            const float f = back && i0 + j == 0 ? ex2((float)tail * l2) : full;
+            s.x = fmaf(f, s.x, u[j].x); s.y = fmaf(f, s.y, u[j].y); s.z = fmaf(f, s.z, u[j].z); s.w = fmaf(f, s.w, u[j].w);
+            *p[j] = s;
+        }
+    }
+}
+
+// --------------------------------------------------------------------- outputs
+template <int D>
+struct DecOutCfg {
+    static constexpr int NCH = D / 64;
+    static constexpr int CHUNK = 128 * 128;              // 128 tokens of one 64-feature chunk
+    static constexpr int TILE = NCH * CHUNK;
+    static constexpr int NST = D == 128 ? 5 : 9;         // ring of operand tiles
+    static constexpr int LO_OFF = NST * TILE;            // lo part of the weighted operand (hi in its tile's place)
+    static constexpr int X_OFF = LO_OFF + TILE;          // the state as bf16: 128 rows (d = 64: hi rows, lo rows) x D
+    static constexpr int COL_OFF = X_OFF + TILE;         // lam^0 .. lam^31
+    static constexpr int BAR_OFF = COL_OFF + 128;
+    static constexpr int SMEM = BAR_OFF + 512;
+    static constexpr int THREADS = 448;                  // 4 score warps, 8 state warps, loads, MMAs
+    static constexpr int X_COL = 0, S_COL = 128, O1_COL = 256, O2_COL = 384;   // TMEM
+};
+static_assert(DecOutCfg<128>::SMEM <= 232448 && DecOutCfg<64>::SMEM <= 232448, "shared memory");
+
+template <int D>
+struct DecOutBars {
+    uint64_t full[DecOutCfg<D>::NST], empty[DecOutCfg<D>::NST];
+    uint64_t s_full, p_ready, x_ready, w_ready, o_full, x_done, mma_done;
+    uint32_t tmem_base;
+    int abort;
+};
+static_assert(sizeof(DecOutBars<64>) <= 512, "barrier block");
+
+// grid (segments x heads, passes)
+template <int D>
+__global__ void __launch_bounds__(DecOutCfg<D>::THREADS, 1)
+decay_out_kernel(const __grid_constant__ DecayPasses passes, const DecayShape sh, const int32_t* __restrict__ cu,
+                 const float* __restrict__ log_decay, int* status) {
+    using C = DecOutCfg<D>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    if (smem_u32(smem) & 1023) {
+        if (threadIdx.x == 0) report(status, kStatusMisaligned);
+        return;
+    }
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const DecayPass& ps = passes.p[blockIdx.y];
+    const int head = blockIdx.x % sh.heads;
+    const bool back = ps.back;
+    const Segment g = find_segment(cu, sh, blockIdx.x / sh.heads, status);
+    if (g.seq < 0) return;
+    const int n = (g.len + 127) / 128;                   // chunks; step t is chunk t, or n - 1 - t backwards
+    auto chunk_of = [&](int t) { return back ? n - 1 - t : t; };
+    const long long own = ((long long)g.seq * sh.heads + head) * D * D;
+    const bool ends = back ? g.first : g.last;           // this CTA reaches the end of the walk
+    float* last = ends && ps.last ? ps.last + own : nullptr;
+    const float* x0 = nullptr;                           // the state before step 0
+    if (back ? g.last : g.first) x0 = ps.first ? ps.first + own : nullptr;
+    else x0 = ps.border + ((long long)(back ? g.begin : g.begin - sh.seg) / sh.seg * sh.heads + head) * D * D;
+    if (n == 0) {                                        // an empty sequence: the state goes through
+        if (last)
+            for (int e = tid; e < D * D; e += C::THREADS) last[e] = x0 ? x0[e] : 0.f;
+        return;
+    }
+    const int updates = last ? n : n - 1;                // steps whose state is needed
+    uint8_t* ring = smem;
+    uint8_t* sLo = smem + C::LO_OFF;
+    uint8_t* sX = smem + C::X_OFF;
+    float* sCol = reinterpret_cast<float*>(smem + C::COL_OFF);
+    DecOutBars<D>* bars = reinterpret_cast<DecOutBars<D>*>(smem + C::BAR_OFF);
+    volatile int* abort_flag = &bars->abort;
+    const float l2 = decay_log2(log_decay, head);
+    if (tid == 0) {
+        bars->abort = 0;
+        for (int x = 0; x < C::NST; ++x) { mbar_init(&bars->full[x], 1); mbar_init(&bars->empty[x], 1); }
+        mbar_init(&bars->s_full, 1);
+        mbar_init(&bars->p_ready, 128);
+        mbar_init(&bars->x_ready, 256);
+        mbar_init(&bars->w_ready, 256);
+        mbar_init(&bars->o_full, 1);
+        mbar_init(&bars->x_done, 1);
+        mbar_init(&bars->mma_done, 1);
+        fence_barrier_init();
+    }
+    if (tid < 32) sCol[tid] = ex2((float)tid * l2);
+    if (warp == 13) { tmem_alloc(&bars->tmem_base, 512); tmem_relinquish(); }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tbase = bars->tmem_base;
+    auto fail = [&]() { *abort_flag = 1; report(status, kStatusTimeout); };
+    // ring items of step t: B, A, C at 3 t, 3 t + 1, 3 t + 2
+    auto slot = [&](int i) { return ring + (i % C::NST) * C::TILE; };
+    auto item_wait = [&](int i) { return mma_wait(&bars->full[i % C::NST], (i / C::NST) & 1, abort_flag); };
+
+    if (warp == 12) {
+        if (lane == 0) {
+            // ---------------------------------------------------------- loads
+            int issued = 0;
+            for (int i = 0; i < 3 * n; ++i) {
+                const int st = i % C::NST;
+                if (i >= C::NST && !mbar_wait(&bars->empty[st], (i / C::NST - 1) & 1, abort_flag)) { fail(); break; }
+                const CUtensorMap* map = i % 3 == 0 ? &ps.b : i % 3 == 1 ? &ps.a : &ps.c;
+                const int row = g.begin + 128 * chunk_of(i / 3);
+                mbar_arrive_expect_tx(&bars->full[st], C::TILE);
+                for (int c = 0; c < 2 * C::NCH; ++c)     // boxes of 64 tokens x 64 features
+                    tma_load_3d(slot(i) + c * 8192, map, &bars->full[st], 64 * (c >> 1), head, row + 64 * (c & 1));
+                ++issued;
+            }
+            if (*abort_flag)
+                for (int i = max(0, issued - C::NST); i < issued; ++i) wait_noabort(&bars->full[i % C::NST], (i / C::NST) & 1);
+        }
+    } else if (warp == 13) {
+        if (lane == 0) {
+            // ----------------------------------------------------------- MMAs
+            constexpr uint32_t id_s = idesc_bf16_f32(128, 128, false, false);
+            constexpr uint32_t id_o = idesc_bf16_f32(128, D, false, true);
+            constexpr uint32_t id_x = idesc_bf16_f32(128, D, true, true);
+            const uint32_t lo = smem_u32(sLo), xs = smem_u32(sX);
+            auto issue_s = [&](int t) {
+                if (!item_wait(3 * t) || !item_wait(3 * t + 1)) return false;
+                tc_fence_after();
+                const uint32_t b = smem_u32(slot(3 * t)), a = smem_u32(slot(3 * t + 1));
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t o = (kk >> 2) * C::CHUNK + (kk & 3) * 32;
+                    mma_bf16_ss(tbase + C::S_COL, smem_desc_sw128(a + o, 16, 1024), smem_desc_sw128(b + o, 16, 1024), id_s, kk > 0);
+                }
+                mma_commit(&bars->s_full);
+                return true;
+            };
+            bool ok = issue_s(0);
+            for (int t = 0; t < n && ok; ++t) {
+                const uint32_t b = smem_u32(slot(3 * t)), a = smem_u32(slot(3 * t + 1)), c = smem_u32(slot(3 * t + 2));
+                // O1 = P C (the score warps have read O1 and O2 of step t - 1 before they wrote P)
+                if (!(ok = mma_wait(&bars->p_ready, t & 1, abort_flag) && item_wait(3 * t + 2))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)
+                    mma_bf16_ts(tbase + C::O1_COL, tbase + C::S_COL + kk * 8, smem_desc_sw128(c + kk * 2048, C::CHUNK, 1024), id_o, kk > 0);
+                // O2 = A X
+                if (!(ok = mma_wait(&bars->x_ready, t & 1, abort_flag))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk) {         // d = 64: the features twice, over hi and lo rows
+                    const int f = kk % (D / 16);
+                    mma_bf16_ss(tbase + C::O2_COL, smem_desc_sw128(a + (f >> 2) * C::CHUNK + (f & 3) * 32, 16, 1024),
+                                smem_desc_sw128(xs + kk * 2048, C::CHUNK, 1024), id_o, kk > 0);
+                }
+                mma_commit(&bars->o_full);
+                mma_commit(&bars->empty[(3 * t + 1) % C::NST]);
+                if (t + 1 < n && !(ok = issue_s(t + 1))) break;
+                if (t < updates) {
+                    // X += (B w)^T C
+                    if (!(ok = mma_wait(&bars->w_ready, t & 1, abort_flag))) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk) {
+                        const uint64_t cd = smem_desc_sw128(c + kk * 2048, C::CHUNK, 1024);
+                        if (D == 128) {
+                            mma_bf16_ss(tbase + C::X_COL, smem_desc_sw128(b + kk * 2048, C::CHUNK, 1024), cd, id_x, 1);
+                            mma_bf16_ss(tbase + C::X_COL, smem_desc_sw128(lo + kk * 2048, C::CHUNK, 1024), cd, id_x, 1);
+                        } else {
+                            mma_bf16_ss(tbase + C::X_COL, smem_desc_sw128(b + kk * 2048, lo - b, 1024), cd, id_x, 1);
+                        }
+                    }
+                    mma_commit(&bars->x_done);
+                    mma_commit(&bars->empty[(3 * t) % C::NST]);
+                    mma_commit(&bars->empty[(3 * t + 2) % C::NST]);
+                }
+            }
+            if (!ok) fail();
+            mma_commit(&bars->mma_done);
+            wait_noabort(&bars->mma_done, 0);
+        }
+    } else if (warp < 4) {
+        // ------------------------------------------------- weights and outputs
+        const int r = tid;                               // token of the chunk
+        const uint32_t lanes = (uint32_t)(32 * warp) << 16;
+        const uint32_t tS = tbase + lanes + C::S_COL, tO1 = tbase + lanes + C::O1_COL, tO2 = tbase + lanes + C::O2_COL;
+        bool ok = true;
+        for (int t = 0; t < n; ++t) {
+            const int tok = 128 * chunk_of(t), rows = min(128, g.len - tok);
+            if (rows < 128) {
+                // C's rows behind the sequence are another one's: zeros
+                if (!__all_sync(0xffffffffu, item_wait(3 * t + 2))) { ok = false; break; }
+                uint8_t* c = slot(3 * t + 2);
+                for (int u = r; u < (128 - rows) * 8 * C::NCH; u += 128)
+                    *reinterpret_cast<uint4*>(c + (u % C::NCH) * C::CHUNK + rows * 128 + (u / C::NCH) * 16) = make_uint4(0, 0, 0, 0);
+                fence_proxy_async_smem();
+            }
+            if (!__all_sync(0xffffffffu, mbar_wait(&bars->s_full, t & 1, abort_flag))) { ok = false; break; }
+            tc_fence_after();
+            // P over the scores: 32 columns at a time.  Away from the diagonal
+            // lam^|i-j| is lam^(to the block's near end) lam^(within the block),
+            // both factors at most 1.
+#pragma unroll 1
+            for (int blk = 0; blk < 4; ++blk) {
+                uint32_t pk[16];
+                if (blk == warp) {
+                    float s[32];
+                    tmem_ld_32x32b_x32(tS + 32 * blk, s);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        const int dist = back ? e - lane : lane - e;
+                        s[e] = dist >= 0 && 32 * blk + e < rows ? s[e] * ps.p_scale * ex2((float)dist * l2) : 0.f;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) pk[e] = pack_bf16x2(s[2 * e], s[2 * e + 1]);
+                } else if (back ? blk > warp : blk < warp) {
+                    float s[32];
+                    tmem_ld_32x32b_x32(tS + 32 * blk, s);
+                    tmem_wait_ld();
+                    const float f = ps.p_scale * ex2((float)(back ? 32 * blk - r : r - 32 * blk - 31) * l2);
+                    if (back) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) s[e] = 32 * blk + e < rows ? s[e] * (f * sCol[e]) : 0.f;
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) s[e] *= f * sCol[31 - e];
+                    }
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) pk[e] = pack_bf16x2(s[2 * e], s[2 * e + 1]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) pk[e] = 0;
+                }
+                // the packed columns of block blk lie in the scores of block blk / 2, which are read
+                tmem_st_32x32b_x16(tS + 16 * blk, pk);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(&bars->p_ready);
+            if (!__all_sync(0xffffffffu, mbar_wait(&bars->o_full, t & 1, abort_flag))) { ok = false; break; }
+            tc_fence_after();
+            const float f = ps.s_scale * ex2((float)(back ? rows - 1 - r : r + 1) * l2);
+            __nv_bfloat16* po = ps.out + (long long)(g.begin + tok + r) * ps.out_stride + (long long)head * D;
+#pragma unroll
+            for (int c = 0; c < D; c += 32) {
+                float o[32], x[32];
+                tmem_ld_32x32b_x32(tO1 + c, o);
+                tmem_ld_32x32b_x32(tO2 + c, x);
+                tmem_wait_ld();
+                if (r < rows) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = fmaf(f, x[e], o[e]);
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8)
+                        *reinterpret_cast<uint4*>(po + c + e) = make_uint4(pack_bf16x2(o[e], o[e + 1]), pack_bf16x2(o[e + 2], o[e + 3]),
+                                                                           pack_bf16x2(o[e + 4], o[e + 5]), pack_bf16x2(o[e + 6], o[e + 7]));
+                }
+            }
+            tc_fence_before();                           // before the next P lets O1 and O2 be written again
+        }
+        if (!ok) fail();
+    } else {
+        // ---------------------------------------------------------- the state
+        const int id = tid - 128, hf = id >> 7;          // half of the columns
+        const int row = id & 127;                        // TMEM lane
+        const int feat = row & (D - 1);
+        const uint32_t tX = tbase + ((uint32_t)(32 * (warp & 3)) << 16) + C::X_COL + hf * (D / 2);
+        bool ok = true;
+        float x[D / 2];
+        if (x0 && row < D) {
+#pragma unroll
+            for (int c = 0; c < D / 2; c += 4) {
+                const int col = hf * (D / 2) + c;
+                if (ps.trans) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[c + e] = __ldg(x0 + (long long)(col + e) * D + feat);
+                } else {
+                    const float4 y = __ldg(reinterpret_cast<const float4*>(x0 + (long long)feat * D + col));
+                    x[c] = y.x; x[c + 1] = y.y; x[c + 2] = y.z; x[c + 3] = y.w;
+                }
+            }
+        } else {
+#pragma unroll
+            for (int c = 0; c < D / 2; ++c) x[c] = 0.f;
+        }
+        for (int t = 0; t < n; ++t) {
+            const int tok = 128 * chunk_of(t), rows = min(128, g.len - tok);
+            if (t > 0) {
+                // products of step t - 1 and the scores of step t have finished
+                if (!__all_sync(0xffffffffu, mbar_wait(&bars->x_done, (t - 1) & 1, abort_flag))) { ok = false; break; }
+                tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < D / 2; c += 32) tmem_ld_32x32b_x32(tX + c, *reinterpret_cast<float(*)[32]>(&x[c]));
+                tmem_wait_ld();
+            }
+            uint8_t* xr = sX + row * 128;
+#pragma unroll
+            for (int c = 0; c < D / 2; c += 8) {
+                const int col = hf * (D / 2) + c;
+                *reinterpret_cast<uint4*>(xr + (col >> 6) * C::CHUNK + ((((col & 63) >> 3) ^ (row & 7)) << 4)) =
+                    make_uint4(pack_bf16x2(x[c], x[c + 1]), pack_bf16x2(x[c + 2], x[c + 3]), pack_bf16x2(x[c + 4], x[c + 5]),
+                               pack_bf16x2(x[c + 6], x[c + 7]));
+            }
+            if (t < updates) {
+                const float f = ex2((float)rows * l2);
+#pragma unroll
+                for (int c = 0; c < D / 2; ++c) x[c] *= f;
+#pragma unroll
+                for (int c = 0; c < D / 2; c += 32) tmem_st_32x32b_x32f(tX + c, *reinterpret_cast<float(*)[32]>(&x[c]));
+                tmem_wait_st();
+            }
+            if (t == 0 && !__all_sync(0xffffffffu, mbar_wait(&bars->s_full, 0, abort_flag))) { ok = false; break; }
+            tc_fence_before();
+            fence_proxy_async_smem();
+            mbar_arrive(&bars->x_ready);
+            if (t < updates) {
+                if (!__all_sync(0xffffffffu, item_wait(3 * t))) { ok = false; break; }   // (done: its scores are)
+                uint8_t* b = slot(3 * t);
+#pragma unroll
+                for (int u = id; u < C::TILE / 16; u += 256) {
+                    const int r = (u & 1023) / 8;        // token of the chunk
+                    uint4 y = *reinterpret_cast<const uint4*>(b + u * 16), lo;
+                    if (r < rows) {
+                        const float w = ps.w_scale * ex2((float)(back ? r + 1 : rows - 1 - r) * l2);
+                        split_pair(y.x, w, y.x, lo.x);
+                        split_pair(y.y, w, y.y, lo.y);
+                        split_pair(y.z, w, y.z, lo.z);
+                        split_pair(y.w, w, y.w, lo.w);
+                    } else {
+                        y = lo = make_uint4(0, 0, 0, 0);
+                    }
+                    *reinterpret_cast<uint4*>(b + u * 16) = y;
+                    *reinterpret_cast<uint4*>(sLo + u * 16) = lo;
+                }
+                fence_proxy_async_smem();
+                mbar_arrive(&bars->w_ready);
+            }
+        }
+        if (last) {
+            if (ok && !__all_sync(0xffffffffu, mbar_wait(&bars->x_done, (n - 1) & 1, abort_flag))) ok = false;
+            tc_fence_after();
+            if (ok) {
+#pragma unroll
+                for (int c = 0; c < D / 2; c += 32) tmem_ld_32x32b_x32(tX + c, *reinterpret_cast<float(*)[32]>(&x[c]));
+                tmem_wait_ld();
+            }
+            if (D == 64) {
+                // the last products have finished: the bf16 state's place holds the lo part for the hi part's threads
+                float* half = reinterpret_cast<float*>(sX) + hf * 32 * 64 + feat;
+                if (ok && row >= 64) {
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) half[c * 64] = x[c];
+                }
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+                if (ok && row < 64) {
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) x[c] += half[c * 64];
+                }
+            }
+            if (ok && row < D) {
+#pragma unroll
+                for (int c = 0; c < D / 2; c += 4) {
+                    const int col = hf * (D / 2) + c;
+                    if (ps.trans) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) last[(long long)(col + e) * D + feat] = x[c + e];
+                    } else {
+                        *reinterpret_cast<float4*>(last + (long long)feat * D + col) = make_float4(x[c], x[c + 1], x[c + 2], x[c + 3]);
+                    }
+                }
+            }
+        }
+        if (!ok) fail();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 13) tmem_dealloc(tbase, 512);
+}
+
+// --------------------------------------------------------------------- launch
+
+// Chunks of a segment for `walks` scans (heads x passes) over the sequences,
+// whose lengths only the device knows: the m that makes ceil(CTAs / 148)
+// rounds of m chunks (and the launch's fixed part) shortest, all in one
+// sequence assumed.
+static int segment_chunks(int total, int n_seq, long long walks) {
+    const long long chunks = std::max(1ll, ((long long)total + 127) / 128);
+    long long best = chunks;
+    double best_cost = 1e300;
+    for (long long m = 1; m <= chunks; m = m < 64 ? m + 1 : m + m / 32) {
+        const long long segs = (chunks + m - 1) / m + (n_seq - 1);
+        const double rounds = (double)((segs * walks + 147) / 148);
+        const double cost = rounds * (m + 2.0) + (m < chunks ? 4.0 : 0.0);
+        if (cost < best_cost) { best_cost = cost; best = m; }
+    }
+    return (int)best;
+}
+
+static DecayShape decay_shape(int n_seq, int total, int heads, int passes) {
+    return {n_seq, total, heads, 128 * segment_chunks(total, n_seq, (long long)heads * passes)};
+}
+
+static long long decay_segments(const DecayShape& s) { return (long long)s.total / s.seg + s.n_seq; }
+
+static size_t border_bytes(const DecayShape& s, int d) { return (size_t)(s.total / s.seg) * s.heads * d * d * sizeof(float); }
+
+long long decay_work_items(int n_seq, int total, int heads) { return ((long long)total / 128 + n_seq) * heads; }
+
+size_t decay_scratch_bytes(int n_seq, int total, int heads, int d) {
+    return std::max(border_bytes(decay_shape(n_seq, total, heads, 1), d), 2 * border_bytes(decay_shape(n_seq, total, heads, 3), d));
+}
+
+static bool decay_map(CUtensorMap* m, const PackedTensor& t, const DecayArgs& a) {
+    return a.total == 0 || encode_packed_map(m, t, a.total, a.heads, a.d, 1, 64, a.enc);
+}
+
+template <int D>
+static cudaError_t launch_decay(const DecayArgs& a, const DecayShape& sh, const DecayPasses& passes, int n_passes,
+                                const DecayStateArgs& st, const DecayScanArgs& sc, int kinds, cudaStream_t stream) {
+    const unsigned items = (unsigned)(decay_segments(sh) * a.heads);
+    cudaError_t e = cudaFuncSetAttribute(decay_out_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, DecOutCfg<D>::SMEM);
+    if (e != cudaSuccess) return e;
+    if (a.total > sh.seg) {                              // some sequence may have several segments
+        e = cudaFuncSetAttribute(decay_state_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, DecStateCfg<D>::SMEM);
+        if (e != cudaSuccess) return e;
+        decay_state_kernel<D><<<dim3(items, kinds), DecStateCfg<D>::THREADS, DecStateCfg<D>::SMEM, stream>>>(st, sh, a.cu, a.log_decay, a.status);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        decay_scan_kernel<D><<<dim3((unsigned)((long long)a.n_seq * a.heads), D * D / 1024, kinds), 256, 0, stream>>>(sc, sh, a.cu, a.log_decay, a.status);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
+    decay_out_kernel<D><<<dim3(items, n_passes), DecOutCfg<D>::THREADS, DecOutCfg<D>::SMEM, stream>>>(passes, sh, a.cu, a.log_decay, a.status);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_decay_fwd(const DecayArgs& a, cudaStream_t stream) {
+    const DecayShape sh = decay_shape(a.n_seq, a.total, a.heads, 1);
+    float* border = reinterpret_cast<float*>(a.scratch);
+    DecayPasses ps{};
+    DecayStateArgs st{};
+    DecayPass& p = ps.p[0];
+    if (!decay_map(&p.a, a.q, a) || !decay_map(&p.b, a.k, a) || !decay_map(&p.c, a.v, a)) return cudaErrorInvalidValue;
+    p.out = static_cast<__nv_bfloat16*>(a.out.p);
+    p.out_stride = a.out.stride;
+    p.first = a.state_in;
+    p.last = a.state_out;
+    p.border = border;
+    p.w_scale = 1.f;
+    p.p_scale = p.s_scale = a.scale;
+    st.b[0] = p.b;
+    st.c[0] = p.c;
+    st.border[0] = border;
+    st.w_scale[0] = 1.f;
+    DecayScanArgs sc{};
+    sc.border[0] = border;
+    sc.first[0] = a.state_in;
+    return a.d == 128 ? launch_decay<128>(a, sh, ps, 1, st, sc, 1, stream) : launch_decay<64>(a, sh, ps, 1, st, sc, 1, stream);
+}
+
+cudaError_t launch_decay_bwd(const DecayArgs& a, cudaStream_t stream) {
+    const DecayShape sh = decay_shape(a.n_seq, a.total, a.heads, 3);
+    float* border[2] = {reinterpret_cast<float*>(a.scratch), reinterpret_cast<float*>(a.scratch + border_bytes(sh, a.d))};
+    CUtensorMap mq, mk, mv, mg;
+    if (!decay_map(&mq, a.q, a) || !decay_map(&mk, a.k, a) || !decay_map(&mv, a.v, a) || !decay_map(&mg, a.dout, a))
+        return cudaErrorInvalidValue;
+    auto pass = [&](const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mc, const PackedTensor& out, bool back, bool trans) {
+        DecayPass p{};
+        p.a = ma; p.b = mb; p.c = mc;
+        p.out = static_cast<__nv_bfloat16*>(out.p);
+        p.out_stride = out.stride;
+        p.first = back ? a.dstate_out : a.state_in;
+        p.border = border[back];
+        p.back = back;
+        p.trans = trans;
+        // backwards the state is the gradient of S, which has the scale in it
+        p.w_scale = back ? a.scale : 1.f;
+        p.p_scale = a.scale;
+        p.s_scale = back ? 1.f : a.scale;
+        return p;
+    };
+    DecayPasses ps{};
+    ps.p[0] = pass(mg, mv, mk, a.dq, false, true);
+    ps.p[1] = pass(mv, mg, mq, a.dk, true, true);
+    ps.p[2] = pass(mk, mq, mg, a.dv, true, false);
+    ps.p[2].last = a.dstate_in;
+    DecayStateArgs st{};
+    st.b[0] = mk; st.c[0] = mv; st.w_scale[0] = 1.f;
+    st.b[1] = mq; st.c[1] = mg; st.w_scale[1] = a.scale;
+    DecayScanArgs sc{};
+    sc.first[0] = a.state_in;
+    sc.first[1] = a.dstate_out;
+    for (int i = 0; i < 2; ++i) st.border[i] = sc.border[i] = border[i], st.back[i] = sc.back[i] = i;
+    return a.d == 128 ? launch_decay<128>(a, sh, ps, 3, st, sc, 2, stream) : launch_decay<64>(a, sh, ps, 3, st, sc, 2, stream);
+}
+
+}  // namespace vsa

@@ -1,0 +1,78 @@
+// decay_step.cu -- recurrent form of the linear attention with a decay per
+// head (decay_attn.cu): one new token for each sequence,
+//     S = lam S + k^T v,     o = scale q S,
+// in fp32 but for the bf16 inputs and output.
+//
+// The work is reading and writing S once (8 d^2 bytes against 5 d^2 flops):
+// one CTA per sequence and head, 256 threads with four columns each and d/8
+// (d = 128) or d/16 (d = 64) rows, all of whose loads are issued before the
+// first is used; o is summed over a thread's rows in registers and over the
+// CTA's row groups in shared memory (a fixed order).
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "common.cuh"
+#include "packed.h"
+
+namespace vsa {
+
+template <int D>
+__global__ void __launch_bounds__(256)
+decay_step_kernel(const PackedTensor q, const PackedTensor k, const PackedTensor v, const PackedTensor out,
+                  const float* __restrict__ log_decay, const float* state, float* state_out, const int heads,
+                  const float scale) {
+    constexpr int TPR = D / 4;                  // threads per row
+    constexpr int GROUPS = 256 / TPR;           // rows per pass
+    constexpr int ROWS = D / GROUPS;            // rows of a thread
+    __shared__ float4 part[GROUPS][TPR];
+    const int head = blockIdx.x % heads;
+    const long long b = blockIdx.x / heads;
+    const int c = threadIdx.x % TPR * 4, g = threadIdx.x / TPR;
+    const long long base = (long long)blockIdx.x * D * D + c;
+    float4 s[ROWS];
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) s[i] = *reinterpret_cast<const float4*>(state + base + (long long)(g + GROUPS * i) * D);
+    auto row = [&](const PackedTensor& t) { return static_cast<const __nv_bfloat16*>(t.p) + b * t.stride + (long long)head * D; };
+    const uint2 vr = __ldg(reinterpret_cast<const uint2*>(row(v) + c));
+    const float v0 = __uint_as_float(vr.x << 16), v1 = __uint_as_float(vr.x & 0xffff0000u);
+    const float v2 = __uint_as_float(vr.y << 16), v3 = __uint_as_float(vr.y & 0xffff0000u);
+    const float lam = expf(__ldg(log_decay + head));
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        const int a = g + GROUPS * i;
+        const float ka = __bfloat162float(row(k)[a]), qa = __bfloat162float(row(q)[a]);
+        s[i].x = fmaf(s[i].x, lam, ka * v0);
+        s[i].y = fmaf(s[i].y, lam, ka * v1);
+        s[i].z = fmaf(s[i].z, lam, ka * v2);
+        s[i].w = fmaf(s[i].w, lam, ka * v3);
+        *reinterpret_cast<float4*>(state_out + base + (long long)a * D) = s[i];
+        o.x = fmaf(qa, s[i].x, o.x);
+        o.y = fmaf(qa, s[i].y, o.y);
+        o.z = fmaf(qa, s[i].z, o.z);
+        o.w = fmaf(qa, s[i].w, o.w);
+    }
+    part[g][threadIdx.x % TPR] = o;
+    __syncthreads();
+    if (g == 0) {
+#pragma unroll
+        for (int i = 1; i < GROUPS; ++i) {
+            const float4 p = part[i][threadIdx.x % TPR];
+            o.x += p.x; o.y += p.y; o.z += p.z; o.w += p.w;
+        }
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(out.p) + b * out.stride + (long long)head * D + c) =
+            make_uint2(pack_bf16x2(o.x * scale, o.y * scale), pack_bf16x2(o.z * scale, o.w * scale));
+    }
+}
+
+cudaError_t launch_decay_step(const DecayStepArgs& a, cudaStream_t stream) {
+    const unsigned n = (unsigned)((long long)a.batch * a.heads);
+    if (a.d == 128)
+        decay_step_kernel<128><<<n, 256, 0, stream>>>(a.q, a.k, a.v, a.out, a.log_decay, a.state, a.state_out, a.heads, a.scale);
+    else
+        decay_step_kernel<64><<<n, 256, 0, stream>>>(a.q, a.k, a.v, a.out, a.log_decay, a.state, a.state_out, a.heads, a.scale);
+    return cudaGetLastError();
+}
+
+}  // namespace vsa

@@ -34,11 +34,12 @@ struct SeqTile {
     int tile;    // tile within the sequence
 };
 
-// Tile t of the tiles of `len` rows that the sequences are cut into, sequence
-// after sequence (whole warp; every lane gets the result).  Four sequences per
-// lane and step: one round trip to L2 covers 128 sequences.
+// Tile t of the tiles of `len` rows that the sequences are cut into (`least`
+// for an empty one), sequence after sequence (whole warp; every lane gets the
+// result).  Four sequences per lane and step: one round trip to L2 covers 128
+// sequences.
 __device__ __forceinline__ SeqTile find_tile(const int32_t* __restrict__ cu, int n_seq, int total, int len, int t,
-                                             int* status) {
+                                             int* status, int least = 0) {
     const int lane = threadIdx.x & 31;
     long long base = 0;            // 64 bits: borders that overlap can sum to more than the rows
     for (int s0 = 0; s0 < n_seq; s0 += 128) {
@@ -48,7 +49,7 @@ __device__ __forceinline__ SeqTile find_tile(const int32_t* __restrict__ cu, int
         for (int e = 0; e < 4; ++e) {
             const int s = s0 + 4 * lane + e;
             cnt[e] = 0;
-            if (s < n_seq) cnt[e] = (seq_range(cu, s, total, status).len + len - 1) / len;
+            if (s < n_seq) cnt[e] = max(least, (seq_range(cu, s, total, status).len + len - 1) / len);
             sum += cnt[e];
         }
         long long incl = sum;

@@ -58,15 +58,26 @@ struct DecayArgs {
     const float* dstate_out;     // or null
     float* dstate_in;            // or null
     float scale;
-    uint8_t* scratch;
+    uint8_t* scratch;            // behind the workspace's status block
     int* status;
     PFN_cuTensorMapEncodeTiled_v12000 enc;
 };
 
+long long decay_work_items(int n_seq, int total, int heads);   // CTAs of the largest launch, at most 2^31 - 1
 size_t decay_scratch_bytes(int n_seq, int total, int heads, int d);
 cudaError_t launch_decay_fwd(const DecayArgs& a, cudaStream_t stream);
 cudaError_t launch_decay_bwd(const DecayArgs& a, cudaStream_t stream);
-cudaError_t launch_decay_step(const DecayArgs& a, int batch, const float* state, float* state_out,
-                              cudaStream_t stream);
+
+// One token per sequence: q, k, v, out [batch][heads][d], states [batch][heads][d][d].
+struct DecayStepArgs {
+    int batch, heads, d;
+    PackedTensor q, k, v, out;
+    const float* log_decay;
+    const float* state;
+    float* state_out;            // may be `state`
+    float scale;
+};
+
+cudaError_t launch_decay_step(const DecayStepArgs& a, cudaStream_t stream);
 
 }  // namespace vsa

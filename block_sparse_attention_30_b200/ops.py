@@ -237,6 +237,54 @@ def vsa_packed_attn_bwd(q, k, v, out_f32, dout, cu_q, cu_k, lse, dq, dk, dv, wor
             _stream(stream)))
 
 
+def vsa_decay_attn_workspace_bytes(total, n_seq, heads, head_dim) -> int:
+    return _lib.lib().vsa_decay_attn_workspace_bytes(total, n_seq, heads, head_dim)
+
+
+def vsa_decay_attn_fwd(q, k, v, log_decay, cu, out, workspace, scale=None, state_in=None, state_out=None, stream=None):
+    """Causal linear attention with a decay per head over packed sequences:
+    S_t = exp(log_decay) S_(t-1) + k_t^T v_t, out_t = scale q_t S_t.
+
+    q, k, v, out: bf16 [total, heads, d] (rows may be strided); log_decay: fp32
+    [heads]; cu: int32 borders; state_in, state_out (optional): fp32 [n_seq,
+    heads, d, d], the states before and after each sequence.  scale: 1/sqrt(d)
+    if not given."""
+    (t, h, d), n = q.shape, _borders(cu)[1]
+    st = (n, h, d, d)
+    with _same_device(q, k, v, log_decay, cu, out, workspace, state_in, state_out):
+        _lib.check("vsa_decay_attn_fwd", _lib.lib().vsa_decay_attn_fwd(
+            *_rows(q), *_rows(k, h, d, t), *_rows(v, h, d, t), _f32(log_decay, (h,)), cu.data_ptr(), _f32(state_in, st),
+            _f32(state_out, st), *_rows(out, h, d, t), d ** -0.5 if scale is None else scale, t, n, h, d,
+            workspace.data_ptr(), workspace.numel(), _stream(stream)))
+
+
+def vsa_decay_attn_bwd(q, k, v, dout, log_decay, cu, dq, dk, dv, workspace, scale=None, state_in=None, dstate_out=None,
+                       dstate_in=None, stream=None):
+    """Gradients of vsa_decay_attn_fwd, written into dq, dk, dv (bf16) and, if
+    given, dstate_in (fp32); dstate_out: the gradient of the states after each
+    sequence, if there is one.  The decays are constants."""
+    (t, h, d), n = q.shape, _borders(cu)[1]
+    st = (n, h, d, d)
+    with _same_device(q, k, v, dout, log_decay, cu, dq, dk, dv, workspace, state_in, dstate_out, dstate_in):
+        _lib.check("vsa_decay_attn_bwd", _lib.lib().vsa_decay_attn_bwd(
+            *_rows(q), *_rows(k, h, d, t), *_rows(v, h, d, t), *_rows(dout, h, d, t), _f32(log_decay, (h,)), cu.data_ptr(),
+            _f32(state_in, st), _f32(dstate_out, st), *_rows(dq, h, d, t), *_rows(dk, h, d, t), *_rows(dv, h, d, t),
+            _f32(dstate_in, st), d ** -0.5 if scale is None else scale, t, n, h, d, workspace.data_ptr(),
+            workspace.numel(), _stream(stream)))
+
+
+def vsa_decay_attn_step(q, k, v, log_decay, state, out, scale=None, state_out=None, stream=None):
+    """One new token for each of the sequences: q, k, v, out bf16 [batch, heads,
+    d], state fp32 [batch, heads, d, d], updated in place or into state_out."""
+    n, h, d = q.shape
+    state_out = state if state_out is None else state_out
+    with _same_device(q, k, v, log_decay, state, state_out, out):
+        _lib.check("vsa_decay_attn_step", _lib.lib().vsa_decay_attn_step(
+            *_rows(q), *_rows(k, h, d, n), *_rows(v, h, d, n), _f32(log_decay, (h,)), _f32(state, (n, h, d, d)),
+            _f32(state_out, (n, h, d, d)), *_rows(out, h, d, n), d ** -0.5 if scale is None else scale, n, h, d,
+            _stream(stream)))
+
+
 def vsa_device_status(workspace, stream=None) -> int:
     """Synchronise and return the device status code (0 = VSA_OK)."""
     return _lib.lib().vsa_device_status(workspace.data_ptr(), _stream(stream))

@@ -336,6 +336,54 @@ vsa_status vsa_packed_attn_bwd(const vsa_bf16* q, long long q_stride, const vsa_
                                int head_dim, int causal, void* workspace, size_t workspace_bytes,
                                vsa_stream_t stream);
 
+/* Bytes of workspace vsa_decay_attn_fwd and vsa_decay_attn_bwd need for these
+ * shapes: the status block and the fp32 states at the borders of segments
+ * that long sequences are cut into.  0 for invalid shapes. */
+size_t vsa_decay_attn_workspace_bytes(int total, int n_seq, int heads, int head_dim);
+
+/* Causal linear attention with a decay per head over packed sequences.  For
+ * each sequence and head, with lam = exp(log_decay[head]) (log_decay <= 0,
+ * -inf for no memory at all) and S starting as state_in:
+ *     S_t = lam S_(t-1) + k_t^T v_t,   out_t = scale q_t S_t
+ * (the mask j <= t with weights lam^(t-j), computed in chunks of 128 tokens).
+ * state_in, state_out: fp32 [n_seq][heads][d][d] (row: feature of k, column:
+ * feature of v), the states before each sequence's first and after its last
+ * token; either may be NULL (zeros; not written); they must not overlap.  A
+ * sequence without tokens passes its state through.  States are fp32
+ * throughout (their update splits k, times its decay, into bf16 hi + lo);
+ * scores times their decays, and the state as the operand of q S, are rounded
+ * to bf16. */
+vsa_status vsa_decay_attn_fwd(const vsa_bf16* q, long long q_stride, const vsa_bf16* k, long long k_stride,
+                              const vsa_bf16* v, long long v_stride, const float* log_decay, const int32_t* cu,
+                              const float* state_in, float* state_out, vsa_bf16* out, long long out_stride,
+                              float scale, int total, int n_seq, int heads, int head_dim, void* workspace,
+                              size_t workspace_bytes, vsa_stream_t stream);
+
+/* Gradients of vsa_decay_attn_fwd, the decays being constants: dout is the
+ * gradient of out, dstate_out (or NULL: zeros) that of state_out; dstate_in
+ * (or NULL) receives that of state_in.  With R_t the gradient of S_t, backwards
+ * in time R_t = lam R_(t+1) + scale q_t^T dout_t (R_last = dstate_out + its term),
+ *     dq_t = scale S_t dout_t,  dk_t = R_t v_t,  dv_t = k_t R_t,
+ *     dstate_in = lam R_first (dstate_out, for a sequence without tokens).
+ * Sums are fp32 in a fixed order: the same call gives the same bits.  dq, dk,
+ * dv, dstate_in must not overlap the inputs or one another. */
+vsa_status vsa_decay_attn_bwd(const vsa_bf16* q, long long q_stride, const vsa_bf16* k, long long k_stride,
+                              const vsa_bf16* v, long long v_stride, const vsa_bf16* dout, long long dout_stride,
+                              const float* log_decay, const int32_t* cu, const float* state_in,
+                              const float* dstate_out, vsa_bf16* dq, long long dq_stride, vsa_bf16* dk,
+                              long long dk_stride, vsa_bf16* dv, long long dv_stride, float* dstate_in, float scale,
+                              int total, int n_seq, int heads, int head_dim, void* workspace,
+                              size_t workspace_bytes, vsa_stream_t stream);
+
+/* The recurrent form: one new token for each of `batch` sequences.  q, k, v,
+ * out: bf16 [batch][heads][d] (rows `*_stride` apart as above); state, state_out:
+ * fp32 [batch][heads][d][d], state_out == state updates in place (any other
+ * overlap is not allowed).  Needs no workspace. */
+vsa_status vsa_decay_attn_step(const vsa_bf16* q, long long q_stride, const vsa_bf16* k, long long k_stride,
+                               const vsa_bf16* v, long long v_stride, const float* log_decay, const float* state,
+                               float* state_out, vsa_bf16* out, long long out_stride, float scale, int batch,
+                               int heads, int head_dim, vsa_stream_t stream);
+
 /* Self-test of the device failure path (no counterpart on the pages): a
  * one-warp kernel waits on a barrier nobody arrives at, gives up after
  * `limit_cycles` SM clock cycles exactly as the library's kernels do, and
