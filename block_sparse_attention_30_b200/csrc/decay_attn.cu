@@ -20,20 +20,20 @@
 //                       one GEMM with the tokens as its inner dimension;
 //   decay_scan_kernel   the states at the borders, border after border;
 //   decay_out_kernel    one CTA per segment and head walks its chunks with the
-//                       state in TMEM: per chunk
+//                       state in registers: per chunk
 //                         scores A B^T, times lam^|i-j|, as bf16 P;
 //                         O1 = P C, O2 = A X, out = O1 + lam^(..) O2;
-//                         X = lam^128 X + (B w)^T C.
+//                         U = (B w)^T C, X = lam^128 X + U.
 // Sequences of one segment need the last launch alone.
 //
-// The state is fp32 throughout (TMEM, scratch, outputs).  The weighted operand
+// The state is fp32 throughout (registers, scratch, outputs).  The weighted operand
 // of its update is split into bf16 hi + lo (2^-17 relative), so the update is
 // good to about fp32; the state is rounded to bf16 only as the operand of A X
 // and P only as the operand of P C (2^-8 relative at most, as much as
 // the rounding of the output).
 //
 // At d = 64 hi and lo are the two halves of one M = 128 operand: the state's
-// hi part lies in TMEM lanes 0-63 and its lo part in lanes 64-127, A X runs
+// hi part belongs to TMEM lanes 0-63 and its lo part to lanes 64-127, A X runs
 // over both, and they are added when the state leaves the kernel.
 #include <algorithm>
 #include <cmath>
@@ -105,6 +105,34 @@ __device__ __forceinline__ void split_pair(uint32_t x, float w, uint32_t& hi, ui
     lo = pack_bf16x2(x0 - __uint_as_float(hi << 16), x1 - __uint_as_float(hi & 0xffff0000u));
 }
 
+__device__ __forceinline__ void split8(uint4& x, float w, uint4& lo) {
+    split_pair(x.x, w, x.x, lo.x);
+    split_pair(x.y, w, x.y, lo.y);
+    split_pair(x.z, w, x.z, lo.z);
+    split_pair(x.w, w, x.w, lo.w);
+}
+
+// Four lanes with four 16-byte units of a row each -> unit (lane & 3) of each
+// of the four rows, so that their stores fill 64 bytes of a row together.
+__device__ __forceinline__ void transpose_units(uint4 (&u)[4], int lane) {
+    uint32_t* x = reinterpret_cast<uint32_t*>(u);
+#pragma unroll
+    for (int m = 2; m > 0; m >>= 1) {
+        const bool up = lane & m;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i & m) continue;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                uint32_t &a = x[4 * i + e], &b = x[4 * (i + m) + e];
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? a : b, m);
+                if (up) a = got;
+                else b = got;
+            }
+        }
+    }
+}
+
 // ---------------------------------------------------------------- border sums
 template <int D>
 struct DecStateCfg {
@@ -146,7 +174,7 @@ decay_state_kernel(const __grid_constant__ DecayStateArgs args, const DecayShape
         if (threadIdx.x == 0) report(status, kStatusMisaligned);
         return;
     }
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = warp_uniform(tid >> 5), lane = tid & 31;
     const int head = blockIdx.x % sh.heads, kind = blockIdx.y, back = args.back[kind];
     const Segment g = find_segment(cu, sh, blockIdx.x / sh.heads, status);
     if (g.seq < 0 || (back ? g.first : g.last)) return;
@@ -162,11 +190,11 @@ decay_state_kernel(const __grid_constant__ DecayStateArgs args, const DecayShape
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tbase = bars->tmem_base;
+    const uint32_t tbase = warp_uniform(bars->tmem_base);
     auto fail = [&]() { *abort_flag = 1; report(status, kStatusTimeout); };
-    const int n = (g.len + 63) / 64;
+    const int n = warp_uniform((g.len + 63) / 64);
     if (warp == 8) {
-        if (lane == 0) {
+        if (elect_one()) {
             constexpr uint32_t id = idesc_bf16_f32(128, D, true, true);
             int issued = 0;
             auto load = [&](int t) {
@@ -220,11 +248,7 @@ decay_state_kernel(const __grid_constant__ DecayStateArgs args, const DecayShape
                 const int r = 64 * t + (u & 511) / 8;    // token of the segment
                 uint4 x = *reinterpret_cast<const uint4*>(st + u * 16), lo;
                 if (r < g.len) {
-                    const float w = w0 * ex2((float)(back ? r + 1 : g.len - 1 - r) * l2);
-                    split_pair(x.x, w, x.x, lo.x);
-                    split_pair(x.y, w, x.y, lo.y);
-                    split_pair(x.z, w, x.z, lo.z);
-                    split_pair(x.w, w, x.w, lo.w);
+                    split8(x, w0 * ex2((float)(back ? r + 1 : g.len - 1 - r) * l2), lo);
                 } else {                                 // another sequence's rows
                     x = lo = make_uint4(0, 0, 0, 0);
                     *reinterpret_cast<uint4*>(st + C::TILE + u * 16) = x;
@@ -283,7 +307,7 @@ struct DecayScanArgs {
 // D^2 / 1024, kinds of state), 4 elements per thread.
 template <int D>
 __global__ void __launch_bounds__(256)
-decay_scan_kernel(const DecayScanArgs args, const DecayShape sh, const int32_t* __restrict__ cu,
+decay_scan_kernel(const __grid_constant__ DecayScanArgs args, const DecayShape sh, const int32_t* __restrict__ cu,
                   const float* __restrict__ log_decay, int* status) {
     const int head = blockIdx.x % sh.heads, seq = blockIdx.x / sh.heads, kind = blockIdx.z;
     const SeqRange r = seq_range(cu, seq, sh.total, status);
@@ -296,25 +320,20 @@ decay_scan_kernel(const DecayScanArgs args, const DecayShape sh, const int32_t* 
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
     if (args.first[kind]) s = __ldg(reinterpret_cast<const float4*>(args.first[kind] + ((long long)seq * sh.heads + head) * D * D + e));
     const int tail = r.len - n * sh.seg;                 // tokens of the last segment
-    float* base = args.border[kind] + (long long)head * D * D + e;
+    const long long step = (long long)sh.heads * D * D;
+    float* base = args.border[kind] + (r.begin / sh.seg) * step + (long long)head * D * D + e;    // border 0
     constexpr int AHEAD = 8;
     for (int i0 = 0; i0 < n; i0 += AHEAD) {
         float4 u[AHEAD];
-        float4* p[AHEAD];
 #pragma unroll
-        for (int j = 0; j < AHEAD; ++j) {
-            const int b = back ? n - 1 - i0 - j : i0 + j;          // border b lies behind segment b
-            if (i0 + j < n) {
-                p[j] = reinterpret_cast<float4*>(base + ((long long)r.begin + (long long)b * sh.seg) / sh.seg * sh.heads * D * D);
-                u[j] = *p[j];
-            }
-        }
+        for (int j = 0; j < AHEAD; ++j)
+            if (i0 + j < n) u[j] = *reinterpret_cast<const float4*>(base + (back ? n - 1 - i0 - j : i0 + j) * step);
 #pragma unroll
         for (int j = 0; j < AHEAD; ++j) {
             if (i0 + j >= n) break;
             const float f = back && i0 + j == 0 ? ex2((float)tail * l2) : full;
             s.x = fmaf(f, s.x, u[j].x); s.y = fmaf(f, s.y, u[j].y); s.z = fmaf(f, s.z, u[j].z); s.w = fmaf(f, s.w, u[j].w);
-            *p[j] = s;
+            *reinterpret_cast<float4*>(base + (back ? n - 1 - i0 - j : i0 + j) * step) = s;
         }
     }
 }
@@ -325,44 +344,49 @@ struct DecOutCfg {
     static constexpr int NCH = D / 64;
     static constexpr int CHUNK = 128 * 128;              // 128 tokens of one 64-feature chunk
     static constexpr int TILE = NCH * CHUNK;
-    static constexpr int NST = D == 128 ? 5 : 9;         // ring of operand tiles
-    static constexpr int LO_OFF = NST * TILE;            // lo part of the weighted operand (hi in its tile's place)
+    static constexpr int NB = D == 128 ? 2 : 3;          // slots of the ring of B tiles
+    static constexpr int NAC = D == 128 ? 3 : 6;         // of the ring of A and C tiles, in turn
+    static constexpr int AC_OFF = NB * TILE;
+    static constexpr int LO_OFF = (NB + NAC) * TILE;     // lo part of the weighted operand (hi in its tile's place)
     static constexpr int X_OFF = LO_OFF + TILE;          // the state as bf16: 128 rows (d = 64: hi rows, lo rows) x D
-    static constexpr int COL_OFF = X_OFF + TILE;         // lam^0 .. lam^31
-    static constexpr int BAR_OFF = COL_OFF + 128;
+    static constexpr int POW_OFF = X_OFF + TILE;         // 64 floats: powers of lam, see the weights
+    static constexpr int BAR_OFF = POW_OFF + 256;
     static constexpr int SMEM = BAR_OFF + 512;
-    static constexpr int THREADS = 448;                  // 4 score warps, 8 state warps, loads, MMAs
-    static constexpr int X_COL = 0, S_COL = 128, O1_COL = 256, O2_COL = 384;   // TMEM
+    static constexpr int THREADS = 768;                  // warpgroups: 2 scores, 2 state, outputs, loads and MMAs; 80 registers a thread
+    static constexpr int REG_SCORE = 72, REG_STATE = 104, REG_OUT = 80, REG_LOAD = 48;   // 2 * 72 + 2 * 104 + 80 + 48 = 6 * 80
+    static constexpr int U_COL = 0, S_COL = 128, O1_COL = 256, O2_COL = 384;  // TMEM
 };
 static_assert(DecOutCfg<128>::SMEM <= 232448 && DecOutCfg<64>::SMEM <= 232448, "shared memory");
 
 template <int D>
 struct DecOutBars {
-    uint64_t full[DecOutCfg<D>::NST], empty[DecOutCfg<D>::NST];
-    uint64_t s_full, p_ready, x_ready, w_ready, o_full, x_done, mma_done;
+    uint64_t b_full[DecOutCfg<D>::NB], b_empty[DecOutCfg<D>::NB];
+    uint64_t ac_full[DecOutCfg<D>::NAC], ac_empty[DecOutCfg<D>::NAC];
+    uint64_t s_full, p_ready, x_ready, w_ready, o_full, o_free, u_done, mma_done;
     uint32_t tmem_base;
     int abort;
 };
 static_assert(sizeof(DecOutBars<64>) <= 512, "barrier block");
 
-// grid (segments x heads, passes)
+// grid (passes x segments x heads: the passes over one segment run side by
+// side and share its tiles in L2)
 template <int D>
 __global__ void __launch_bounds__(DecOutCfg<D>::THREADS, 1)
-decay_out_kernel(const __grid_constant__ DecayPasses passes, const DecayShape sh, const int32_t* __restrict__ cu,
-                 const float* __restrict__ log_decay, int* status) {
+decay_out_kernel(const __grid_constant__ DecayPasses passes, const int n_passes, const DecayShape sh,
+                 const int32_t* __restrict__ cu, const float* __restrict__ log_decay, int* status) {
     using C = DecOutCfg<D>;
     extern __shared__ __align__(1024) uint8_t smem[];
     if (smem_u32(smem) & 1023) {
         if (threadIdx.x == 0) report(status, kStatusMisaligned);
         return;
     }
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const DecayPass& ps = passes.p[blockIdx.y];
-    const int head = blockIdx.x % sh.heads;
+    const int tid = threadIdx.x, warp = warp_uniform(tid >> 5), lane = tid & 31;
+    const DecayPass& ps = passes.p[blockIdx.x % n_passes];
+    const int item = blockIdx.x / n_passes, head = item % sh.heads;
     const bool back = ps.back;
-    const Segment g = find_segment(cu, sh, blockIdx.x / sh.heads, status);
+    const Segment g = find_segment(cu, sh, item / sh.heads, status);
     if (g.seq < 0) return;
-    const int n = (g.len + 127) / 128;                   // chunks; step t is chunk t, or n - 1 - t backwards
+    const int n = warp_uniform((g.len + 127) / 128);                   // chunks; step t is chunk t, or n - 1 - t backwards
     auto chunk_of = [&](int t) { return back ? n - 1 - t : t; };
     const long long own = ((long long)g.seq * sh.heads + head) * D * D;
     const bool ends = back ? g.first : g.last;           // this CTA reaches the end of the walk
@@ -375,65 +399,87 @@ decay_out_kernel(const __grid_constant__ DecayPasses passes, const DecayShape sh
             for (int e = tid; e < D * D; e += C::THREADS) last[e] = x0 ? x0[e] : 0.f;
         return;
     }
-    const int updates = last ? n : n - 1;                // steps whose state is needed
-    uint8_t* ring = smem;
+    const int updates = warp_uniform(last ? n : n - 1);                // steps whose update of the state is needed
     uint8_t* sLo = smem + C::LO_OFF;
     uint8_t* sX = smem + C::X_OFF;
-    float* sCol = reinterpret_cast<float*>(smem + C::COL_OFF);
+    float* sPow = reinterpret_cast<float*>(smem + C::POW_OFF);
     DecOutBars<D>* bars = reinterpret_cast<DecOutBars<D>*>(smem + C::BAR_OFF);
     volatile int* abort_flag = &bars->abort;
     const float l2 = decay_log2(log_decay, head);
     if (tid == 0) {
         bars->abort = 0;
-        for (int x = 0; x < C::NST; ++x) { mbar_init(&bars->full[x], 1); mbar_init(&bars->empty[x], 1); }
+        for (int x = 0; x < C::NB; ++x) { mbar_init(&bars->b_full[x], 1); mbar_init(&bars->b_empty[x], 1); }
+        for (int x = 0; x < C::NAC; ++x) { mbar_init(&bars->ac_full[x], 1); mbar_init(&bars->ac_empty[x], 1); }
         mbar_init(&bars->s_full, 1);
-        mbar_init(&bars->p_ready, 128);
+        mbar_init(&bars->p_ready, 256);
         mbar_init(&bars->x_ready, 256);
         mbar_init(&bars->w_ready, 256);
         mbar_init(&bars->o_full, 1);
-        mbar_init(&bars->x_done, 1);
+        mbar_init(&bars->o_free, 128);
+        mbar_init(&bars->u_done, 1);
         mbar_init(&bars->mma_done, 1);
         fence_barrier_init();
     }
-    if (tid < 32) sCol[tid] = ex2((float)tid * l2);
-    if (warp == 13) { tmem_alloc(&bars->tmem_base, 512); tmem_relinquish(); }
+    // forward lam^31 .. lam^0 and zeros, backwards zeros and lam^0 .. lam^31
+    if (tid < 64) sPow[tid] = (back ? tid >= 32 : tid < 32) ? ex2((float)(back ? tid - 32 : 31 - tid) * l2) : 0.f;
+    if (warp == 21) { tmem_alloc(&bars->tmem_base, 512); tmem_relinquish(); }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tbase = bars->tmem_base;
+    const uint32_t tbase = warp_uniform(bars->tmem_base);
     auto fail = [&]() { *abort_flag = 1; report(status, kStatusTimeout); };
-    // ring items of step t: B, A, C at 3 t, 3 t + 1, 3 t + 2
-    auto slot = [&](int i) { return ring + (i % C::NST) * C::TILE; };
-    auto item_wait = [&](int i) { return mma_wait(&bars->full[i % C::NST], (i / C::NST) & 1, abort_flag); };
+    // B of step t, and item i of the A and C tiles (A of step t at 2 t, C at 2 t + 1)
+    auto b_slot = [&](int t) { return smem + (t % C::NB) * C::TILE; };
+    auto b_wait = [&](int t) { return mma_wait(&bars->b_full[t % C::NB], (t / C::NB) & 1, abort_flag); };
+    auto ac_slot = [&](int i) { return smem + C::AC_OFF + (i % C::NAC) * C::TILE; };
+    auto ac_wait = [&](int i) { return mma_wait(&bars->ac_full[i % C::NAC], (i / C::NAC) & 1, abort_flag); };
 
-    if (warp == 12) {
-        if (lane == 0) {
+    if (warp >= 20) {
+      reg_dec<C::REG_LOAD>();
+      if (warp == 20) {
+        if (elect_one()) {
             // ---------------------------------------------------------- loads
-            int issued = 0;
-            for (int i = 0; i < 3 * n; ++i) {
-                const int st = i % C::NST;
-                if (i >= C::NST && !mbar_wait(&bars->empty[st], (i / C::NST - 1) & 1, abort_flag)) { fail(); break; }
-                const CUtensorMap* map = i % 3 == 0 ? &ps.b : i % 3 == 1 ? &ps.a : &ps.c;
-                const int row = g.begin + 128 * chunk_of(i / 3);
-                mbar_arrive_expect_tx(&bars->full[st], C::TILE);
+            // in the order in which slots are freed: C of step t + 1 follows
+            // A of step t, B and A of step t + 2 follow the update of step t
+            int nb = 0, nac = 0;
+            auto load = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* full, int t) {
+                const int row = g.begin + 128 * chunk_of(t);
+                mbar_arrive_expect_tx(full, C::TILE);
                 for (int c = 0; c < 2 * C::NCH; ++c)     // boxes of 64 tokens x 64 features
-                    tma_load_3d(slot(i) + c * 8192, map, &bars->full[st], 64 * (c >> 1), head, row + 64 * (c & 1));
-                ++issued;
+                    tma_load_3d(dst + c * 8192, map, full, 64 * (c >> 1), head, row + 64 * (c & 1));
+            };
+            auto load_ac = [&](const CUtensorMap* map, int t) {
+                const int x = nac % C::NAC;
+                if (nac >= C::NAC && !mbar_wait(&bars->ac_empty[x], (nac / C::NAC - 1) & 1, abort_flag)) return false;
+                load(ac_slot(nac), map, &bars->ac_full[x], t);
+                ++nac;
+                return true;
+            };
+            bool ok = true;
+            for (int t = 0; t < n && ok; ++t) {
+                const int x = t % C::NB;
+                if (t >= C::NB && !(ok = mbar_wait(&bars->b_empty[x], (t / C::NB - 1) & 1, abort_flag))) break;
+                load(b_slot(t), &ps.b, &bars->b_full[x], t);
+                ++nb;
+                ok = load_ac(&ps.a, t) && load_ac(&ps.c, t);
             }
-            if (*abort_flag)
-                for (int i = max(0, issued - C::NST); i < issued; ++i) wait_noabort(&bars->full[i % C::NST], (i / C::NST) & 1);
+            if (!ok) fail();
+            if (*abort_flag) {
+                for (int i = max(0, nb - C::NB); i < nb; ++i) wait_noabort(&bars->b_full[i % C::NB], (i / C::NB) & 1);
+                for (int i = max(0, nac - C::NAC); i < nac; ++i) wait_noabort(&bars->ac_full[i % C::NAC], (i / C::NAC) & 1);
+            }
         }
-    } else if (warp == 13) {
-        if (lane == 0) {
+      } else if (warp == 21) {
+        if (elect_one()) {
             // ----------------------------------------------------------- MMAs
             constexpr uint32_t id_s = idesc_bf16_f32(128, 128, false, false);
             constexpr uint32_t id_o = idesc_bf16_f32(128, D, false, true);
             constexpr uint32_t id_x = idesc_bf16_f32(128, D, true, true);
             const uint32_t lo = smem_u32(sLo), xs = smem_u32(sX);
             auto issue_s = [&](int t) {
-                if (!item_wait(3 * t) || !item_wait(3 * t + 1)) return false;
+                if (!b_wait(t) || !ac_wait(2 * t)) return false;
                 tc_fence_after();
-                const uint32_t b = smem_u32(slot(3 * t)), a = smem_u32(slot(3 * t + 1));
+                const uint32_t b = smem_u32(b_slot(t)), a = smem_u32(ac_slot(2 * t));
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                     const uint32_t o = (kk >> 2) * C::CHUNK + (kk & 3) * 32;
@@ -444,13 +490,16 @@ decay_out_kernel(const __grid_constant__ DecayPasses passes, const DecayShape sh
             };
             bool ok = issue_s(0);
             for (int t = 0; t < n && ok; ++t) {
-                const uint32_t b = smem_u32(slot(3 * t)), a = smem_u32(slot(3 * t + 1)), c = smem_u32(slot(3 * t + 2));
-                // O1 = P C (the score warps have read O1 and O2 of step t - 1 before they wrote P)
-                if (!(ok = mma_wait(&bars->p_ready, t & 1, abort_flag) && item_wait(3 * t + 2))) break;
+                const uint32_t b = smem_u32(b_slot(t)), a = smem_u32(ac_slot(2 * t)), c = smem_u32(ac_slot(2 * t + 1));
+                // O1 = P C
+                if (!(ok = (t == 0 || mma_wait(&bars->o_free, (t - 1) & 1, abort_flag)) && ac_wait(2 * t + 1) &&
+                           mma_wait(&bars->p_ready, t & 1, abort_flag)))
+                    break;
                 tc_fence_after();
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                    mma_bf16_ts(tbase + C::O1_COL, tbase + C::S_COL + kk * 8, smem_desc_sw128(c + kk * 2048, C::CHUNK, 1024), id_o, kk > 0);
+                for (int kk = 0; kk < 8; ++kk)           // P: 64 tokens in 32 columns, each half where its scores were
+                    mma_bf16_ts(tbase + C::O1_COL, tbase + C::S_COL + (kk >> 2) * 64 + (kk & 3) * 8,
+                                smem_desc_sw128(c + kk * 2048, C::CHUNK, 1024), id_o, kk > 0);
                 // O2 = A X
                 if (!(ok = mma_wait(&bars->x_ready, t & 1, abort_flag))) break;
                 tc_fence_after();
@@ -461,77 +510,76 @@ decay_out_kernel(const __grid_constant__ DecayPasses passes, const DecayShape sh
                                 smem_desc_sw128(xs + kk * 2048, C::CHUNK, 1024), id_o, kk > 0);
                 }
                 mma_commit(&bars->o_full);
-                mma_commit(&bars->empty[(3 * t + 1) % C::NST]);
+                mma_commit(&bars->ac_empty[(2 * t) % C::NAC]);
                 if (t + 1 < n && !(ok = issue_s(t + 1))) break;
                 if (t < updates) {
-                    // X += (B w)^T C
+                    // U = (B w)^T C
                     if (!(ok = mma_wait(&bars->w_ready, t & 1, abort_flag))) break;
                     tc_fence_after();
 #pragma unroll
                     for (int kk = 0; kk < 8; ++kk) {
                         const uint64_t cd = smem_desc_sw128(c + kk * 2048, C::CHUNK, 1024);
                         if (D == 128) {
-                            mma_bf16_ss(tbase + C::X_COL, smem_desc_sw128(b + kk * 2048, C::CHUNK, 1024), cd, id_x, 1);
-                            mma_bf16_ss(tbase + C::X_COL, smem_desc_sw128(lo + kk * 2048, C::CHUNK, 1024), cd, id_x, 1);
+                            mma_bf16_ss(tbase + C::U_COL, smem_desc_sw128(b + kk * 2048, C::CHUNK, 1024), cd, id_x, kk > 0);
+                            mma_bf16_ss(tbase + C::U_COL, smem_desc_sw128(lo + kk * 2048, C::CHUNK, 1024), cd, id_x, 1);
                         } else {
-                            mma_bf16_ss(tbase + C::X_COL, smem_desc_sw128(b + kk * 2048, lo - b, 1024), cd, id_x, 1);
+                            mma_bf16_ss(tbase + C::U_COL, smem_desc_sw128(b + kk * 2048, lo - b, 1024), cd, id_x, kk > 0);
                         }
                     }
-                    mma_commit(&bars->x_done);
-                    mma_commit(&bars->empty[(3 * t) % C::NST]);
-                    mma_commit(&bars->empty[(3 * t + 2) % C::NST]);
+                    mma_commit(&bars->u_done);
+                    mma_commit(&bars->b_empty[t % C::NB]);
+                    mma_commit(&bars->ac_empty[(2 * t + 1) % C::NAC]);
                 }
             }
             if (!ok) fail();
             mma_commit(&bars->mma_done);
             wait_noabort(&bars->mma_done, 0);
         }
-    } else if (warp < 4) {
-        // ------------------------------------------------- weights and outputs
-        const int r = tid;                               // token of the chunk
-        const uint32_t lanes = (uint32_t)(32 * warp) << 16;
-        const uint32_t tS = tbase + lanes + C::S_COL, tO1 = tbase + lanes + C::O1_COL, tO2 = tbase + lanes + C::O2_COL;
+      }
+    } else if (warp < 8) {
+        reg_dec<C::REG_SCORE>();
+        // -------------------------------------------------------- the weights
+        const int quarter = warp & 3, hf = warp >> 2;    // 32 tokens; half of the columns
+        const int r = 32 * quarter + lane;               // token of the chunk
+        const uint32_t tS = tbase + ((uint32_t)(32 * quarter) << 16) + C::S_COL + 64 * hf;
+        // lam^|i-j| is lam^(to the near end of j's block of 32) times
+        // lam^(within the block), both factors at most 1; in the diagonal block
+        // it is a table's entry at j - i, 0 on the masked side.
         bool ok = true;
         for (int t = 0; t < n; ++t) {
-            const int tok = 128 * chunk_of(t), rows = min(128, g.len - tok);
+            const int rows = min(128, g.len - 128 * chunk_of(t));
             if (rows < 128) {
                 // C's rows behind the sequence are another one's: zeros
-                if (!__all_sync(0xffffffffu, item_wait(3 * t + 2))) { ok = false; break; }
-                uint8_t* c = slot(3 * t + 2);
-                for (int u = r; u < (128 - rows) * 8 * C::NCH; u += 128)
+                if (!__all_sync(0xffffffffu, ac_wait(2 * t + 1))) { ok = false; break; }
+                uint8_t* c = ac_slot(2 * t + 1);
+                for (int u = tid; u < (128 - rows) * 8 * C::NCH; u += 256)
                     *reinterpret_cast<uint4*>(c + (u % C::NCH) * C::CHUNK + rows * 128 + (u / C::NCH) * 16) = make_uint4(0, 0, 0, 0);
                 fence_proxy_async_smem();
             }
             if (!__all_sync(0xffffffffu, mbar_wait(&bars->s_full, t & 1, abort_flag))) { ok = false; break; }
             tc_fence_after();
-            // P over the scores: 32 columns at a time.  Away from the diagonal
-            // lam^|i-j| is lam^(to the block's near end) lam^(within the block),
-            // both factors at most 1.
+            // P over the scores, 32 columns at a time (a loop: the kernel's
+            // roles have to share the instruction cache)
 #pragma unroll 1
-            for (int blk = 0; blk < 4; ++blk) {
+            for (int h = 0; h < 2; ++h) {
+                const int blk = 2 * hf + h;
                 uint32_t pk[16];
-                if (blk == warp) {
+                if (back ? blk >= quarter : blk <= quarter) {
+                    const int far = blk == quarter ? 0 : back ? 32 * blk - r : r - 32 * blk - 31;
+                    const float* y = sPow + (blk == quarter ? (back ? 32 : 31) - lane : back ? 32 : 0);
+                    const float f = ps.p_scale * ex2((float)far * l2);
                     float s[32];
-                    tmem_ld_32x32b_x32(tS + 32 * blk, s);
+                    tmem_ld_32x32b_x32(tS + 32 * h, s);
                     tmem_wait_ld();
+                    const uint64_t f2 = f32x2(f, f);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        const int dist = back ? e - lane : lane - e;
-                        s[e] = dist >= 0 && 32 * blk + e < rows ? s[e] * ps.p_scale * ex2((float)dist * l2) : 0.f;
-                    }
+                    for (int e = 0; e < 32; e += 2)
+                        unf32x2(mul_f32x2(f32x2(s[e], s[e + 1]), mul_f32x2(f2, f32x2(y[e], y[e + 1]))), s[e], s[e + 1]);
+                    if (rows < 128) {                    // scores of rows behind the sequence may be anything
+                        const int lo = back && blk == quarter ? lane : 0;
+                        const int hi = min(rows - 32 * blk, !back && blk == quarter ? lane + 1 : 32);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) pk[e] = pack_bf16x2(s[2 * e], s[2 * e + 1]);
-                } else if (back ? blk > warp : blk < warp) {
-                    float s[32];
-                    tmem_ld_32x32b_x32(tS + 32 * blk, s);
-                    tmem_wait_ld();
-                    const float f = ps.p_scale * ex2((float)(back ? 32 * blk - r : r - 32 * blk - 31) * l2);
-                    if (back) {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) s[e] = 32 * blk + e < rows ? s[e] * (f * sCol[e]) : 0.f;
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) s[e] *= f * sCol[31 - e];
+                        for (int e = 0; e < 32; ++e) s[e] = e >= lo && e < hi ? s[e] : 0.f;
                     }
 #pragma unroll
                     for (int e = 0; e < 16; ++e) pk[e] = pack_bf16x2(s[2 * e], s[2 * e + 1]);
@@ -539,40 +587,60 @@ decay_out_kernel(const __grid_constant__ DecayPasses passes, const DecayShape sh
 #pragma unroll
                     for (int e = 0; e < 16; ++e) pk[e] = 0;
                 }
-                // the packed columns of block blk lie in the scores of block blk / 2, which are read
-                tmem_st_32x32b_x16(tS + 16 * blk, pk);
+                tmem_st_32x32b_x16(tS + 16 * h, pk);     // (over scores of this thread's that are read or masked)
             }
             tmem_wait_st();
             tc_fence_before();
             mbar_arrive(&bars->p_ready);
+        }
+        if (!ok) fail();
+    } else if (warp >= 16) {
+        // -------------------------------------------------------- the outputs
+        const int quarter = warp & 3, r = 32 * quarter + lane;
+        const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
+        const float f_full = ps.s_scale * ex2((float)(back ? 127 - r : r + 1) * l2);
+        bool ok = true;
+        for (int t = 0; t < n; ++t) {
+            const int tok = 128 * chunk_of(t), rows = min(128, g.len - tok);
+            const float f = back && rows < 128 ? ps.s_scale * ex2((float)(rows - 1 - r) * l2) : f_full;
+            // lane l stores units l & 3 of the rows of its four lanes
+            __nv_bfloat16* po = ps.out + (long long)(g.begin + tok + (r & ~3)) * ps.out_stride + (long long)head * D + (lane & 3) * 8;
             if (!__all_sync(0xffffffffu, mbar_wait(&bars->o_full, t & 1, abort_flag))) { ok = false; break; }
             tc_fence_after();
-            const float f = ps.s_scale * ex2((float)(back ? rows - 1 - r : r + 1) * l2);
-            __nv_bfloat16* po = ps.out + (long long)(g.begin + tok + r) * ps.out_stride + (long long)head * D;
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < D; c += 32) {
-                float o[32], x[32];
-                tmem_ld_32x32b_x32(tO1 + c, o);
-                tmem_ld_32x32b_x32(tO2 + c, x);
-                tmem_wait_ld();
-                if (r < rows) {
+                float o[32];
+                uint4 u[4];
+                {
+                    float x[32];
+                    tmem_ld_32x32b_x32(tbase + lanes + C::O1_COL + c, o);
+                    tmem_ld_32x32b_x32(tbase + lanes + C::O2_COL + c, x);
+                    tmem_wait_ld();
+                    const uint64_t f2 = f32x2(f, f);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = fmaf(f, x[e], o[e]);
-#pragma unroll
-                    for (int e = 0; e < 32; e += 8)
-                        *reinterpret_cast<uint4*>(po + c + e) = make_uint4(pack_bf16x2(o[e], o[e + 1]), pack_bf16x2(o[e + 2], o[e + 3]),
-                                                                           pack_bf16x2(o[e + 4], o[e + 5]), pack_bf16x2(o[e + 6], o[e + 7]));
+                    for (int e = 0; e < 32; e += 2) unf32x2(fma_f32x2(f2, f32x2(x[e], x[e + 1]), f32x2(o[e], o[e + 1])), o[e], o[e + 1]);
                 }
+                if (c + 32 == D) {
+                    tc_fence_before();
+                    mbar_arrive(&bars->o_free);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    u[e] = make_uint4(pack_bf16x2(o[8 * e], o[8 * e + 1]), pack_bf16x2(o[8 * e + 2], o[8 * e + 3]),
+                                      pack_bf16x2(o[8 * e + 4], o[8 * e + 5]), pack_bf16x2(o[8 * e + 6], o[8 * e + 7]));
+                transpose_units(u, lane);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if ((r & ~3) + e < rows) *reinterpret_cast<uint4*>(po + e * ps.out_stride + c) = u[e];
             }
-            tc_fence_before();                           // before the next P lets O1 and O2 be written again
         }
         if (!ok) fail();
     } else {
+        reg_inc<C::REG_STATE>();
         // ---------------------------------------------------------- the state
-        const int id = tid - 128, hf = id >> 7;          // half of the columns
-        const int row = id & 127;                        // TMEM lane
-        const int feat = row & (D - 1);
-        const uint32_t tX = tbase + ((uint32_t)(32 * (warp & 3)) << 16) + C::X_COL + hf * (D / 2);
+        // in registers: a row (TMEM lane) and half of its columns
+        const int id = tid - 256, hf = id >> 7, row = id & 127, feat = row & (D - 1);
+        const uint32_t tU = tbase + ((uint32_t)(32 * (warp & 3)) << 16) + C::U_COL + hf * (D / 2);
         bool ok = true;
         float x[D / 2];
         if (x0 && row < D) {
@@ -591,16 +659,36 @@ decay_out_kernel(const __grid_constant__ DecayPasses passes, const DecayShape sh
 #pragma unroll
             for (int c = 0; c < D / 2; ++c) x[c] = 0.f;
         }
+        // weights of this thread's tokens in a chunk of `rows`
+        float w[4];
+        int w_rows = 0;
+        auto set_weights = [&](int rows) {
+            w_rows = rows;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = id / 8 + 32 * i;
+                w[i] = ps.w_scale * ex2((float)(back ? r + 1 : rows - 1 - r) * l2);
+            }
+        };
+        // X = lam^tokens X + U, once the products of step t have finished
+        auto update = [&](int t) {
+            if (!__all_sync(0xffffffffu, mbar_wait(&bars->u_done, t & 1, abort_flag))) return false;
+            tc_fence_after();
+            const float f = ex2((float)min(128, g.len - 128 * chunk_of(t)) * l2);
+#pragma unroll
+            for (int c = 0; c < D / 2; c += 32) {
+                float u[32];
+                tmem_ld_32x32b_x32(tU + c, u);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) x[c + e] = fmaf(f, x[c + e], u[e]);
+            }
+            tc_fence_before();
+            return true;
+        };
         for (int t = 0; t < n; ++t) {
             const int tok = 128 * chunk_of(t), rows = min(128, g.len - tok);
-            if (t > 0) {
-                // products of step t - 1 and the scores of step t have finished
-                if (!__all_sync(0xffffffffu, mbar_wait(&bars->x_done, (t - 1) & 1, abort_flag))) { ok = false; break; }
-                tc_fence_after();
-#pragma unroll
-                for (int c = 0; c < D / 2; c += 32) tmem_ld_32x32b_x32(tX + c, *reinterpret_cast<float(*)[32]>(&x[c]));
-                tmem_wait_ld();
-            }
+            if (t > 0 && !update(t - 1)) { ok = false; break; }    // then the scores of step t have finished too
             uint8_t* xr = sX + row * 128;
 #pragma unroll
             for (int c = 0; c < D / 2; c += 8) {
@@ -609,49 +697,30 @@ decay_out_kernel(const __grid_constant__ DecayPasses passes, const DecayShape sh
                     make_uint4(pack_bf16x2(x[c], x[c + 1]), pack_bf16x2(x[c + 2], x[c + 3]), pack_bf16x2(x[c + 4], x[c + 5]),
                                pack_bf16x2(x[c + 6], x[c + 7]));
             }
-            if (t < updates) {
-                const float f = ex2((float)rows * l2);
-#pragma unroll
-                for (int c = 0; c < D / 2; ++c) x[c] *= f;
-#pragma unroll
-                for (int c = 0; c < D / 2; c += 32) tmem_st_32x32b_x32f(tX + c, *reinterpret_cast<float(*)[32]>(&x[c]));
-                tmem_wait_st();
-            }
             if (t == 0 && !__all_sync(0xffffffffu, mbar_wait(&bars->s_full, 0, abort_flag))) { ok = false; break; }
-            tc_fence_before();
             fence_proxy_async_smem();
             mbar_arrive(&bars->x_ready);
             if (t < updates) {
-                if (!__all_sync(0xffffffffu, item_wait(3 * t))) { ok = false; break; }   // (done: its scores are)
-                uint8_t* b = slot(3 * t);
+                if (!__all_sync(0xffffffffu, b_wait(t))) { ok = false; break; }   // (long done: the scores are)
+                uint8_t* b = b_slot(t);
+                if (rows != w_rows) set_weights(rows);
+#pragma unroll 1
+                for (int o = id * 16; o < C::TILE; o += C::CHUNK) {
 #pragma unroll
-                for (int u = id; u < C::TILE / 16; u += 256) {
-                    const int r = (u & 1023) / 8;        // token of the chunk
-                    uint4 y = *reinterpret_cast<const uint4*>(b + u * 16), lo;
-                    if (r < rows) {
-                        const float w = ps.w_scale * ex2((float)(back ? r + 1 : rows - 1 - r) * l2);
-                        split_pair(y.x, w, y.x, lo.x);
-                        split_pair(y.y, w, y.y, lo.y);
-                        split_pair(y.z, w, y.z, lo.z);
-                        split_pair(y.w, w, y.w, lo.w);
-                    } else {
-                        y = lo = make_uint4(0, 0, 0, 0);
+                    for (int i = 0; i < 4; ++i) {        // a 16-byte unit of token id / 8 + 32 i
+                        uint4 y = *reinterpret_cast<const uint4*>(b + o + 4096 * i), lo;
+                        split8(y, w[i], lo);
+                        if (rows < 128 && id / 8 + 32 * i >= rows) y = lo = make_uint4(0, 0, 0, 0);
+                        *reinterpret_cast<uint4*>(b + o + 4096 * i) = y;
+                        *reinterpret_cast<uint4*>(sLo + o + 4096 * i) = lo;
                     }
-                    *reinterpret_cast<uint4*>(b + u * 16) = y;
-                    *reinterpret_cast<uint4*>(sLo + u * 16) = lo;
                 }
                 fence_proxy_async_smem();
                 mbar_arrive(&bars->w_ready);
             }
         }
         if (last) {
-            if (ok && !__all_sync(0xffffffffu, mbar_wait(&bars->x_done, (n - 1) & 1, abort_flag))) ok = false;
-            tc_fence_after();
-            if (ok) {
-#pragma unroll
-                for (int c = 0; c < D / 2; c += 32) tmem_ld_32x32b_x32(tX + c, *reinterpret_cast<float(*)[32]>(&x[c]));
-                tmem_wait_ld();
-            }
+            if (ok && !update(n - 1)) ok = false;
             if (D == 64) {
                 // the last products have finished: the bf16 state's place holds the lo part for the hi part's threads
                 float* half = reinterpret_cast<float*>(sX) + hf * 32 * 64 + feat;
@@ -683,7 +752,7 @@ decay_out_kernel(const __grid_constant__ DecayPasses passes, const DecayShape sh
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 13) tmem_dealloc(tbase, 512);
+    if (warp == 21) tmem_dealloc(tbase, 512);
 }
 
 // --------------------------------------------------------------------- launch
@@ -713,7 +782,7 @@ static long long decay_segments(const DecayShape& s) { return (long long)s.total
 
 static size_t border_bytes(const DecayShape& s, int d) { return (size_t)(s.total / s.seg) * s.heads * d * d * sizeof(float); }
 
-long long decay_work_items(int n_seq, int total, int heads) { return ((long long)total / 128 + n_seq) * heads; }
+long long decay_work_items(int n_seq, int total, int heads) { return 3 * ((long long)total / 128 + n_seq) * heads; }
 
 size_t decay_scratch_bytes(int n_seq, int total, int heads, int d) {
     return std::max(border_bytes(decay_shape(n_seq, total, heads, 1), d), 2 * border_bytes(decay_shape(n_seq, total, heads, 3), d));
@@ -737,7 +806,7 @@ static cudaError_t launch_decay(const DecayArgs& a, const DecayShape& sh, const 
         decay_scan_kernel<D><<<dim3((unsigned)((long long)a.n_seq * a.heads), D * D / 1024, kinds), 256, 0, stream>>>(sc, sh, a.cu, a.log_decay, a.status);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
-    decay_out_kernel<D><<<dim3(items, n_passes), DecOutCfg<D>::THREADS, DecOutCfg<D>::SMEM, stream>>>(passes, sh, a.cu, a.log_decay, a.status);
+    decay_out_kernel<D><<<items * n_passes, DecOutCfg<D>::THREADS, DecOutCfg<D>::SMEM, stream>>>(passes, n_passes, sh, a.cu, a.log_decay, a.status);
     return cudaGetLastError();
 }
 

@@ -20,6 +20,21 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
+// One lane of the (converged) warp, and a value that is the same in all its
+// lanes.  An MMA takes its descriptors from uniform registers: where the
+// compiler can see that a warp-uniform branch, one elected thread and values
+// made uniform lead to it, an issue takes 50 to 70 cycles instead of 100 to
+// 200 (128 x 128 x 16 bf16: the product itself takes 64).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+template <typename T>
+__device__ __forceinline__ T warp_uniform(T x) {
+    return __shfl_sync(0xffffffffu, x, 0);
+}
+
 // ------------------------------------------------------------------ mbarrier
 
 __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
