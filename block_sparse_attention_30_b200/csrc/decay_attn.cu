@@ -13,9 +13,9 @@
 //     dv:  k, q, dout and dk: v, dout, q backwards in time (state: the
 //          gradient of S, transposed for dk).
 //
-// Tokens go in chunks of 128.  A sequence is cut into segments (a rule on the
-// sizes, see segment_chunks), and three launches compute
-//   decay_state_kernel  each segment's own contribution to the state at its
+// Tokens go in chunks of 128.  A sequence is cut into segments, and these into
+// parts (a rule on the sizes, see decay_shape); three launches compute
+//   decay_state_kernel  each part's own contribution to the state at its
 //                       border: (b w)^T c with w = lam^(tokens to the border),
 //                       one GEMM with the tokens as its inner dimension;
 //   decay_scan_kernel   the states at the borders, border after border;
@@ -68,7 +68,8 @@ struct DecayPasses {
 };
 
 struct DecayShape {
-    int n_seq, total, heads, seg;      // seg: tokens of a segment, a multiple of 128
+    int n_seq, total, heads;
+    int seg, part;               // tokens of a segment and of a part of it (multiples of 128)
 };
 
 // log2(lam); below 2^-1024 a decay is a plain 0 (and lam^0 stays 1)
@@ -77,32 +78,36 @@ __device__ __forceinline__ float decay_log2(const float* __restrict__ log_decay,
     return x < -1024.f ? -1024.f : x;
 }
 
-// Where a segment lies, and its border's place in the scratch: the borders
-// start full segments, whose starts are `seg` rows apart at least.
-struct Segment {
-    int seq, begin, len;         // first row and rows of the segment
-    bool first, last;            // of its sequence
+// A piece (segment or part) of a sequence.  The border behind a part that is
+// not the sequence's last has its place in the scratch at (the part's first
+// row) / part: these parts are full, so no two start within one multiple.
+struct Piece {
+    int seq, begin, len;         // first row and rows
+    int off, rest;               // tokens of the sequence before it and from its first on
 };
 
-__device__ __forceinline__ Segment find_segment(const int32_t* __restrict__ cu, const DecayShape& s, int t, int* status) {
-    Segment g{-1, 0, 0, false, false};
-    const SeqTile at = find_tile(cu, s.n_seq, s.total, s.seg, t, status, 1);
+__device__ __forceinline__ Piece find_piece(const int32_t* __restrict__ cu, const DecayShape& s, int len, int t, int* status) {
+    Piece g{-1, 0, 0, 0, 0};
+    const SeqTile at = find_tile(cu, s.n_seq, s.total, len, t, status, 1);
     if (at.seq < 0) return g;
     const SeqRange r = seq_range(cu, at.seq, s.total, status);
-    const int off = at.tile * s.seg;
     g.seq = at.seq;
-    g.begin = r.begin + off;
-    g.len = min(s.seg, r.len - off);
-    g.first = off == 0;
-    g.last = off + s.seg >= r.len;
+    g.off = at.tile * len;
+    g.rest = r.len - g.off;
+    g.begin = r.begin + g.off;
+    g.len = min(len, g.rest);
     return g;
 }
 
 // bf16 pairs x times w as hi + lo.
 __device__ __forceinline__ void split_pair(uint32_t x, float w, uint32_t& hi, uint32_t& lo) {
-    const float x0 = __uint_as_float(x << 16) * w, x1 = __uint_as_float(x & 0xffff0000u) * w;
+    const uint64_t p = mul_f32x2(f32x2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u)), f32x2(w, w));
+    float x0, x1;
+    unf32x2(p, x0, x1);
     hi = pack_bf16x2(x0, x1);
-    lo = pack_bf16x2(x0 - __uint_as_float(hi << 16), x1 - __uint_as_float(hi & 0xffff0000u));
+    // p - hi, exactly
+    unf32x2(fma_f32x2(f32x2(__uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u)), f32x2(-1.f, -1.f), p), x0, x1);
+    lo = pack_bf16x2(x0, x1);
 }
 
 __device__ __forceinline__ void split8(uint4& x, float w, uint4& lo) {
@@ -140,7 +145,7 @@ struct DecStateCfg {
     static constexpr int CHUNK = 64 * 128;               // 64 tokens of one 64-feature chunk
     static constexpr int TILE = NCH * CHUNK;
     static constexpr int STAGE = 3 * TILE;               // b (hi in its place), c, lo
-    static constexpr int NST = D == 128 ? 4 : 8;
+    static constexpr int NST = D == 128 ? 2 : 4;         // (two CTAs per SM)
     static constexpr int BAR_OFF = NST * STAGE;
     static constexpr int SMEM = BAR_OFF + 512;
     static constexpr int THREADS = 288;                  // 8 transform warps, loads and MMAs
@@ -162,10 +167,11 @@ struct DecayStateArgs {
     float w_scale[2];
 };
 
-// grid (segments x heads, kinds of state).  Forward in time the sum of segment
-// s goes to the border behind it, backwards that of segment s + 1.
+// grid (parts x heads, kinds of state).  Forward in time the sum of part p
+// goes to the border behind it, backwards that of part p + 1; parts of the
+// walk's last segment reach no border that is needed.
 template <int D>
-__global__ void __launch_bounds__(DecStateCfg<D>::THREADS, 1)
+__global__ void __launch_bounds__(DecStateCfg<D>::THREADS, 2)
 decay_state_kernel(const __grid_constant__ DecayStateArgs args, const DecayShape sh, const int32_t* __restrict__ cu,
                    const float* __restrict__ log_decay, int* status) {
     using C = DecStateCfg<D>;
@@ -176,8 +182,8 @@ decay_state_kernel(const __grid_constant__ DecayStateArgs args, const DecayShape
     }
     const int tid = threadIdx.x, warp = warp_uniform(tid >> 5), lane = tid & 31;
     const int head = blockIdx.x % sh.heads, kind = blockIdx.y, back = args.back[kind];
-    const Segment g = find_segment(cu, sh, blockIdx.x / sh.heads, status);
-    if (g.seq < 0 || (back ? g.first : g.last)) return;
+    const Piece g = find_piece(cu, sh, sh.part, blockIdx.x / sh.heads, status);
+    if (g.seq < 0 || (back ? g.off < sh.seg : g.rest <= sh.seg - g.off % sh.seg)) return;
     DecStateBars<D>* bars = reinterpret_cast<DecStateBars<D>*>(smem + C::BAR_OFF);
     volatile int* abort_flag = &bars->abort;
     if (tid == 0) {
@@ -192,7 +198,10 @@ decay_state_kernel(const __grid_constant__ DecayStateArgs args, const DecayShape
     tc_fence_after();
     const uint32_t tbase = warp_uniform(bars->tmem_base);
     auto fail = [&]() { *abort_flag = 1; report(status, kStatusTimeout); };
+    // steps of 64 tokens, against the direction of decay_out_kernel's walk: what
+    // that reads first is what this one read last, and still in L2
     const int n = warp_uniform((g.len + 63) / 64);
+    auto token_of = [&](int t) { return 64 * (back ? t : n - 1 - t); };
     if (warp == 8) {
         if (elect_one()) {
             constexpr uint32_t id = idesc_bf16_f32(128, D, true, true);
@@ -202,8 +211,8 @@ decay_state_kernel(const __grid_constant__ DecayStateArgs args, const DecayShape
                 uint64_t* bar = &bars->full[t % C::NST];
                 mbar_arrive_expect_tx(bar, 2 * C::TILE);
                 for (int c = 0; c < C::NCH; ++c) {
-                    tma_load_3d(st + c * C::CHUNK, &args.b[kind], bar, 64 * c, head, g.begin + 64 * t);
-                    tma_load_3d(st + C::TILE + c * C::CHUNK, &args.c[kind], bar, 64 * c, head, g.begin + 64 * t);
+                    tma_load_3d(st + c * C::CHUNK, &args.b[kind], bar, 64 * c, head, g.begin + token_of(t));
+                    tma_load_3d(st + C::TILE + c * C::CHUNK, &args.c[kind], bar, 64 * c, head, g.begin + token_of(t));
                 }
                 ++issued;
             };
@@ -245,7 +254,7 @@ decay_state_kernel(const __grid_constant__ DecayStateArgs args, const DecayShape
             uint8_t* st = smem + (t % C::NST) * C::STAGE;
 #pragma unroll
             for (int u = tid; u < C::TILE / 16; u += 256) {
-                const int r = 64 * t + (u & 511) / 8;    // token of the segment
+                const int r = token_of(t) + (u & 511) / 8;   // token of the part
                 uint4 x = *reinterpret_cast<const uint4*>(st + u * 16), lo;
                 if (r < g.len) {
                     split8(x, w0 * ex2((float)(back ? r + 1 : g.len - 1 - r) * l2), lo);
@@ -263,7 +272,7 @@ decay_state_kernel(const __grid_constant__ DecayStateArgs args, const DecayShape
         if (!ok) fail();
         tc_fence_after();
         const int row = 32 * (warp & 3) + lane, hf = warp >> 2;   // feature of b (d = 64: of hi, lo), half of c's
-        const long long slot = (back ? g.begin - sh.seg : g.begin) / sh.seg;
+        const long long slot = (back ? g.begin - sh.part : g.begin) / sh.part;
         float* dst = args.border[kind] + (slot * sh.heads + head) * D * D;
         float x[D / 2];
         if (ok) {
@@ -285,10 +294,19 @@ decay_state_kernel(const __grid_constant__ DecayStateArgs args, const DecayShape
                 for (int c = 0; c < 32; ++c) x[c] += half[c * 64];
             }
         }
-        if (ok && row < D) {
+        if (ok && row < D) {                             // (whole warps)
 #pragma unroll
-            for (int c = 0; c < D / 2; c += 4)
-                *reinterpret_cast<float4*>(dst + (long long)row * D + hf * (D / 2) + c) = make_float4(x[c], x[c + 1], x[c + 2], x[c + 3]);
+            for (int c = 0; c < D / 2; c += 16) {
+                uint4 u[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    u[e] = make_uint4(__float_as_uint(x[c + 4 * e]), __float_as_uint(x[c + 4 * e + 1]), __float_as_uint(x[c + 4 * e + 2]),
+                                      __float_as_uint(x[c + 4 * e + 3]));
+                transpose_units(u, lane);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    *reinterpret_cast<uint4*>(dst + (long long)((row & ~3) + e) * D + hf * (D / 2) + c + (lane & 3) * 4) = u[e];
+            }
         }
     }
     tc_fence_before();
@@ -311,29 +329,31 @@ decay_scan_kernel(const __grid_constant__ DecayScanArgs args, const DecayShape s
                   const float* __restrict__ log_decay, int* status) {
     const int head = blockIdx.x % sh.heads, seq = blockIdx.x / sh.heads, kind = blockIdx.z;
     const SeqRange r = seq_range(cu, seq, sh.total, status);
-    const int n = (r.len + sh.seg - 1) / sh.seg - 1;     // borders
-    if (n < 1) return;
+    if (r.len <= sh.seg) return;
+    const int back = args.back[kind];
+    const int per = sh.seg / sh.part, parts = (r.len + sh.part - 1) / sh.part;
+    // border b lies behind part b: forward those up to the last segment's, backwards from the last one down to the first segment's
+    const int n = back ? parts - per : (r.len - 1) / sh.seg * per, b0 = back ? parts - 2 : 0;
     const int e = (blockIdx.y * 256 + threadIdx.x) * 4;
     const float l2 = decay_log2(log_decay, head);
-    const int back = args.back[kind];
-    const float full = ex2((float)sh.seg * l2);
+    const float full = ex2((float)sh.part * l2);
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
     if (args.first[kind]) s = __ldg(reinterpret_cast<const float4*>(args.first[kind] + ((long long)seq * sh.heads + head) * D * D + e));
-    const int tail = r.len - n * sh.seg;                 // tokens of the last segment
+    const int tail = r.len - (parts - 1) * sh.part;      // tokens of the last part
     const long long step = (long long)sh.heads * D * D;
-    float* base = args.border[kind] + (r.begin / sh.seg) * step + (long long)head * D * D + e;    // border 0
+    float* base = args.border[kind] + (r.begin / sh.part) * step + (long long)head * D * D + e;   // border 0
     constexpr int AHEAD = 8;
     for (int i0 = 0; i0 < n; i0 += AHEAD) {
         float4 u[AHEAD];
 #pragma unroll
         for (int j = 0; j < AHEAD; ++j)
-            if (i0 + j < n) u[j] = *reinterpret_cast<const float4*>(base + (back ? n - 1 - i0 - j : i0 + j) * step);
+            if (i0 + j < n) u[j] = *reinterpret_cast<const float4*>(base + (back ? b0 - i0 - j : i0 + j) * step);
 #pragma unroll
         for (int j = 0; j < AHEAD; ++j) {
             if (i0 + j >= n) break;
             const float f = back && i0 + j == 0 ? ex2((float)tail * l2) : full;
             s.x = fmaf(f, s.x, u[j].x); s.y = fmaf(f, s.y, u[j].y); s.z = fmaf(f, s.z, u[j].z); s.w = fmaf(f, s.w, u[j].w);
-            *reinterpret_cast<float4*>(base + (back ? n - 1 - i0 - j : i0 + j) * step) = s;
+            *reinterpret_cast<float4*>(base + (back ? b0 - i0 - j : i0 + j) * step) = s;
         }
     }
 }
@@ -349,6 +369,8 @@ struct DecOutCfg {
     static constexpr int AC_OFF = NB * TILE;
     static constexpr int LO_OFF = (NB + NAC) * TILE;     // lo part of the weighted operand (hi in its tile's place)
     static constexpr int X_OFF = LO_OFF + TILE;          // the state as bf16: 128 rows (d = 64: hi rows, lo rows) x D
+    static constexpr int UNITS = 4 * NCH;                // 16-byte units of the weighted operand per thread pair,
+    static constexpr int UNITS_P = D == 128 ? 5 : 2;     // of which the score warps split so many
     static constexpr int POW_OFF = X_OFF + TILE;         // 64 floats: powers of lam, see the weights
     static constexpr int BAR_OFF = POW_OFF + 256;
     static constexpr int SMEM = BAR_OFF + 512;
@@ -384,16 +406,17 @@ decay_out_kernel(const __grid_constant__ DecayPasses passes, const int n_passes,
     const DecayPass& ps = passes.p[blockIdx.x % n_passes];
     const int item = blockIdx.x / n_passes, head = item % sh.heads;
     const bool back = ps.back;
-    const Segment g = find_segment(cu, sh, item / sh.heads, status);
+    const Piece g = find_piece(cu, sh, sh.seg, item / sh.heads, status);
     if (g.seq < 0) return;
+    const bool g_first = g.off == 0, g_last = g.rest <= sh.seg;
     const int n = warp_uniform((g.len + 127) / 128);                   // chunks; step t is chunk t, or n - 1 - t backwards
     auto chunk_of = [&](int t) { return back ? n - 1 - t : t; };
     const long long own = ((long long)g.seq * sh.heads + head) * D * D;
-    const bool ends = back ? g.first : g.last;           // this CTA reaches the end of the walk
+    const bool ends = back ? g_first : g_last;           // this CTA reaches the end of the walk
     float* last = ends && ps.last ? ps.last + own : nullptr;
     const float* x0 = nullptr;                           // the state before step 0
-    if (back ? g.last : g.first) x0 = ps.first ? ps.first + own : nullptr;
-    else x0 = ps.border + ((long long)(back ? g.begin : g.begin - sh.seg) / sh.seg * sh.heads + head) * D * D;
+    if (back ? g_last : g_first) x0 = ps.first ? ps.first + own : nullptr;
+    else x0 = ps.border + ((long long)((back ? g.begin + sh.seg : g.begin) - sh.part) / sh.part * sh.heads + head) * D * D;
     if (n == 0) {                                        // an empty sequence: the state goes through
         if (last)
             for (int e = tid; e < D * D; e += C::THREADS) last[e] = x0 ? x0[e] : 0.f;
@@ -413,7 +436,7 @@ decay_out_kernel(const __grid_constant__ DecayPasses passes, const int n_passes,
         mbar_init(&bars->s_full, 1);
         mbar_init(&bars->p_ready, 256);
         mbar_init(&bars->x_ready, 256);
-        mbar_init(&bars->w_ready, 256);
+        mbar_init(&bars->w_ready, 512);
         mbar_init(&bars->o_full, 1);
         mbar_init(&bars->o_free, 128);
         mbar_init(&bars->u_done, 1);
@@ -434,6 +457,24 @@ decay_out_kernel(const __grid_constant__ DecayPasses passes, const int n_passes,
     auto ac_slot = [&](int i) { return smem + C::AC_OFF + (i % C::NAC) * C::TILE; };
     auto ac_wait = [&](int i) { return mma_wait(&bars->ac_full[i % C::NAC], (i / C::NAC) & 1, abort_flag); };
 
+    // hi and lo of B w for the units [i0, i1) of this one of 256 threads
+    auto split_units = [&](int t, int id, int i0, int i1, int rows) {
+        if (!__all_sync(0xffffffffu, b_wait(t))) return false;     // (long done: the scores are)
+        uint8_t* b = b_slot(t);
+#pragma unroll
+        for (int i = i0; i < i1; ++i) {
+            const int r = id / 8 + 32 * (i & 3);         // token of the chunk
+            uint4 y = *reinterpret_cast<const uint4*>(b + id * 16 + 4096 * i), lo;
+            split8(y, ps.w_scale * ex2((float)(back ? r + 1 : rows - 1 - r) * l2), lo);
+            if (r >= rows) y = lo = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(b + id * 16 + 4096 * i) = y;
+            *reinterpret_cast<uint4*>(sLo + id * 16 + 4096 * i) = lo;
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(&bars->w_ready);
+        return true;
+    };
+
     if (warp >= 20) {
       reg_dec<C::REG_LOAD>();
       if (warp == 20) {
@@ -445,8 +486,7 @@ decay_out_kernel(const __grid_constant__ DecayPasses passes, const int n_passes,
             auto load = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* full, int t) {
                 const int row = g.begin + 128 * chunk_of(t);
                 mbar_arrive_expect_tx(full, C::TILE);
-                for (int c = 0; c < 2 * C::NCH; ++c)     // boxes of 64 tokens x 64 features
-                    tma_load_3d(dst + c * 8192, map, full, 64 * (c >> 1), head, row + 64 * (c & 1));
+                for (int c = 0; c < C::NCH; ++c) tma_load_3d(dst + c * C::CHUNK, map, full, 64 * c, head, row);
             };
             auto load_ac = [&](const CUtensorMap* map, int t) {
                 const int x = nac % C::NAC;
@@ -477,7 +517,6 @@ decay_out_kernel(const __grid_constant__ DecayPasses passes, const int n_passes,
             constexpr uint32_t id_x = idesc_bf16_f32(128, D, true, true);
             const uint32_t lo = smem_u32(sLo), xs = smem_u32(sX);
             auto issue_s = [&](int t) {
-                if (!b_wait(t) || !ac_wait(2 * t)) return false;
                 tc_fence_after();
                 const uint32_t b = smem_u32(b_slot(t)), a = smem_u32(ac_slot(2 * t));
 #pragma unroll
@@ -486,9 +525,9 @@ decay_out_kernel(const __grid_constant__ DecayPasses passes, const int n_passes,
                     mma_bf16_ss(tbase + C::S_COL, smem_desc_sw128(a + o, 16, 1024), smem_desc_sw128(b + o, 16, 1024), id_s, kk > 0);
                 }
                 mma_commit(&bars->s_full);
-                return true;
             };
-            bool ok = issue_s(0);
+            bool ok = b_wait(0) && ac_wait(0);
+            if (ok) issue_s(0);
             for (int t = 0; t < n && ok; ++t) {
                 const uint32_t b = smem_u32(b_slot(t)), a = smem_u32(ac_slot(2 * t)), c = smem_u32(ac_slot(2 * t + 1));
                 // O1 = P C
@@ -511,24 +550,35 @@ decay_out_kernel(const __grid_constant__ DecayPasses passes, const int n_passes,
                 }
                 mma_commit(&bars->o_full);
                 mma_commit(&bars->ac_empty[(2 * t) % C::NAC]);
-                if (t + 1 < n && !(ok = issue_s(t + 1))) break;
-                if (t < updates) {
-                    // U = (B w)^T C
-                    if (!(ok = mma_wait(&bars->w_ready, t & 1, abort_flag))) break;
-                    tc_fence_after();
+                // the scores of step t + 1 and U of step t, as their inputs arrive
+                bool s_next = t + 1 < n, u_next = t < updates;
+                const unsigned long long t0 = clock64();
+                while (s_next || u_next) {
+                    if (s_next && mbar_test_wait(&bars->b_full[(t + 1) % C::NB], ((t + 1) / C::NB) & 1) &&
+                               mbar_test_wait(&bars->ac_full[(2 * t + 2) % C::NAC], ((2 * t + 2) / C::NAC) & 1)) {
+                        issue_s(t + 1);
+                        s_next = false;
+                    } else if (u_next && mbar_test_wait(&bars->w_ready, t & 1)) {
+                        tc_fence_after();
+                        // U = (B w)^T C
 #pragma unroll
-                    for (int kk = 0; kk < 8; ++kk) {
-                        const uint64_t cd = smem_desc_sw128(c + kk * 2048, C::CHUNK, 1024);
-                        if (D == 128) {
-                            mma_bf16_ss(tbase + C::U_COL, smem_desc_sw128(b + kk * 2048, C::CHUNK, 1024), cd, id_x, kk > 0);
-                            mma_bf16_ss(tbase + C::U_COL, smem_desc_sw128(lo + kk * 2048, C::CHUNK, 1024), cd, id_x, 1);
-                        } else {
-                            mma_bf16_ss(tbase + C::U_COL, smem_desc_sw128(b + kk * 2048, lo - b, 1024), cd, id_x, kk > 0);
+                        for (int kk = 0; kk < 8; ++kk) {
+                            const uint64_t cd = smem_desc_sw128(c + kk * 2048, C::CHUNK, 1024);
+                            if (D == 128) {
+                                mma_bf16_ss(tbase + C::U_COL, smem_desc_sw128(b + kk * 2048, C::CHUNK, 1024), cd, id_x, kk > 0);
+                                mma_bf16_ss(tbase + C::U_COL, smem_desc_sw128(lo + kk * 2048, C::CHUNK, 1024), cd, id_x, 1);
+                            } else {
+                                mma_bf16_ss(tbase + C::U_COL, smem_desc_sw128(b + kk * 2048, lo - b, 1024), cd, id_x, kk > 0);
+                            }
                         }
+                        mma_commit(&bars->u_done);
+                        mma_commit(&bars->b_empty[t % C::NB]);
+                        mma_commit(&bars->ac_empty[(2 * t + 1) % C::NAC]);
+                        u_next = false;
+                    } else if (*abort_flag || clock64() - t0 > VSA_WAIT_LIMIT_CYCLES) {
+                        ok = false;
+                        break;
                     }
-                    mma_commit(&bars->u_done);
-                    mma_commit(&bars->b_empty[t % C::NB]);
-                    mma_commit(&bars->ac_empty[(2 * t + 1) % C::NAC]);
                 }
             }
             if (!ok) fail();
@@ -592,6 +642,11 @@ decay_out_kernel(const __grid_constant__ DecayPasses passes, const int n_passes,
             tmem_wait_st();
             tc_fence_before();
             mbar_arrive(&bars->p_ready);
+            if (t < updates) {
+                // the products that read the last step's lo part have finished
+                if (t > 0 && !__all_sync(0xffffffffu, mbar_wait(&bars->u_done, (t - 1) & 1, abort_flag))) { ok = false; break; }
+                if (!split_units(t, tid, 0, C::UNITS_P, rows)) { ok = false; break; }
+            }
         }
         if (!ok) fail();
     } else if (warp >= 16) {
@@ -659,17 +714,6 @@ decay_out_kernel(const __grid_constant__ DecayPasses passes, const int n_passes,
 #pragma unroll
             for (int c = 0; c < D / 2; ++c) x[c] = 0.f;
         }
-        // weights of this thread's tokens in a chunk of `rows`
-        float w[4];
-        int w_rows = 0;
-        auto set_weights = [&](int rows) {
-            w_rows = rows;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = id / 8 + 32 * i;
-                w[i] = ps.w_scale * ex2((float)(back ? r + 1 : rows - 1 - r) * l2);
-            }
-        };
         // X = lam^tokens X + U, once the products of step t have finished
         auto update = [&](int t) {
             if (!__all_sync(0xffffffffu, mbar_wait(&bars->u_done, t & 1, abort_flag))) return false;
@@ -688,7 +732,7 @@ decay_out_kernel(const __grid_constant__ DecayPasses passes, const int n_passes,
         };
         for (int t = 0; t < n; ++t) {
             const int tok = 128 * chunk_of(t), rows = min(128, g.len - tok);
-            if (t > 0 && !update(t - 1)) { ok = false; break; }    // then the scores of step t have finished too
+            if (t > 0 && !update(t - 1)) { ok = false; break; }
             uint8_t* xr = sX + row * 128;
 #pragma unroll
             for (int c = 0; c < D / 2; c += 8) {
@@ -697,27 +741,11 @@ decay_out_kernel(const __grid_constant__ DecayPasses passes, const int n_passes,
                     make_uint4(pack_bf16x2(x[c], x[c + 1]), pack_bf16x2(x[c + 2], x[c + 3]), pack_bf16x2(x[c + 4], x[c + 5]),
                                pack_bf16x2(x[c + 6], x[c + 7]));
             }
-            if (t == 0 && !__all_sync(0xffffffffu, mbar_wait(&bars->s_full, 0, abort_flag))) { ok = false; break; }
+            // (before x_ready: step t + 1's scores wait for that, so this phase cannot be missed)
+            if (!__all_sync(0xffffffffu, mbar_wait(&bars->s_full, t & 1, abort_flag))) { ok = false; break; }
             fence_proxy_async_smem();
             mbar_arrive(&bars->x_ready);
-            if (t < updates) {
-                if (!__all_sync(0xffffffffu, b_wait(t))) { ok = false; break; }   // (long done: the scores are)
-                uint8_t* b = b_slot(t);
-                if (rows != w_rows) set_weights(rows);
-#pragma unroll 1
-                for (int o = id * 16; o < C::TILE; o += C::CHUNK) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {        // a 16-byte unit of token id / 8 + 32 i
-                        uint4 y = *reinterpret_cast<const uint4*>(b + o + 4096 * i), lo;
-                        split8(y, w[i], lo);
-                        if (rows < 128 && id / 8 + 32 * i >= rows) y = lo = make_uint4(0, 0, 0, 0);
-                        *reinterpret_cast<uint4*>(b + o + 4096 * i) = y;
-                        *reinterpret_cast<uint4*>(sLo + o + 4096 * i) = lo;
-                    }
-                }
-                fence_proxy_async_smem();
-                mbar_arrive(&bars->w_ready);
-            }
+            if (t < updates && !split_units(t, id, C::UNITS_P, C::UNITS, rows)) { ok = false; break; }
         }
         if (last) {
             if (ok && !update(n - 1)) ok = false;
@@ -757,66 +785,80 @@ decay_out_kernel(const __grid_constant__ DecayPasses passes, const int n_passes,
 
 // --------------------------------------------------------------------- launch
 
-// Chunks of a segment for `walks` scans (heads x passes) over the sequences,
-// whose lengths only the device knows: the m that makes ceil(CTAs / 148)
-// rounds of m chunks (and the launch's fixed part) shortest, all in one
-// sequence assumed.
-static int segment_chunks(int total, int n_seq, long long walks) {
+// How the sequences are cut, whose lengths only the device knows: m chunks to
+// a segment.  Times in units of one chunk of decay_out_kernel, which takes 0.75
+// of the time at which all SMs together reach the memory's bandwidth (so 111
+// walking CTAs saturate it); 2.5 of them are a CTA's start and end, 0.5 is a
+// chunk's share of the border sums' reading (two of four tensors), 3 the two
+// further launches.  The sequences are taken to be at most 2.5 times the
+// average (a longer one is cut, the rest are not).  With several passes over
+// the same tensors, segments small enough for the running ones to stay in L2
+// (some 80 MB) spare reading them again.
+static DecayShape decay_shape(int n_seq, int total, int heads, int d, int passes) {
     const long long chunks = std::max(1ll, ((long long)total + 127) / 128);
-    long long best = chunks;
+    const long long longest = n_seq == 1 ? chunks : std::min(chunks, (5 * chunks + 2 * n_seq - 1) / (2 * n_seq));
+    const double walks = (double)heads * passes, kinds = passes > 1 ? 2 : 1;
+    long long best = longest;
     double best_cost = 1e300;
-    for (long long m = 1; m <= chunks; m = m < 64 ? m + 1 : m + m / 32) {
-        const long long segs = (chunks + m - 1) / m + (n_seq - 1);
-        const double rounds = (double)((segs * walks + 147) / 148);
-        const double cost = rounds * (m + 2.0) + (m < chunks ? 4.0 : 0.0);
+    for (long long m = 1; m <= longest; m = m < 64 ? m + 1 : std::min(m + m / 32, m < longest ? longest : m + 1)) {
+        const double segs = n_seq == 1 ? (double)((chunks + m - 1) / m) : (double)chunks / m + (m < longest ? 0.5 : 0.0) * n_seq;
+        const double rounds = std::ceil(std::max(segs, (double)n_seq) * walks / 148);
+        const double tile = 128.0 * d * 2, set = std::min(148.0, segs * walks) / passes * 4 * tile * m;
+        const double per_pass = passes == 1 ? 1.0 : set < 80e6 ? 7.0 / 12 : 10.0 / 12;
+        double cost = std::max(rounds * (m + 2.5) * 0.75, chunks * walks / 148 * per_pass);
+        if (m < longest) cost += 0.55 * kinds * heads * chunks / 148 * (1.0 - (double)m / longest) + 3.0;
         if (cost < best_cost) { best_cost = cost; best = m; }
     }
-    return (int)best;
+    // parts: two CTAs per SM, at least 4 chunks each
+    long long parts = 1;
+    for (long long k = 2; k <= std::min(best / 4, 64ll); ++k) {
+        if (best % k) continue;
+        if ((double)chunks / (best / parts) * heads * kinds >= 4 * 296) break;
+        parts = k;
+    }
+    return {n_seq, total, heads, (int)(128 * best), (int)(128 * (best / parts))};
 }
 
-static DecayShape decay_shape(int n_seq, int total, int heads, int passes) {
-    return {n_seq, total, heads, 128 * segment_chunks(total, n_seq, (long long)heads * passes)};
-}
-
-static long long decay_segments(const DecayShape& s) { return (long long)s.total / s.seg + s.n_seq; }
-
-static size_t border_bytes(const DecayShape& s, int d) { return (size_t)(s.total / s.seg) * s.heads * d * d * sizeof(float); }
+static size_t border_bytes(const DecayShape& s, int d) { return (size_t)(s.total / s.part) * s.heads * d * d * sizeof(float); }
 
 long long decay_work_items(int n_seq, int total, int heads) { return 3 * ((long long)total / 128 + n_seq) * heads; }
 
 size_t decay_scratch_bytes(int n_seq, int total, int heads, int d) {
-    return std::max(border_bytes(decay_shape(n_seq, total, heads, 1), d), 2 * border_bytes(decay_shape(n_seq, total, heads, 3), d));
+    return std::max(border_bytes(decay_shape(n_seq, total, heads, d, 1), d), 2 * border_bytes(decay_shape(n_seq, total, heads, d, 3), d));
 }
 
-static bool decay_map(CUtensorMap* m, const PackedTensor& t, const DecayArgs& a) {
-    return a.total == 0 || encode_packed_map(m, t, a.total, a.heads, a.d, 1, 64, a.enc);
+static bool decay_map(CUtensorMap* m, const PackedTensor& t, const DecayArgs& a, int box_rows) {
+    return a.total == 0 || encode_packed_map(m, t, a.total, a.heads, a.d, 1, box_rows, a.enc);
 }
 
 template <int D>
 static cudaError_t launch_decay(const DecayArgs& a, const DecayShape& sh, const DecayPasses& passes, int n_passes,
                                 const DecayStateArgs& st, const DecayScanArgs& sc, int kinds, cudaStream_t stream) {
-    const unsigned items = (unsigned)(decay_segments(sh) * a.heads);
+    const unsigned segs = (unsigned)(((long long)sh.total / sh.seg + sh.n_seq) * a.heads);
+    const unsigned parts = (unsigned)(((long long)sh.total / sh.part + sh.n_seq) * a.heads);
     cudaError_t e = cudaFuncSetAttribute(decay_out_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, DecOutCfg<D>::SMEM);
     if (e != cudaSuccess) return e;
     if (a.total > sh.seg) {                              // some sequence may have several segments
         e = cudaFuncSetAttribute(decay_state_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, DecStateCfg<D>::SMEM);
         if (e != cudaSuccess) return e;
-        decay_state_kernel<D><<<dim3(items, kinds), DecStateCfg<D>::THREADS, DecStateCfg<D>::SMEM, stream>>>(st, sh, a.cu, a.log_decay, a.status);
+        decay_state_kernel<D><<<dim3(parts, kinds), DecStateCfg<D>::THREADS, DecStateCfg<D>::SMEM, stream>>>(st, sh, a.cu, a.log_decay, a.status);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
         decay_scan_kernel<D><<<dim3((unsigned)((long long)a.n_seq * a.heads), D * D / 1024, kinds), 256, 0, stream>>>(sc, sh, a.cu, a.log_decay, a.status);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
-    decay_out_kernel<D><<<items * n_passes, DecOutCfg<D>::THREADS, DecOutCfg<D>::SMEM, stream>>>(passes, n_passes, sh, a.cu, a.log_decay, a.status);
+    decay_out_kernel<D><<<segs * n_passes, DecOutCfg<D>::THREADS, DecOutCfg<D>::SMEM, stream>>>(passes, n_passes, sh, a.cu, a.log_decay, a.status);
     return cudaGetLastError();
 }
 
 cudaError_t launch_decay_fwd(const DecayArgs& a, cudaStream_t stream) {
-    const DecayShape sh = decay_shape(a.n_seq, a.total, a.heads, 1);
+    const DecayShape sh = decay_shape(a.n_seq, a.total, a.heads, a.d, 1);
     float* border = reinterpret_cast<float*>(a.scratch);
     DecayPasses ps{};
     DecayStateArgs st{};
     DecayPass& p = ps.p[0];
-    if (!decay_map(&p.a, a.q, a) || !decay_map(&p.b, a.k, a) || !decay_map(&p.c, a.v, a)) return cudaErrorInvalidValue;
+    if (!decay_map(&p.a, a.q, a, 128) || !decay_map(&p.b, a.k, a, 128) || !decay_map(&p.c, a.v, a, 128) ||
+        !decay_map(&st.b[0], a.k, a, 64) || !decay_map(&st.c[0], a.v, a, 64))
+        return cudaErrorInvalidValue;
     p.out = static_cast<__nv_bfloat16*>(a.out.p);
     p.out_stride = a.out.stride;
     p.first = a.state_in;
@@ -824,8 +866,6 @@ cudaError_t launch_decay_fwd(const DecayArgs& a, cudaStream_t stream) {
     p.border = border;
     p.w_scale = 1.f;
     p.p_scale = p.s_scale = a.scale;
-    st.b[0] = p.b;
-    st.c[0] = p.c;
     st.border[0] = border;
     st.w_scale[0] = 1.f;
     DecayScanArgs sc{};
@@ -835,10 +875,13 @@ cudaError_t launch_decay_fwd(const DecayArgs& a, cudaStream_t stream) {
 }
 
 cudaError_t launch_decay_bwd(const DecayArgs& a, cudaStream_t stream) {
-    const DecayShape sh = decay_shape(a.n_seq, a.total, a.heads, 3);
+    const DecayShape sh = decay_shape(a.n_seq, a.total, a.heads, a.d, 3);
     float* border[2] = {reinterpret_cast<float*>(a.scratch), reinterpret_cast<float*>(a.scratch + border_bytes(sh, a.d))};
     CUtensorMap mq, mk, mv, mg;
-    if (!decay_map(&mq, a.q, a) || !decay_map(&mk, a.k, a) || !decay_map(&mv, a.v, a) || !decay_map(&mg, a.dout, a))
+    DecayStateArgs st{};
+    if (!decay_map(&mq, a.q, a, 128) || !decay_map(&mk, a.k, a, 128) || !decay_map(&mv, a.v, a, 128) || !decay_map(&mg, a.dout, a, 128) ||
+        !decay_map(&st.b[0], a.k, a, 64) || !decay_map(&st.c[0], a.v, a, 64) || !decay_map(&st.b[1], a.q, a, 64) ||
+        !decay_map(&st.c[1], a.dout, a, 64))
         return cudaErrorInvalidValue;
     auto pass = [&](const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mc, const PackedTensor& out, bool back, bool trans) {
         DecayPass p{};
@@ -860,9 +903,8 @@ cudaError_t launch_decay_bwd(const DecayArgs& a, cudaStream_t stream) {
     ps.p[1] = pass(mv, mg, mq, a.dk, true, true);
     ps.p[2] = pass(mk, mq, mg, a.dv, true, false);
     ps.p[2].last = a.dstate_in;
-    DecayStateArgs st{};
-    st.b[0] = mk; st.c[0] = mv; st.w_scale[0] = 1.f;
-    st.b[1] = mq; st.c[1] = mg; st.w_scale[1] = a.scale;
+    st.w_scale[0] = 1.f;
+    st.w_scale[1] = a.scale;
     DecayScanArgs sc{};
     sc.first[0] = a.state_in;
     sc.first[1] = a.dstate_out;
