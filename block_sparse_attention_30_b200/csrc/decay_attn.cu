@@ -371,8 +371,8 @@ struct DecOutCfg {
     static constexpr int X_OFF = LO_OFF + TILE;          // the state as bf16: 128 rows (d = 64: hi rows, lo rows) x D
     static constexpr int UNITS = 4 * NCH;                // 16-byte units of the weighted operand per thread pair,
     static constexpr int UNITS_P = D == 128 ? 5 : 2;     // of which the score warps split so many
-    static constexpr int POW_OFF = X_OFF + TILE;         // 64 floats: powers of lam, see the weights
-    static constexpr int BAR_OFF = POW_OFF + 256;
+    static constexpr int POW_OFF = X_OFF + TILE;         // powers of lam, see the weights: 64 floats, and again one float on
+    static constexpr int BAR_OFF = POW_OFF + 2 * 256 + 16;
     static constexpr int SMEM = BAR_OFF + 512;
     static constexpr int THREADS = 768;                  // warpgroups: 2 scores, 2 state, outputs, loads and MMAs; 80 registers a thread
     static constexpr int REG_SCORE = 72, REG_STATE = 104, REG_OUT = 80, REG_LOAD = 48;   // 2 * 72 + 2 * 104 + 80 + 48 = 6 * 80
@@ -382,9 +382,9 @@ static_assert(DecOutCfg<128>::SMEM <= 232448 && DecOutCfg<64>::SMEM <= 232448, "
 
 template <int D>
 struct DecOutBars {
-    uint64_t b_full[DecOutCfg<D>::NB], b_empty[DecOutCfg<D>::NB];
-    uint64_t ac_full[DecOutCfg<D>::NAC], ac_empty[DecOutCfg<D>::NAC];
-    uint64_t s_full, p_ready, x_ready, w_ready, o_full, o_free, u_done, mma_done;
+    uint64_t b_full[DecOutCfg<D>::NB], ac_full[DecOutCfg<D>::NAC];
+    uint64_t u_done[DecOutCfg<D>::NB];   // every product of a step in this slot of B
+    uint64_t s_full, p_ready, x_ready, w_ready, o_full, o_free, mma_done;
     uint32_t tmem_base;
     int abort;
 };
@@ -431,20 +431,23 @@ decay_out_kernel(const __grid_constant__ DecayPasses passes, const int n_passes,
     const float l2 = decay_log2(log_decay, head);
     if (tid == 0) {
         bars->abort = 0;
-        for (int x = 0; x < C::NB; ++x) { mbar_init(&bars->b_full[x], 1); mbar_init(&bars->b_empty[x], 1); }
-        for (int x = 0; x < C::NAC; ++x) { mbar_init(&bars->ac_full[x], 1); mbar_init(&bars->ac_empty[x], 1); }
+        for (int x = 0; x < C::NB; ++x) { mbar_init(&bars->b_full[x], 1); mbar_init(&bars->u_done[x], 1); }
+        for (int x = 0; x < C::NAC; ++x) mbar_init(&bars->ac_full[x], 1);
         mbar_init(&bars->s_full, 1);
         mbar_init(&bars->p_ready, 256);
         mbar_init(&bars->x_ready, 256);
         mbar_init(&bars->w_ready, 512);
         mbar_init(&bars->o_full, 1);
         mbar_init(&bars->o_free, 128);
-        mbar_init(&bars->u_done, 1);
         mbar_init(&bars->mma_done, 1);
         fence_barrier_init();
     }
     // forward lam^31 .. lam^0 and zeros, backwards zeros and lam^0 .. lam^31
-    if (tid < 64) sPow[tid] = (back ? tid >= 32 : tid < 32) ? ex2((float)(back ? tid - 32 : 31 - tid) * l2) : 0.f;
+    if (tid < 64) {
+        const float y = (back ? tid >= 32 : tid < 32) ? ex2((float)(back ? tid - 32 : 31 - tid) * l2) : 0.f;
+        sPow[tid] = y;
+        sPow[64 + 1 + tid] = y;                          // for pairs that start at an odd place
+    }
     if (warp == 21) { tmem_alloc(&bars->tmem_base, 512); tmem_relinquish(); }
     tc_fence_before();
     __syncthreads();
@@ -456,6 +459,7 @@ decay_out_kernel(const __grid_constant__ DecayPasses passes, const int n_passes,
     auto b_wait = [&](int t) { return mma_wait(&bars->b_full[t % C::NB], (t / C::NB) & 1, abort_flag); };
     auto ac_slot = [&](int i) { return smem + C::AC_OFF + (i % C::NAC) * C::TILE; };
     auto ac_wait = [&](int i) { return mma_wait(&bars->ac_full[i % C::NAC], (i / C::NAC) & 1, abort_flag); };
+    auto u_wait = [&](int t) { return mbar_wait(&bars->u_done[t % C::NB], (t / C::NB) & 1, abort_flag); };
 
     // hi and lo of B w for the units [i0, i1) of this one of 256 threads
     auto split_units = [&](int t, int id, int i0, int i1, int rows) {
@@ -480,8 +484,9 @@ decay_out_kernel(const __grid_constant__ DecayPasses passes, const int n_passes,
       if (warp == 20) {
         if (elect_one()) {
             // ---------------------------------------------------------- loads
-            // in the order in which slots are freed: C of step t + 1 follows
-            // A of step t, B and A of step t + 2 follow the update of step t
+            // When step t - NB has finished, so has what was in the slots of
+            // B and A (d = 64: and C) of step t; at d = 128 C takes the slot
+            // of A of step t - 1, free with that step's outputs.
             int nb = 0, nac = 0;
             auto load = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* full, int t) {
                 const int row = g.begin + 128 * chunk_of(t);
@@ -489,19 +494,18 @@ decay_out_kernel(const __grid_constant__ DecayPasses passes, const int n_passes,
                 for (int c = 0; c < C::NCH; ++c) tma_load_3d(dst + c * C::CHUNK, map, full, 64 * c, head, row);
             };
             auto load_ac = [&](const CUtensorMap* map, int t) {
-                const int x = nac % C::NAC;
-                if (nac >= C::NAC && !mbar_wait(&bars->ac_empty[x], (nac / C::NAC - 1) & 1, abort_flag)) return false;
-                load(ac_slot(nac), map, &bars->ac_full[x], t);
+                load(ac_slot(nac), map, &bars->ac_full[nac % C::NAC], t);
                 ++nac;
-                return true;
             };
+            static_assert(D == 128 ? C::NB == 2 && C::NAC == 3 : C::NAC == 2 * C::NB, "which products free a slot");
             bool ok = true;
             for (int t = 0; t < n && ok; ++t) {
-                const int x = t % C::NB;
-                if (t >= C::NB && !(ok = mbar_wait(&bars->b_empty[x], (t / C::NB - 1) & 1, abort_flag))) break;
-                load(b_slot(t), &ps.b, &bars->b_full[x], t);
+                if (t >= C::NB && !(ok = u_wait(t - C::NB))) break;
+                load(b_slot(t), &ps.b, &bars->b_full[t % C::NB], t);
                 ++nb;
-                ok = load_ac(&ps.a, t) && load_ac(&ps.c, t);
+                load_ac(&ps.a, t);
+                if (D == 128 && t > 0 && !(ok = mbar_wait(&bars->o_full, (t - 1) & 1, abort_flag))) break;
+                load_ac(&ps.c, t);
             }
             if (!ok) fail();
             if (*abort_flag) {
@@ -549,7 +553,6 @@ decay_out_kernel(const __grid_constant__ DecayPasses passes, const int n_passes,
                                 smem_desc_sw128(xs + kk * 2048, C::CHUNK, 1024), id_o, kk > 0);
                 }
                 mma_commit(&bars->o_full);
-                mma_commit(&bars->ac_empty[(2 * t) % C::NAC]);
                 // the scores of step t + 1 and U of step t, as their inputs arrive
                 bool s_next = t + 1 < n, u_next = t < updates;
                 const unsigned long long t0 = clock64();
@@ -571,9 +574,7 @@ decay_out_kernel(const __grid_constant__ DecayPasses passes, const int n_passes,
                                 mma_bf16_ss(tbase + C::U_COL, smem_desc_sw128(b + kk * 2048, lo - b, 1024), cd, id_x, kk > 0);
                             }
                         }
-                        mma_commit(&bars->u_done);
-                        mma_commit(&bars->b_empty[t % C::NB]);
-                        mma_commit(&bars->ac_empty[(2 * t + 1) % C::NAC]);
+                        mma_commit(&bars->u_done[t % C::NB]);
                         u_next = false;
                     } else if (*abort_flag || clock64() - t0 > VSA_WAIT_LIMIT_CYCLES) {
                         ok = false;
@@ -616,7 +617,8 @@ decay_out_kernel(const __grid_constant__ DecayPasses passes, const int n_passes,
                 uint32_t pk[16];
                 if (back ? blk >= quarter : blk <= quarter) {
                     const int far = blk == quarter ? 0 : back ? 32 * blk - r : r - 32 * blk - 31;
-                    const float* y = sPow + (blk == quarter ? (back ? 32 : 31) - lane : back ? 32 : 0);
+                    const int at = blk == quarter ? (back ? 32 : 31) - lane : back ? 32 : 0;
+                    const uint64_t* y = reinterpret_cast<const uint64_t*>(sPow + (at & 1 ? 64 + 1 + at : at));
                     const float f = ps.p_scale * ex2((float)far * l2);
                     float s[32];
                     tmem_ld_32x32b_x32(tS + 32 * h, s);
@@ -624,7 +626,7 @@ decay_out_kernel(const __grid_constant__ DecayPasses passes, const int n_passes,
                     const uint64_t f2 = f32x2(f, f);
 #pragma unroll
                     for (int e = 0; e < 32; e += 2)
-                        unf32x2(mul_f32x2(f32x2(s[e], s[e + 1]), mul_f32x2(f2, f32x2(y[e], y[e + 1]))), s[e], s[e + 1]);
+                        unf32x2(mul_f32x2(f32x2(s[e], s[e + 1]), mul_f32x2(f2, y[e / 2])), s[e], s[e + 1]);
                     if (rows < 128) {                    // scores of rows behind the sequence may be anything
                         const int lo = back && blk == quarter ? lane : 0;
                         const int hi = min(rows - 32 * blk, !back && blk == quarter ? lane + 1 : 32);
@@ -644,7 +646,7 @@ decay_out_kernel(const __grid_constant__ DecayPasses passes, const int n_passes,
             mbar_arrive(&bars->p_ready);
             if (t < updates) {
                 // the products that read the last step's lo part have finished
-                if (t > 0 && !__all_sync(0xffffffffu, mbar_wait(&bars->u_done, (t - 1) & 1, abort_flag))) { ok = false; break; }
+                if (t > 0 && !__all_sync(0xffffffffu, u_wait(t - 1))) { ok = false; break; }
                 if (!split_units(t, tid, 0, C::UNITS_P, rows)) { ok = false; break; }
             }
         }
@@ -716,7 +718,7 @@ decay_out_kernel(const __grid_constant__ DecayPasses passes, const int n_passes,
         }
         // X = lam^tokens X + U, once the products of step t have finished
         auto update = [&](int t) {
-            if (!__all_sync(0xffffffffu, mbar_wait(&bars->u_done, t & 1, abort_flag))) return false;
+            if (!__all_sync(0xffffffffu, u_wait(t))) return false;
             tc_fence_after();
             const float f = ex2((float)min(128, g.len - 128 * chunk_of(t)) * l2);
 #pragma unroll
