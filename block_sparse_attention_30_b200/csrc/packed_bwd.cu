@@ -190,7 +190,7 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
         if (threadIdx.x == 0) report(status, kStatusMisaligned);
         return;
     }
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = warp_uniform(tid >> 5), lane = tid & 31;
     const int group = sh.heads_q / sh.heads_kv;
     const int kvh = blockIdx.x % sh.heads_kv;
     // the last tiles of a sequence see the most keys: they start first
@@ -198,7 +198,7 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
     if (at.seq < 0) return;
     const SeqRange qr = seq_range(cu_q, at.seq, sh.total_q, status), kr = seq_range(cu_k, at.seq, sh.total_k, status);
     const int tok0 = at.tile * tok_per_tile;
-    const int n = (seen_keys(min(tok0 + tok_per_tile, qr.len) - 1, qr.len, kr.len, causal) + 127) / 128;   // key blocks
+    const int n = warp_uniform((seen_keys(min(tok0 + tok_per_tile, qr.len) - 1, qr.len, kr.len, causal) + 127) / 128);   // key blocks
     uint8_t* sQ = smem;
     uint8_t* sG = smem + C::TILE;
     uint8_t* sK = smem + 2 * C::TILE;                    // 3 slots: a K block is read by S and, two steps later, by dQ
@@ -210,12 +210,12 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tbase = bars->tmem_base;
+    const uint32_t tbase = warp_uniform(bars->tmem_base);
     const uint32_t tDP = tbase + 256, tAcc = tbase + 384;     // S of block j at 128 (j & 1)
     auto fail = [&]() { *abort_flag = 1; report(status, kStatusTimeout); };
 
     if (warp == 8) {
-        if (lane == 0 && n > 0) {
+        if (n > 0 && elect_one()) {
             mbar_arrive_expect_tx(&bars->own_full, 2 * C::NCH * tok_per_tile * group * 128);
             for (int c = 0; c < C::NCH; ++c) {
                 tma_load_3d(sQ + c * C::CHUNK, &mq, &bars->own_full, 64 * c, kvh * group, qr.begin + tok0);
@@ -246,7 +246,7 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
             }
         }
     } else if (warp == 9) {
-        if (lane == 0 && n > 0) {
+        if (n > 0 && elect_one()) {
             const uint32_t q = smem_u32(sQ), g = smem_u32(sG), k = smem_u32(sK), v = smem_u32(sV);
             auto issue_s = [&](int t) {
                 if (!mma_wait(&bars->x_full[t % 3], (t / 3) & 1, abort_flag)) return false;
@@ -362,7 +362,7 @@ packed_dkdv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
         if (threadIdx.x == 0) report(status, kStatusMisaligned);
         return;
     }
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = warp_uniform(tid >> 5), lane = tid & 31;
     const int group = sh.heads_q / sh.heads_kv;
     const int kvh = blockIdx.x % sh.heads_kv;
     // the first tiles of a sequence are seen by the most queries: they start first
@@ -374,7 +374,7 @@ packed_dkdv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
     // first query token that sees key0, and the blocks from its on
     const int tok_first = causal ? max(0, key0 + qr.len - kr.len) : 0;
     const int b0 = tok_first / tok_per_tile;
-    const int n = max(0, (qr.len + tok_per_tile - 1) / tok_per_tile - b0);
+    const int n = warp_uniform(max(0, (qr.len + tok_per_tile - 1) / tok_per_tile - b0));
     uint8_t* sK = smem;
     uint8_t* sV = smem + C::TILE;
     uint8_t* sQ = smem + 2 * C::TILE;                    // 2 slots
@@ -392,12 +392,12 @@ packed_dkdv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tbase = bars->tmem_base;
+    const uint32_t tbase = warp_uniform(bars->tmem_base);
     const uint32_t tS = tbase, tDP = tbase + 128, tDV = tbase + 256, tDK = tbase + 384;
     auto fail = [&]() { *abort_flag = 1; report(status, kStatusTimeout); };
 
     if (warp == 8) {
-        if (lane == 0 && n > 0) {
+        if (n > 0 && elect_one()) {
             mbar_arrive_expect_tx(&bars->own_full, 2 * C::TILE);
             for (int c = 0; c < C::NCH; ++c) {
                 tma_load_3d(sK + c * C::CHUNK, &mk, &bars->own_full, 64 * c, kvh, kr.begin + key0);
@@ -426,7 +426,7 @@ packed_dkdv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
             }
         }
     } else if (warp == 9) {
-        if (lane == 0 && n > 0) {
+        if (n > 0 && elect_one()) {
             const uint32_t k = smem_u32(sK), v = smem_u32(sV), q = smem_u32(sQ), g = smem_u32(sG);
             auto issue_s = [&](int t) {
                 if (!mma_wait(&bars->x_full[t & 1], (t / 2) & 1, abort_flag)) return false;
