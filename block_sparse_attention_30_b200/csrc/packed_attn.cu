@@ -121,7 +121,7 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
         if (threadIdx.x == 0) report(status, kStatusMisaligned);
         return;
     }
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = warp_uniform(tid >> 5);
     const int group = sh.heads_q / sh.heads_kv;
     const int kvh = blockIdx.x % sh.heads_kv;
     const int split = blockIdx.y;
@@ -148,16 +148,16 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tbase = bars->tmem_base;
+    const uint32_t tbase = warp_uniform(bars->tmem_base);
     auto fail = [&]() { *abort_flag = 1; report(status, kStatusTimeout); };
-    const int n = w.hi - w.lo;                           // blocks hi - 1 down to lo: step t is block hi - 1 - t
+    const int n = warp_uniform(w.hi - w.lo);             // blocks hi - 1 down to lo: step t is block hi - 1 - t
     // tile x takes part from step first[x] on
-    const int first[2] = {max(0, w.hi - w.nb[0]), max(0, w.hi - w.nb[1])};
+    const int first[2] = {warp_uniform(max(0, w.hi - w.nb[0])), warp_uniform(max(0, w.hi - w.nb[1]))};
 
     if (warp >= 8) {
       reg_dec<C::REG_LOAD>();
       if (warp == 8) {
-        if (lane == 0) {
+        if (elect_one()) {
             // ------------------------------------------------------ loads
             // ring item 2 t is K of step t, item 2 t + 1 its V
             bool q_issued[2] = {false, false};
@@ -188,43 +188,53 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
             }
         }
       } else if (warp == 9) {
-        if (lane == 0 && n > 0) {
+        if (n > 0) {
             // ------------------------------------------------------- MMAs
+            // (the whole warp walks the loop, so that every branch and value is
+            // uniform; one elected lane issues)
             const uint32_t id_s = idesc_bf16_f32(128, 128, false, false);
             const uint32_t id_o = idesc_bf16_f32(128, D, false, true);
-            const uint32_t q_addr = smem_u32(sQ), r_addr = smem_u32(ring);
-            auto item = [&](int i) { return mma_wait(&bars->full[i % C::NST], (i / C::NST) & 1, abort_flag); };
+            const uint64_t q_desc = smem_desc_sw128(smem_u32(sQ), 16, 1024);
+            const uint64_t k_desc = smem_desc_sw128(smem_u32(ring), 16, 1024), v_desc = smem_desc_sw128(smem_u32(ring), C::CHUNK, 1024);
+            auto wait = [&](uint64_t* bar, int parity) { return __all_sync(0xffffffffu, mma_wait(bar, parity, abort_flag)) != 0; };
+            auto item = [&](int i) { return wait(&bars->full[i % C::NST], (i / C::NST) & 1); };
             auto issue_s = [&](int x, int t) {
-                const uint32_t a0 = q_addr + x * C::TILE, b0 = r_addr + ((2 * t) % C::NST) * C::TILE;
+                const uint64_t a0 = desc_add(q_desc, x * C::TILE), b0 = desc_add(k_desc, ((2 * t) % C::NST) * C::TILE);
+                if (elect_one()) {
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t o = (kk >> 2) * C::CHUNK + (kk & 3) * 32;
-                    mma_bf16_ss(tbase + C::S_COL + 128 * x, smem_desc_sw128(a0 + o, 16, 1024),
-                                smem_desc_sw128(b0 + o, 16, 1024), id_s, kk > 0);
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t o = (kk >> 2) * C::CHUNK + (kk & 3) * 32;
+                        mma_bf16_ss(tbase + C::S_COL + 128 * x, desc_add(a0, o), desc_add(b0, o), id_s, kk > 0);
+                    }
+                    mma_commit(&bars->s_full[x]);
                 }
-                mma_commit(&bars->s_full[x]);
+                __syncwarp();
             };
             auto issue_o = [&](int x, int t) {
-                const uint32_t b0 = r_addr + ((2 * t + 1) % C::NST) * C::TILE;
+                const uint64_t b0 = desc_add(v_desc, ((2 * t + 1) % C::NST) * C::TILE);
+                if (elect_one()) {
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk)               // 16 keys per MMA
-                    mma_bf16_ts(tbase + C::O_COL + D * x, tbase + C::S_COL + 128 * x + kk * 8,
-                                smem_desc_sw128(b0 + kk * 2048, C::CHUNK, 1024), id_o, t > first[x] || kk > 0);
+                    for (int kk = 0; kk < 8; ++kk)           // 16 keys per MMA
+                        mma_bf16_ts(tbase + C::O_COL + D * x, tbase + C::S_COL + 128 * x + kk * 8,
+                                    desc_add(b0, kk * 2048), id_o, t > first[x] || kk > 0);
+                    if (t == n - 1) mma_commit(&bars->o_full[x]);
+                }
+                __syncwarp();
             };
             bool ok = true;
             for (int x = 0; x < 2 && ok; ++x)
-                if (first[x] < n) ok = mma_wait(&bars->q_full[x], 0, abort_flag);
+                if (first[x] < n) ok = wait(&bars->q_full[x], 0);
             // step t: P V of step t, then S of step t + 1 over the same columns
             // (MMAs of one thread run in issue order); step -1 has only the S
             for (int t = -1; t < n && ok; ++t) {
                 bool have_k = false, have_v = false;
-                for (int x = 0; x < 2 && ok; ++x) {
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
                     if (t >= first[x] && t >= 0) {
                         if (!have_v) { ok = item(2 * t + 1); have_v = true; }
-                        if (!ok || !(ok = mma_wait(&bars->p_full[x], (t - first[x]) & 1, abort_flag))) break;
+                        if (!ok || !(ok = wait(&bars->p_full[x], (t - first[x]) & 1))) break;
                         tc_fence_after();
                         issue_o(x, t);
-                        if (t == n - 1) mma_commit(&bars->o_full[x]);
                     }
                     if (t + 1 >= first[x] && t + 1 < n) {
                         if (!have_k) { ok = item(2 * t + 2); have_k = true; }
@@ -234,11 +244,15 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
                     }
                 }
                 if (!ok) break;
-                if (t >= 0) mma_commit(&bars->empty[(2 * t + 1) % C::NST]);
-                if (t + 1 < n) mma_commit(&bars->empty[(2 * t + 2) % C::NST]);
+                if (elect_one()) {
+                    if (t >= 0) mma_commit(&bars->empty[(2 * t + 1) % C::NST]);
+                    if (t + 1 < n) mma_commit(&bars->empty[(2 * t + 2) % C::NST]);
+                }
+                __syncwarp();
             }
             if (!ok) fail();
-            mma_commit(&bars->mma_done);
+            if (elect_one()) mma_commit(&bars->mma_done);
+            __syncwarp();
             wait_noabort(&bars->mma_done, 0);
         }
       }
