@@ -67,7 +67,7 @@ template <int D>
 struct PackBars {
     uint64_t q_full[2];
     uint64_t full[PackCfg<D>::NST], empty[PackCfg<D>::NST];
-    uint64_t s_full[2], p_full[2], o_full[2];
+    uint64_t s_full[2], p_half[2], p_full[2], o_full[2];
     uint64_t mma_done;                   // every MMA of the CTA finished
     uint32_t tmem_base;
     int abort;
@@ -137,6 +137,7 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
         for (int x = 0; x < 2; ++x) {
             mbar_init(&bars->q_full[x], 1);
             mbar_init(&bars->s_full[x], 1);
+            mbar_init(&bars->p_half[x], 128);
             mbar_init(&bars->p_full[x], 128);
             mbar_init(&bars->o_full[x], 1);
         }
@@ -210,14 +211,14 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
                 }
                 __syncwarp();
             };
-            auto issue_o = [&](int x, int t) {
+            auto issue_o = [&](int x, int t, int half) {     // 64 keys
                 const uint64_t b0 = desc_add(v_desc, ((2 * t + 1) % C::NST) * C::TILE);
                 if (elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)           // 16 keys per MMA
-                        mma_bf16_ts(tbase + C::O_COL + D * x, tbase + C::S_COL + 128 * x + kk * 8,
-                                    desc_add(b0, kk * 2048), id_o, t > first[x] || kk > 0);
-                    if (t == n - 1) mma_commit(&bars->o_full[x]);
+                    for (int kk = 0; kk < 4; ++kk)           // 16 keys per MMA
+                        mma_bf16_ts(tbase + C::O_COL + D * x, tbase + C::S_COL + 128 * x + 32 * half + kk * 8,
+                                    desc_add(b0, 8192 * half + kk * 2048), id_o, t > first[x] || half || kk > 0);
+                    if (half && t == n - 1) mma_commit(&bars->o_full[x]);
                 }
                 __syncwarp();
             };
@@ -232,9 +233,12 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
                 for (int x = 0; x < 2; ++x) {
                     if (t >= first[x] && t >= 0) {
                         if (!have_v) { ok = item(2 * t + 1); have_v = true; }
-                        if (!ok || !(ok = wait(&bars->p_full[x], (t - first[x]) & 1))) break;
+                        if (!ok || !(ok = wait(&bars->p_half[x], (t - first[x]) & 1))) break;
                         tc_fence_after();
-                        issue_o(x, t);
+                        issue_o(x, t, 0);
+                        if (!(ok = wait(&bars->p_full[x], (t - first[x]) & 1))) break;
+                        tc_fence_after();
+                        issue_o(x, t, 1);
                     }
                     if (t + 1 >= first[x] && t + 1 < n) {
                         if (!have_k) { ok = item(2 * t + 2); have_k = true; }
@@ -338,6 +342,11 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
                     else acc0 = add_f32x2(acc0, f32x2(p0, p1));
                 }
                 tmem_st_32x32b_x16(tS + 16 * c, pk);
+                if (c == 1) {                            // P V starts on the first half of the keys
+                    tmem_wait_st();
+                    tc_fence_before();
+                    mbar_arrive(&bars->p_half[x]);
+                }
             }
             float a0, a1, b0, b1;
             unf32x2(acc0, a0, a1);

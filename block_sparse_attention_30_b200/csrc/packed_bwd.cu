@@ -125,26 +125,37 @@ __device__ __forceinline__ void bwd_bars_init(PackBwdBars* b) {
     fence_barrier_init();
 }
 
-// acc (+)= A B^T, both tiles of 128 rows in shared memory, K-major.
+// acc = A B^T, both tiles of 128 rows in shared memory (K-major descriptors).
+// Here and below the whole warp calls, one elected lane issues, and its
+// completion is committed to the given barriers.
 template <int D>
-__device__ __forceinline__ void mma_scores(uint32_t acc, uint32_t a, uint32_t b) {
+__device__ __forceinline__ void mma_scores(uint32_t acc, uint64_t a, uint64_t b, uint64_t* bar, uint64_t* bar2 = nullptr) {
     constexpr uint32_t id = idesc_bf16_f32(128, 128, false, false);
+    if (elect_one()) {
 #pragma unroll
-    for (int kk = 0; kk < D / 16; ++kk) {
-        const uint32_t o = (kk >> 2) * PackBwdCfg<D>::CHUNK + (kk & 3) * 32;
-        mma_bf16_ss(acc, smem_desc_sw128(a + o, 16, 1024), smem_desc_sw128(b + o, 16, 1024), id, kk > 0);
+        for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t o = (kk >> 2) * PackBwdCfg<D>::CHUNK + (kk & 3) * 32;
+            mma_bf16_ss(acc, desc_add(a, o), desc_add(b, o), id, kk > 0);
+        }
+        mma_commit(bar);
+        if (bar2) mma_commit(bar2);
     }
+    __syncwarp();
 }
 
 // acc (+)= T X: T 128 x 128 bf16 in TMEM (columns 0-63 of its inner dimension
-// at t, 64-127 at t + 64), X a tile of 128 rows x D in shared memory.
+// at t, 64-127 at t + 64), X a tile of 128 rows x D in shared memory (MN-major
+// descriptor).
 template <int D>
-__device__ __forceinline__ void mma_weighted(uint32_t acc, uint32_t t, uint32_t x, bool accumulate) {
+__device__ __forceinline__ void mma_weighted(uint32_t acc, uint32_t t, uint64_t x, bool accumulate, uint64_t* bar) {
     constexpr uint32_t id = idesc_bf16_f32(128, D, false, true);
+    if (elect_one()) {
 #pragma unroll
-    for (int kk = 0; kk < 8; ++kk)
-        mma_bf16_ts(acc, t + (kk >> 2) * 64 + (kk & 3) * 8, smem_desc_sw128(x + kk * 2048, PackBwdCfg<D>::CHUNK, 1024), id,
-                    accumulate || kk > 0);
+        for (int kk = 0; kk < 8; ++kk)
+            mma_bf16_ts(acc, t + (kk >> 2) * 64 + (kk & 3) * 8, desc_add(x, kk * 2048), id, accumulate || kk > 0);
+        if (bar) mma_commit(bar);
+    }
+    __syncwarp();
 }
 
 // Rows [from, 128) of a tile become zeros (256 threads).
@@ -246,35 +257,35 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
             }
         }
     } else if (warp == 9) {
-        if (n > 0 && elect_one()) {
-            const uint32_t q = smem_u32(sQ), g = smem_u32(sG), k = smem_u32(sK), v = smem_u32(sV);
-            auto issue_s = [&](int t) {
-                if (!mma_wait(&bars->x_full[t % 3], (t / 3) & 1, abort_flag)) return false;
+        if (n > 0) {
+            const uint64_t q = smem_desc_sw128(smem_u32(sQ), 16, 1024), g = smem_desc_sw128(smem_u32(sG), 16, 1024);
+            const uint64_t k = smem_desc_sw128(smem_u32(sK), 16, 1024), v = smem_desc_sw128(smem_u32(sV), 16, 1024);
+            const uint64_t k_mn = smem_desc_sw128(smem_u32(sK), C::CHUNK, 1024);
+            auto wait = [&](uint64_t* bar, int parity) {
+                const bool done = __all_sync(0xffffffffu, mma_wait(bar, parity, abort_flag));
                 tc_fence_after();
-                mma_scores<D>(tbase + 128 * (t & 1), q, k + (t % 3) * C::TILE);
-                mma_commit(&bars->s_full[t & 1]);
+                return done;
+            };
+            auto issue_s = [&](int t) {
+                if (!wait(&bars->x_full[t % 3], (t / 3) & 1)) return false;
+                mma_scores<D>(tbase + 128 * (t & 1), q, desc_add(k, (t % 3) * C::TILE), &bars->s_full[t & 1]);
                 return true;
             };
             auto issue_dp = [&](int t) {
-                if (!mma_wait(&bars->y_full[t & 1], (t / 2) & 1, abort_flag)) return false;
-                tc_fence_after();
-                mma_scores<D>(tDP, g, v + (t & 1) * C::TILE);
-                mma_commit(&bars->dp_full);
-                mma_commit(&bars->y_empty[t & 1]);
+                if (!wait(&bars->y_full[t & 1], (t / 2) & 1)) return false;
+                mma_scores<D>(tDP, g, desc_add(v, (t & 1) * C::TILE), &bars->dp_full, &bars->y_empty[t & 1]);
                 return true;
             };
-            bool ok = mma_wait(&bars->own_full, 0, abort_flag) && issue_s(0) && issue_dp(0) && (n < 2 || issue_s(1));
+            bool ok = wait(&bars->own_full, 0) && issue_s(0) && issue_dp(0) && (n < 2 || issue_s(1));
             for (int t = 0; t < n && ok; ++t) {
-                ok = mma_wait(&bars->ds_ready, t & 1, abort_flag);
-                if (!ok) break;
-                tc_fence_after();
+                if (!(ok = wait(&bars->ds_ready, t & 1))) break;
                 if (t + 1 < n && !(ok = issue_dp(t + 1))) break;
-                mma_weighted<D>(tAcc, tbase + 128 * (t & 1), k + (t % 3) * C::TILE, t > 0);
-                mma_commit(&bars->x_empty[t % 3]);
+                mma_weighted<D>(tAcc, tbase + 128 * (t & 1), desc_add(k_mn, (t % 3) * C::TILE), t > 0, &bars->x_empty[t % 3]);
                 if (t + 2 < n) ok = issue_s(t + 2);
             }
             if (!ok) fail();
-            mma_commit(&bars->mma_done);
+            if (elect_one()) mma_commit(&bars->mma_done);
+            __syncwarp();
             wait_noabort(&bars->mma_done, 0);
         }
     } else {
@@ -426,36 +437,37 @@ packed_dkdv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
             }
         }
     } else if (warp == 9) {
-        if (n > 0 && elect_one()) {
-            const uint32_t k = smem_u32(sK), v = smem_u32(sV), q = smem_u32(sQ), g = smem_u32(sG);
-            auto issue_s = [&](int t) {
-                if (!mma_wait(&bars->x_full[t & 1], (t / 2) & 1, abort_flag)) return false;
+        if (n > 0) {
+            const uint64_t k = smem_desc_sw128(smem_u32(sK), 16, 1024), v = smem_desc_sw128(smem_u32(sV), 16, 1024);
+            const uint64_t q = smem_desc_sw128(smem_u32(sQ), 16, 1024), g = smem_desc_sw128(smem_u32(sG), 16, 1024);
+            const uint64_t q_mn = smem_desc_sw128(smem_u32(sQ), C::CHUNK, 1024), g_mn = smem_desc_sw128(smem_u32(sG), C::CHUNK, 1024);
+            auto wait = [&](uint64_t* bar, int parity) {
+                const bool done = __all_sync(0xffffffffu, mma_wait(bar, parity, abort_flag));
                 tc_fence_after();
-                mma_scores<D>(tS, k, q + (t & 1) * C::TILE);
-                mma_commit(&bars->s_full[0]);
+                return done;
+            };
+            auto issue_s = [&](int t) {
+                if (!wait(&bars->x_full[t & 1], (t / 2) & 1)) return false;
+                mma_scores<D>(tS, k, desc_add(q, (t & 1) * C::TILE), &bars->s_full[0]);
                 return true;
             };
             auto issue_dp = [&](int t) {
-                if (!mma_wait(&bars->y_full[t & 1], (t / 2) & 1, abort_flag)) return false;
-                tc_fence_after();
-                mma_scores<D>(tDP, v, g + (t & 1) * C::TILE);
-                mma_commit(&bars->dp_full);
+                if (!wait(&bars->y_full[t & 1], (t / 2) & 1)) return false;
+                mma_scores<D>(tDP, v, desc_add(g, (t & 1) * C::TILE), &bars->dp_full);
                 return true;
             };
-            bool ok = mma_wait(&bars->own_full, 0, abort_flag) && issue_s(0) && issue_dp(0);
+            bool ok = wait(&bars->own_full, 0) && issue_s(0) && issue_dp(0);
             for (int t = 0; t < n && ok; ++t) {
-                if (!(ok = mma_wait(&bars->p_ready, t & 1, abort_flag))) break;
-                tc_fence_after();
-                mma_weighted<D>(tDV, tS, g + (t & 1) * C::TILE, t > 0);
+                if (!(ok = wait(&bars->p_ready, t & 1))) break;
+                mma_weighted<D>(tDV, tS, desc_add(g_mn, (t & 1) * C::TILE), t > 0, nullptr);
                 if (t + 1 < n && !(ok = issue_s(t + 1))) break;
-                if (!(ok = mma_wait(&bars->ds_ready, t & 1, abort_flag))) break;
-                tc_fence_after();
-                mma_weighted<D>(tDK, tDP, q + (t & 1) * C::TILE, t > 0);
-                mma_commit(&bars->x_empty[t & 1]);
+                if (!(ok = wait(&bars->ds_ready, t & 1))) break;
+                mma_weighted<D>(tDK, tDP, desc_add(q_mn, (t & 1) * C::TILE), t > 0, &bars->x_empty[t & 1]);
                 if (t + 1 < n) ok = issue_dp(t + 1);
             }
             if (!ok) fail();
-            mma_commit(&bars->mma_done);
+            if (elect_one()) mma_commit(&bars->mma_done);
+            __syncwarp();
             wait_noabort(&bars->mma_done, 0);
         }
     } else {
