@@ -47,32 +47,36 @@
 namespace vsa {
 using namespace sm100;
 
-template <int D>
+// NT tiles of 128 rows per CTA: two, or one where most sequences have no
+// rows for a second (single tokens; two such CTAs share an SM instead).
+template <int D, int NT>
 struct PackCfg {
     static constexpr int NCH = D / 64;                   // 64-feature chunks
     static constexpr int CHUNK = 128 * 128;              // 128 rows of one chunk (bf16)
     static constexpr int TILE = NCH * CHUNK;             // 128 rows of one tensor
-    static constexpr int NST = D == 128 ? 5 : 10;        // K/V ring stages
-    static constexpr int BAR_OFF = (2 + NST) * TILE;
+    static constexpr int NST = (NT == 2 ? 5 : 2) * 128 / D;   // K/V ring stages
+    static constexpr int BAR_OFF = (NT + NST) * TILE;
     static constexpr int SMEM = BAR_OFF + 512;
-    static constexpr int THREADS = 384;                  // 3 warpgroups, 168 registers a thread at launch
-    static constexpr int REG_LOAD = 72, REG_SOFT = 216;  // 128 * 72 + 256 * 216 = 384 * 168
-    static constexpr int TMEM_COLS = 512;
+    static constexpr int THREADS = 128 * (NT + 1);       // softmax warpgroups and the loads' and MMAs'
+    // registers a thread: 168 at launch, 72 + 2 * 216 = 3 * 168; 128 at launch, 56 + 200 = 2 * 128
+    static constexpr int REG_LOAD = NT == 2 ? 72 : 56, REG_SOFT = NT == 2 ? 216 : 200;
+    static constexpr int TMEM_COLS = 256 * NT;
     static constexpr int S_COL = 0;                      // S / P of tile w at 128 w
-    static constexpr int O_COL = 256;                    // O of tile w at 256 + D w
+    static constexpr int O_COL = 128 * NT;               // O of tile w at O_COL + D w
 };
-static_assert(PackCfg<128>::SMEM <= 232448 && PackCfg<64>::SMEM <= 232448, "shared memory");
+static_assert(PackCfg<128, 2>::SMEM <= 232448 && PackCfg<64, 2>::SMEM <= 232448, "shared memory");
+static_assert(PackCfg<128, 1>::SMEM <= 115712 && PackCfg<64, 1>::SMEM <= 115712, "shared memory of two CTAs");
 
-template <int D>
+template <int D, int NT>
 struct PackBars {
     uint64_t q_full[2];
-    uint64_t full[PackCfg<D>::NST], empty[PackCfg<D>::NST];
+    uint64_t full[PackCfg<D, NT>::NST], empty[PackCfg<D, NT>::NST];
     uint64_t s_full[2], p_half[2], p_full[2], o_full[2];
     uint64_t mma_done;                   // every MMA of the CTA finished
     uint32_t tmem_base;
     int abort;
 };
-static_assert(sizeof(PackBars<64>) <= 512, "barrier block");
+static_assert(sizeof(PackBars<64, 2>) <= 512, "barrier block");
 
 // What one CTA works on: rows of the tile pair and its key blocks.
 struct PackWork {
@@ -85,20 +89,20 @@ struct PackWork {
 };
 
 __device__ __forceinline__ PackWork pack_work(const int32_t* __restrict__ cu_q, const int32_t* __restrict__ cu_k,
-                                              const PackedShape& s, int tok_per_tile, int tiles, int t, int causal,
-                                              int n_splits, int split, int* status) {
+                                              const PackedShape& s, int nt, int tok_per_tile, int tiles, int t,
+                                              int causal, int n_splits, int split, int* status) {
     PackWork w;
-    const SeqTile at = find_tile(cu_q, s.n_seq, s.total_q, 2 * tok_per_tile, tiles - 1 - t, status);
+    const SeqTile at = find_tile(cu_q, s.n_seq, s.total_q, nt * tok_per_tile, tiles - 1 - t, status);
     w.seq = at.seq;
     if (at.seq < 0) return w;
     const SeqRange q = seq_range(cu_q, at.seq, s.total_q, status), k = seq_range(cu_k, at.seq, s.total_k, status);
     w.q0 = q.begin; w.nq = q.len; w.k0 = k.begin; w.nk = k.len;
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-        w.tok[x] = (2 * at.tile + x) * tok_per_tile;
+        w.tok[x] = (nt * at.tile + x) * tok_per_tile;
         // the tile's last token sees the most keys
         const int last = min(w.tok[x] + tok_per_tile, w.nq) - 1;
-        w.nb[x] = w.tok[x] < w.nq ? (seen_keys(last, w.nq, w.nk, causal) + 127) / 128 : 0;
+        w.nb[x] = x < nt && w.tok[x] < w.nq ? (seen_keys(last, w.nq, w.nk, causal) + 127) / 128 : 0;
     }
     const int nb = max(w.nb[0], w.nb[1]);
     const int per = (nb + n_splits - 1) / n_splits;
@@ -107,15 +111,15 @@ __device__ __forceinline__ PackWork pack_work(const int32_t* __restrict__ cu_q, 
     return w;
 }
 
-template <int D>
-__global__ void __launch_bounds__(PackCfg<D>::THREADS, 1)
+template <int D, int NT>
+__global__ void __launch_bounds__(PackCfg<D, NT>::THREADS, 3 - NT)
 packed_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                   const __grid_constant__ CUtensorMap mv, const PackedShape sh, const int tok_per_tile,
                   const int tiles, const int32_t* __restrict__ cu_q, const int32_t* __restrict__ cu_k,
                   const int causal, const float scale_log2, __nv_bfloat16* __restrict__ out,
                   const long long out_stride, float* __restrict__ out32, float* __restrict__ lse,
                   const int n_splits, float* __restrict__ part_o, float* __restrict__ part_lse, int* status) {
-    using C = PackCfg<D>;
+    using C = PackCfg<D, NT>;
     extern __shared__ __align__(1024) uint8_t smem[];
     if (smem_u32(smem) & 1023) {
         if (threadIdx.x == 0) report(status, kStatusMisaligned);
@@ -123,18 +127,18 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
     }
     const int tid = threadIdx.x, warp = warp_uniform(tid >> 5);
     const int group = sh.heads_q / sh.heads_kv;
-    const int kvh = blockIdx.x % sh.heads_kv;
-    const int split = blockIdx.y;
-    const PackWork w = pack_work(cu_q, cu_k, sh, tok_per_tile, tiles, blockIdx.x / sh.heads_kv, causal, n_splits, split,
-                                 status);
+    // the shares of a tile start together, so that long sequences come first as a whole
+    const int split = blockIdx.x % n_splits, item = blockIdx.x / n_splits;
+    const int kvh = item % sh.heads_kv;
+    const PackWork w = pack_work(cu_q, cu_k, sh, NT, tok_per_tile, tiles, item / sh.heads_kv, causal, n_splits, split, status);
     if (w.seq < 0) return;                               // uniform over the CTA
     uint8_t* sQ = smem;
-    uint8_t* ring = smem + 2 * C::TILE;
-    PackBars<D>* bars = reinterpret_cast<PackBars<D>*>(smem + C::BAR_OFF);
+    uint8_t* ring = smem + NT * C::TILE;
+    PackBars<D, NT>* bars = reinterpret_cast<PackBars<D, NT>*>(smem + C::BAR_OFF);
     volatile int* abort_flag = &bars->abort;
     if (tid == 0) {
         bars->abort = 0;
-        for (int x = 0; x < 2; ++x) {
+        for (int x = 0; x < NT; ++x) {
             mbar_init(&bars->q_full[x], 1);
             mbar_init(&bars->s_full[x], 1);
             mbar_init(&bars->p_half[x], 128);
@@ -145,7 +149,7 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
         mbar_init(&bars->mma_done, 1);
         fence_barrier_init();
     }
-    if (warp == 9) { tmem_alloc(&bars->tmem_base, C::TMEM_COLS); tmem_relinquish(); }
+    if (warp == 4 * NT + 1) { tmem_alloc(&bars->tmem_base, C::TMEM_COLS); tmem_relinquish(); }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -155,14 +159,14 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
     // tile x takes part from step first[x] on
     const int first[2] = {warp_uniform(max(0, w.hi - w.nb[0])), warp_uniform(max(0, w.hi - w.nb[1]))};
 
-    if (warp >= 8) {
+    if (warp >= 4 * NT) {
       reg_dec<C::REG_LOAD>();
-      if (warp == 8) {
+      if (warp == 4 * NT) {
         if (elect_one()) {
             // ------------------------------------------------------ loads
             // ring item 2 t is K of step t, item 2 t + 1 its V
             bool q_issued[2] = {false, false};
-            for (int x = 0; x < 2 && n > 0; ++x) {
+            for (int x = 0; x < NT && n > 0; ++x) {
                 if (w.tok[x] >= w.nq) continue;
                 mbar_arrive_expect_tx(&bars->q_full[x], C::NCH * tok_per_tile * group * 128);
                 for (int c = 0; c < C::NCH; ++c)
@@ -183,12 +187,12 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
             }
             if (*abort_flag) {
                 // drain: every load must land before the CTA's shared memory is given up
-                for (int x = 0; x < 2; ++x) if (q_issued[x]) wait_noabort(&bars->q_full[x], 0);
+                for (int x = 0; x < NT; ++x) if (q_issued[x]) wait_noabort(&bars->q_full[x], 0);
                 for (int i = max(0, issued - C::NST); i < issued; ++i)
                     wait_noabort(&bars->full[i % C::NST], (i / C::NST) & 1);
             }
         }
-      } else if (warp == 9) {
+      } else if (warp == 4 * NT + 1) {
         if (n > 0) {
             // ------------------------------------------------------- MMAs
             // (the whole warp walks the loop, so that every branch and value is
@@ -223,14 +227,14 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
                 __syncwarp();
             };
             bool ok = true;
-            for (int x = 0; x < 2 && ok; ++x)
+            for (int x = 0; x < NT && ok; ++x)
                 if (first[x] < n) ok = wait(&bars->q_full[x], 0);
             // step t: P V of step t, then S of step t + 1 over the same columns
             // (MMAs of one thread run in issue order); step -1 has only the S
             for (int t = -1; t < n && ok; ++t) {
                 bool have_k = false, have_v = false;
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
+                for (int x = 0; x < NT; ++x) {
                     if (t >= first[x] && t >= 0) {
                         if (!have_v) { ok = item(2 * t + 1); have_v = true; }
                         if (!ok || !(ok = wait(&bars->p_half[x], (t - first[x]) & 1))) break;
@@ -275,6 +279,9 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
         float m_run = -CUDART_INF_F, l_run = 0.f;
         bool ok = true;
         const int f = first[x];
+        // a warp without rows has nothing to compute: what it leaves in its
+        // rows of P only reaches its own rows of O, which are not stored
+        const bool idle = !__any_sync(0xffffffffu, valid);
         for (int t = f; t < n; ++t) {
             const int key0 = 128 * (w.hi - 1 - t);
             if (key0 + 128 > w.nk) {
@@ -287,6 +294,11 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
                 fence_proxy_async_smem();
             }
             if (!__all_sync(0xffffffffu, mbar_wait(&bars->s_full[x], (t - f) & 1, abort_flag))) { ok = false; break; }
+            if (idle) {
+                mbar_arrive(&bars->p_half[x]);
+                mbar_arrive(&bars->p_full[x]);
+                continue;
+            }
             tc_fence_after();
             float s[128];
 #pragma unroll
@@ -408,25 +420,25 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 9) tmem_dealloc(tbase, C::TMEM_COLS);
+    if (warp == 4 * NT + 1) tmem_dealloc(tbase, C::TMEM_COLS);
 }
 
 // Joins the shares of a split key axis: out = sum_s 2^(lse_s - m) O_s / sum_s 2^(lse_s - m), m the largest lse_s.
-// One CTA per tile pair and kv head as in the kernel before it, D / 4 threads per row.
+// One CTA per `tok_per_cta` tokens and kv head as in the kernel before it, D / 4 threads per row.
 template <int D>
 __global__ void __launch_bounds__(256)
-packed_combine_kernel(const PackedShape sh, const int tok_per_tile, const int tiles, const int32_t* __restrict__ cu_q,
+packed_combine_kernel(const PackedShape sh, const int tok_per_cta, const int tiles, const int32_t* __restrict__ cu_q,
                       const int n_splits, const float* __restrict__ part_o, const float* __restrict__ part_lse,
                       __nv_bfloat16* __restrict__ out, const long long out_stride, float* __restrict__ out32,
                       float* __restrict__ lse, int* status) {
     constexpr int TPR = D / 4;
     const int group = sh.heads_q / sh.heads_kv;
     const int kvh = blockIdx.x % sh.heads_kv;
-    const SeqTile at = find_tile(cu_q, sh.n_seq, sh.total_q, 2 * tok_per_tile, tiles - 1 - blockIdx.x / sh.heads_kv, status);
+    const SeqTile at = find_tile(cu_q, sh.n_seq, sh.total_q, tok_per_cta, tiles - 1 - blockIdx.x / sh.heads_kv, status);
     if (at.seq < 0) return;
     const SeqRange q = seq_range(cu_q, at.seq, sh.total_q, status);
-    const int tok0 = at.tile * 2 * tok_per_tile;
-    const int rows = min(2 * tok_per_tile, q.len - tok0) * group;
+    const int tok0 = at.tile * tok_per_cta;
+    const int rows = min(tok_per_cta, q.len - tok0) * group;
     const int f = threadIdx.x % TPR * 4;
     for (int r = threadIdx.x / TPR + blockIdx.y * (256 / TPR); r < rows; r += 256 / TPR * gridDim.y) {
         const long long row = (long long)q.begin + tok0 + r / group;
@@ -462,21 +474,34 @@ bool encode_packed_map(CUtensorMap* m, const PackedTensor& t, int rows, int head
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Upper bound of the tile pairs of 2 x (128 / group) tokens that the
-// sequences are cut into (their lengths are device data).
-static long long pair_bound(const PackedShape& s) {
-    return (long long)s.total_q / (2 * (128 / s.group())) + s.n_seq;
+// One tile per CTA where the average sequence does not fill it.
+static int tiles_per_cta(const PackedShape& s) { return (long long)s.total_q * s.group() <= 128ll * s.n_seq ? 1 : 2; }
+
+// Upper bound of the CTAs' worth of tokens that the sequences are cut into
+// (their lengths are device data).
+static long long cta_bound(const PackedShape& s) {
+    return (long long)s.total_q / (tiles_per_cta(s) * (128 / s.group())) + s.n_seq;
 }
 
-long long packed_work_items(const PackedShape& s) { return pair_bound(s) * s.heads_kv; }
+long long packed_work_items(const PackedShape& s) { return cta_bound(s) * s.heads_kv; }
 
-// Shares the key axis is split into: 1 when the tile pairs fill the GPU.
-// The host knows the average key length only.
+// Shares the key axis is split into, by the time of the rounds of CTAs in
+// units of one block of 128 keys (1.6 us): a CTA takes two more for its start
+// and end, and joining n shares takes two for its launch and n times the
+// partial rows at 3 TB/s.  The host knows the average lengths only.
 int packed_splits(const PackedShape& s) {
     const long long items = packed_work_items(s);
-    const long long blocks = ((long long)s.total_k / s.n_seq + 127) / 128;     // of an average sequence
-    if (items >= 2 * 148 || blocks < 4) return 1;
-    return (int)std::max<long long>(1, std::min<long long>({(4 * 148 + items - 1) / items, blocks / 2, 64}));
+    const double slots = tiles_per_cta(s) == 1 ? 296 : 148;
+    const double blocks = std::max(1.0, (double)s.total_k / s.n_seq / 128);
+    const double rows = (double)s.total_q * s.heads_q * s.d * 4 / 3e12 / 1.6e-6;
+    if (items >= 2 * slots) return 1;                    // enough to balance by themselves
+    int best = 1;
+    double best_cost = 1e300;
+    for (int n = 1; n <= 64 && n <= blocks / 2 + 1; ++n) {
+        const double cost = std::ceil(items * n / slots) * (blocks / n + 2) + (n > 1 ? 2 + n * rows : 0);
+        if (cost < best_cost) { best_cost = cost; best = n; }
+    }
+    return best;
 }
 
 size_t packed_fwd_scratch_bytes(const PackedShape& s) {
@@ -484,14 +509,14 @@ size_t packed_fwd_scratch_bytes(const PackedShape& s) {
     return n > 1 ? (size_t)n * s.total_q * s.heads_q * (s.d + 1) * sizeof(float) : 0;
 }
 
-template <int D>
+template <int D, int NT>
 static cudaError_t launch_packed_fwd_impl(const PackedArgs& a, cudaStream_t stream) {
-    using C = PackCfg<D>;
+    using C = PackCfg<D, NT>;
     // set on every call: a cache by device would need a lock to be re-entrant
-    cudaError_t e = cudaFuncSetAttribute(packed_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    cudaError_t e = cudaFuncSetAttribute(packed_fwd_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
     const int group = a.s.group(), tok = 128 / group;
-    const long long tiles = pair_bound(a.s);
+    const long long tiles = cta_bound(a.s);
     // without keys nothing is read from k and v: any valid address will do for their maps
     const PackedTensor kk = a.s.total_k ? a.k : a.q, vv = a.s.total_k ? a.v : a.q;
     CUtensorMap mq, mk, mv;
@@ -503,23 +528,26 @@ static cudaError_t launch_packed_fwd_impl(const PackedArgs& a, cudaStream_t stre
     float* part_o = reinterpret_cast<float*>(a.scratch);
     float* part_lse = part_o + (size_t)n * a.s.total_q * a.s.heads_q * D;
     const float scale_log2 = 1.4426950408889634f / sqrtf((float)D);
-    packed_fwd_kernel<D><<<dim3((unsigned)(tiles * a.s.heads_kv), n), C::THREADS, C::SMEM, stream>>>(
+    packed_fwd_kernel<D, NT><<<(unsigned)(tiles * a.s.heads_kv * n), C::THREADS, C::SMEM, stream>>>(
         mq, mk, mv, a.s, tok, (int)tiles, a.cu_q, a.cu_k, a.causal, scale_log2,
         static_cast<__nv_bfloat16*>(a.out.p), a.out.stride, a.out32, a.lse, n, part_o, part_lse, a.status);
     if (n > 1) {
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
-        const int rows = 2 * tok * group, per = 256 / (D / 4);
-        const int gy = std::min((rows + per - 1) / per, 8);
+        // rows of an average sequence's share of a CTA
+        const long long rows = std::min<long long>(NT * tok, (a.s.total_q + a.s.n_seq - 1) / a.s.n_seq) * group, per = 256 / (D / 4);
+        const int gy = (int)std::min((rows + per - 1) / per, 8ll);
         packed_combine_kernel<D><<<dim3((unsigned)(tiles * a.s.heads_kv), gy), 256, 0, stream>>>(
-            a.s, tok, (int)tiles, a.cu_q, n, part_o, part_lse, static_cast<__nv_bfloat16*>(a.out.p), a.out.stride,
+            a.s, NT * tok, (int)tiles, a.cu_q, n, part_o, part_lse, static_cast<__nv_bfloat16*>(a.out.p), a.out.stride,
             a.out32, a.lse, a.status);
     }
     return cudaGetLastError();
 }
 
 cudaError_t launch_packed_fwd(const PackedArgs& a, cudaStream_t stream) {
-    return a.s.d == 128 ? launch_packed_fwd_impl<128>(a, stream) : launch_packed_fwd_impl<64>(a, stream);
+    if (tiles_per_cta(a.s) == 1)
+        return a.s.d == 128 ? launch_packed_fwd_impl<128, 1>(a, stream) : launch_packed_fwd_impl<64, 1>(a, stream);
+    return a.s.d == 128 ? launch_packed_fwd_impl<128, 2>(a, stream) : launch_packed_fwd_impl<64, 2>(a, stream);
 }
 
 }  // namespace vsa
