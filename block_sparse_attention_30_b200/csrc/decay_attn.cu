@@ -788,37 +788,50 @@ decay_out_kernel(const __grid_constant__ DecayPasses passes, const int n_passes,
 // --------------------------------------------------------------------- launch
 
 // How the sequences are cut, whose lengths only the device knows: m chunks to
-// a segment.  Times in units of one chunk of decay_out_kernel, which takes 0.75
-// of the time at which all SMs together reach the memory's bandwidth (so 111
-// walking CTAs saturate it); 2.5 of them are a CTA's start and end, 0.5 is a
-// chunk's share of the border sums' reading (two of four tensors), 3 the two
-// further launches.  The sequences are taken to be at most 2.5 times the
-// average (a longer one is cut, the rest are not).  With several passes over
-// the same tensors, segments small enough for the running ones to stay in L2
-// (some 80 MB) spare reading them again.
+// a segment.  Estimated times in units of one chunk of decay_out_kernel (2.6 us
+// at d = 128, 1.9 us at d = 64), each constant from a sweep over m:
+//   outputs  one sequence: rounds of 148 CTAs of m chunks and two more for
+//            their start and end; several: their mean share, half a longest
+//            piece of imbalance, the starts.  The memory bounds them too: at
+//            d = 128 a round of 148 chunks reads and writes 1.1 units' worth
+//            (passes over the same tensors meet in L2).
+//   borders  0.6 units a round of chunks whose sums are needed (half of the
+//            tensors are read), and 3.5 for the two further launches.
+// A sequence is taken to be 2.5 times the average at most; a longer one is cut
+// in pieces of that, which costs its batch little.
 static DecayShape decay_shape(int n_seq, int total, int heads, int d, int passes) {
     const long long chunks = std::max(1ll, ((long long)total + 127) / 128);
-    const long long longest = n_seq == 1 ? chunks : std::min(chunks, (5 * chunks + 2 * n_seq - 1) / (2 * n_seq));
-    const double walks = (double)heads * passes, kinds = passes > 1 ? 2 : 1;
+    const long long longest = n_seq == 1 ? chunks : std::min(chunks, (5 * chunks + 2ll * n_seq - 1) / (2ll * n_seq));
+    const double walks = (double)heads * passes, sums = (double)heads * (passes > 1 ? 2 : 1);
+    const double work = chunks * walks / 148;
+    const double memory = work * (d == 128 ? 1.1 : 0.8) * (passes > 1 ? 7.0 / 12 : 1.0);
     long long best = longest;
     double best_cost = 1e300;
-    for (long long m = 1; m <= longest; m = m < 64 ? m + 1 : std::min(m + m / 32, m < longest ? longest : m + 1)) {
-        const double segs = n_seq == 1 ? (double)((chunks + m - 1) / m) : (double)chunks / m + (m < longest ? 0.5 : 0.0) * n_seq;
-        const double rounds = std::ceil(std::max(segs, (double)n_seq) * walks / 148);
-        const double tile = 128.0 * d * 2, set = std::min(148.0, segs * walks) / passes * 4 * tile * m;
-        const double per_pass = passes == 1 ? 1.0 : set < 80e6 ? 7.0 / 12 : 10.0 / 12;
-        double cost = std::max(rounds * (m + 2.5) * 0.75, chunks * walks / 148 * per_pass);
-        if (m < longest) cost += 0.55 * kinds * heads * chunks / 148 * (1.0 - (double)m / longest) + 3.0;
+    auto consider = [&](long long pieces) {
+        if (pieces < 1 || pieces > longest) return;
+        const long long m = (longest + pieces - 1) / pieces;
+        const bool cut = m < longest;
+        double cost;
+        if (n_seq == 1)
+            cost = std::ceil((double)((chunks + m - 1) / m) * walks / 148) * (m + 2.0);
+        else
+            cost = std::max(m + 2.0, work + 0.5 * m + 2.0 * std::max(1.0, (cut ? (double)chunks / m + 0.5 * n_seq : n_seq) * walks / 148));
+        cost = std::max(cost, memory);
+        if (cut) cost += 0.6 * chunks * sums / 148 * (1.0 - (double)m / longest) + 3.5;
         if (cost < best_cost) { best_cost = cost; best = m; }
+    };
+    for (int pieces = 1; pieces <= 12; ++pieces) consider(pieces);
+    for (int rounds = 1; rounds <= 4; ++rounds) consider((long long)(148 * rounds / walks));
+    // parts of a segment: rounds of two CTAs per SM, 2.5 chunks for a start and end
+    const double cuts = std::max(1.0, n_seq == 1 ? (double)((chunks + best - 1) / best - 1) : (double)chunks / best);
+    long long part = best, k = 1;
+    best_cost = 1e300;
+    for (int i = 1; i <= 4; ++i) {
+        const long long len = (best + i - 1) / i;
+        const double cost = std::ceil(cuts * i * sums / 296) * (len + 2.5);
+        if (cost < best_cost) { best_cost = cost; part = len; k = i; }
     }
-    // parts: two CTAs per SM, at least 4 chunks each
-    long long parts = 1;
-    for (long long k = 2; k <= std::min(best / 4, 64ll); ++k) {
-        if (best % k) continue;
-        if ((double)chunks / (best / parts) * heads * kinds >= 4 * 296) break;
-        parts = k;
-    }
-    return {n_seq, total, heads, (int)(128 * best), (int)(128 * (best / parts))};
+    return {n_seq, total, heads, (int)(128 * part * k), (int)(128 * part)};
 }
 
 static size_t border_bytes(const DecayShape& s, int d) { return (size_t)(s.total / s.part) * s.heads * d * d * sizeof(float); }

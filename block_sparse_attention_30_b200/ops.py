@@ -171,34 +171,52 @@ def new_workspace_bytes(nbytes, device="cuda", stream=None):
     return ws
 
 
-def _rows(x, heads=None, d=None, total=None):
+def _rows(x, shape):
     """A packed bf16 [total, heads, d] tensor -> (pointer, row stride)."""
-    assert x.dtype == torch.bfloat16 and x.is_cuda and x.dim() == 3, "expected a bf16 [total, heads, d] CUDA tensor"
-    t, h, n = x.shape
-    assert (heads is None or h == heads) and (d is None or n == d) and (total is None or t == total), tuple(x.shape)
-    assert t == 0 or ((n == 1 or x.stride(2) == 1) and (h == 1 or x.stride(1) == n)), \
-        "heads and features must be contiguous"
-    return x.data_ptr(), x.stride(0) if t > 1 else h * n
+    assert x.dtype == torch.bfloat16 and x.is_cuda, "expected a bf16 CUDA tensor"
+    assert x.shape == shape, f"expected a tensor of shape {tuple(shape)}, got {tuple(x.shape)}"
+    t, h, n = shape
+    st = x.stride()
+    assert t == 0 or ((n == 1 or st[2] == 1) and (h == 1 or st[1] == n)), "heads and features must be contiguous"
+    return x.data_ptr(), st[0] if t > 1 else h * n
+
+
+def _packed_shape(x):
+    assert x.dim() == 3, "expected a [total, heads, d] tensor"
+    return x.shape
 
 
 def _borders(cu):
     assert cu.dtype == torch.int32 and cu.is_cuda and cu.dim() == 1 and cu.is_contiguous() and cu.numel() >= 2, \
         "expected int32 [n_seq + 1] sequence borders"
-    return cu.data_ptr(), cu.numel() - 1
+    return cu.numel() - 1
 
 
 def _f32(x, shape):
     if x is None:
         return None
-    assert x.dtype == torch.float32 and x.is_cuda and x.is_contiguous() and tuple(x.shape) == tuple(shape), \
-        f"expected a contiguous fp32 tensor of shape {tuple(shape)}"
+    assert x.dtype == torch.float32 and x.is_cuda and x.is_contiguous() and x.shape == shape, \
+        f"expected a contiguous fp32 CUDA tensor of shape {tuple(shape)}"
     return x.data_ptr()
 
 
-def _same_device(*tensors):
-    dev = {x.device for x in tensors if x is not None}
-    assert len(dev) == 1, f"tensors on several devices: {sorted(map(str, dev))}"
-    return torch.cuda.device(dev.pop())
+def _space(workspace):
+    assert workspace.dtype == torch.uint8 and workspace.is_cuda and workspace.is_contiguous(), "expected a uint8 CUDA workspace"
+    return workspace.data_ptr(), workspace.numel()
+
+
+def _run(name, stream, tensors, *args):
+    """Call an entry point on the tensors' device, on `stream` or that device's current stream."""
+    dev = tensors[0].get_device()
+    assert all(x is None or x.get_device() == dev for x in tensors), "tensors on several devices"
+    raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    f = getattr(_lib.lib(), name)
+    if torch.cuda.current_device() == dev:
+        code = f(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            code = f(*args, raw)
+    _lib.check(name, code)
 
 
 def vsa_packed_attn_workspace_bytes(total_q, total_k, n_seq, heads_q, heads_kv, head_dim) -> int:
@@ -213,28 +231,27 @@ def vsa_packed_attn_fwd(q, k, v, cu_q, cu_k, out, workspace, causal=True, out_f3
     Query i of a sequence sees keys up to i + nk - nq (causal) or all of them.
     out_f32 [total_q, heads_q, d] and lse [heads_q, total_q] (fp32) are
     written if given; the backward needs both."""
-    (tq, hq, d), (tk, hk) = q.shape, k.shape[:2]
-    n = _borders(cu_q)[1]
-    assert _borders(cu_k)[1] == n, "cu_q and cu_k describe different numbers of sequences"
-    with _same_device(q, k, v, cu_q, cu_k, out, workspace, out_f32, lse):
-        _lib.check("vsa_packed_attn_fwd", _lib.lib().vsa_packed_attn_fwd(
-            *_rows(q), *_rows(k, hk, d), *_rows(v, hk, d, tk), cu_q.data_ptr(), cu_k.data_ptr(), *_rows(out, hq, d, tq),
-            _f32(out_f32, (tq, hq, d)), _f32(lse, (hq, tq)), tq, tk, n, hq, hk, d, int(bool(causal)),
-            workspace.data_ptr(), workspace.numel(), _stream(stream)))
+    (tq, hq, d), (tk, hk, _) = _packed_shape(q), _packed_shape(k)
+    n = _borders(cu_q)
+    assert _borders(cu_k) == n, "cu_q and cu_k describe different numbers of sequences"
+    kv = (tk, hk, d)
+    _run("vsa_packed_attn_fwd", stream, (q, k, v, cu_q, cu_k, out, workspace, out_f32, lse),
+         *_rows(q, q.shape), *_rows(k, kv), *_rows(v, kv), cu_q.data_ptr(), cu_k.data_ptr(), *_rows(out, q.shape),
+         _f32(out_f32, q.shape), _f32(lse, (hq, tq)), tq, tk, n, hq, hk, d, int(bool(causal)),
+         *_space(workspace))
 
 
 def vsa_packed_attn_bwd(q, k, v, out_f32, dout, cu_q, cu_k, lse, dq, dk, dv, workspace, causal=True, stream=None):
     """Gradients of vsa_packed_attn_fwd, written into dq, dk, dv (bf16, shaped
     as q, k, v; rows may be strided); out_f32 and lse are the forward's."""
-    (tq, hq, d), (tk, hk) = q.shape, k.shape[:2]
-    n = _borders(cu_q)[1]
-    assert _borders(cu_k)[1] == n, "cu_q and cu_k describe different numbers of sequences"
-    with _same_device(q, k, v, out_f32, dout, cu_q, cu_k, lse, dq, dk, dv, workspace):
-        _lib.check("vsa_packed_attn_bwd", _lib.lib().vsa_packed_attn_bwd(
-            *_rows(q), *_rows(k, hk, d), *_rows(v, hk, d, tk), _f32(out_f32, (tq, hq, d)), *_rows(dout, hq, d, tq),
-            cu_q.data_ptr(), cu_k.data_ptr(), _f32(lse, (hq, tq)), *_rows(dq, hq, d, tq), *_rows(dk, hk, d, tk),
-            *_rows(dv, hk, d, tk), tq, tk, n, hq, hk, d, int(bool(causal)), workspace.data_ptr(), workspace.numel(),
-            _stream(stream)))
+    (tq, hq, d), (tk, hk, _) = _packed_shape(q), _packed_shape(k)
+    n = _borders(cu_q)
+    assert _borders(cu_k) == n, "cu_q and cu_k describe different numbers of sequences"
+    kv = (tk, hk, d)
+    _run("vsa_packed_attn_bwd", stream, (q, k, v, out_f32, dout, cu_q, cu_k, lse, dq, dk, dv, workspace),
+         *_rows(q, q.shape), *_rows(k, kv), *_rows(v, kv), _f32(out_f32, q.shape), *_rows(dout, q.shape),
+         cu_q.data_ptr(), cu_k.data_ptr(), _f32(lse, (hq, tq)), *_rows(dq, q.shape), *_rows(dk, kv), *_rows(dv, kv),
+         tq, tk, n, hq, hk, d, int(bool(causal)), *_space(workspace))
 
 
 def vsa_decay_attn_workspace_bytes(total, n_seq, heads, head_dim) -> int:
@@ -249,13 +266,12 @@ def vsa_decay_attn_fwd(q, k, v, log_decay, cu, out, workspace, scale=None, state
     [heads]; cu: int32 borders; state_in, state_out (optional): fp32 [n_seq,
     heads, d, d], the states before and after each sequence.  scale: 1/sqrt(d)
     if not given."""
-    (t, h, d), n = q.shape, _borders(cu)[1]
-    st = (n, h, d, d)
-    with _same_device(q, k, v, log_decay, cu, out, workspace, state_in, state_out):
-        _lib.check("vsa_decay_attn_fwd", _lib.lib().vsa_decay_attn_fwd(
-            *_rows(q), *_rows(k, h, d, t), *_rows(v, h, d, t), _f32(log_decay, (h,)), cu.data_ptr(), _f32(state_in, st),
-            _f32(state_out, st), *_rows(out, h, d, t), d ** -0.5 if scale is None else scale, t, n, h, d,
-            workspace.data_ptr(), workspace.numel(), _stream(stream)))
+    (t, h, d), n = _packed_shape(q), _borders(cu)
+    x, st = q.shape, (n, h, d, d)
+    _run("vsa_decay_attn_fwd", stream, (q, k, v, log_decay, cu, out, workspace, state_in, state_out),
+         *_rows(q, x), *_rows(k, x), *_rows(v, x), _f32(log_decay, (h,)), cu.data_ptr(), _f32(state_in, st),
+         _f32(state_out, st), *_rows(out, x), d ** -0.5 if scale is None else scale, t, n, h, d,
+         *_space(workspace))
 
 
 def vsa_decay_attn_bwd(q, k, v, dout, log_decay, cu, dq, dk, dv, workspace, scale=None, state_in=None, dstate_out=None,
@@ -263,26 +279,23 @@ def vsa_decay_attn_bwd(q, k, v, dout, log_decay, cu, dq, dk, dv, workspace, scal
     """Gradients of vsa_decay_attn_fwd, written into dq, dk, dv (bf16) and, if
     given, dstate_in (fp32); dstate_out: the gradient of the states after each
     sequence, if there is one.  The decays are constants."""
-    (t, h, d), n = q.shape, _borders(cu)[1]
-    st = (n, h, d, d)
-    with _same_device(q, k, v, dout, log_decay, cu, dq, dk, dv, workspace, state_in, dstate_out, dstate_in):
-        _lib.check("vsa_decay_attn_bwd", _lib.lib().vsa_decay_attn_bwd(
-            *_rows(q), *_rows(k, h, d, t), *_rows(v, h, d, t), *_rows(dout, h, d, t), _f32(log_decay, (h,)), cu.data_ptr(),
-            _f32(state_in, st), _f32(dstate_out, st), *_rows(dq, h, d, t), *_rows(dk, h, d, t), *_rows(dv, h, d, t),
-            _f32(dstate_in, st), d ** -0.5 if scale is None else scale, t, n, h, d, workspace.data_ptr(),
-            workspace.numel(), _stream(stream)))
+    (t, h, d), n = _packed_shape(q), _borders(cu)
+    x, st = q.shape, (n, h, d, d)
+    _run("vsa_decay_attn_bwd", stream, (q, k, v, dout, log_decay, cu, dq, dk, dv, workspace, state_in, dstate_out, dstate_in),
+         *_rows(q, x), *_rows(k, x), *_rows(v, x), *_rows(dout, x), _f32(log_decay, (h,)), cu.data_ptr(),
+         _f32(state_in, st), _f32(dstate_out, st), *_rows(dq, x), *_rows(dk, x), *_rows(dv, x), _f32(dstate_in, st),
+         d ** -0.5 if scale is None else scale, t, n, h, d, *_space(workspace))
 
 
 def vsa_decay_attn_step(q, k, v, log_decay, state, out, scale=None, state_out=None, stream=None):
     """One new token for each of the sequences: q, k, v, out bf16 [batch, heads,
     d], state fp32 [batch, heads, d, d], updated in place or into state_out."""
-    n, h, d = q.shape
+    n, h, d = _packed_shape(q)
+    x, st = q.shape, (n, h, d, d)
     state_out = state if state_out is None else state_out
-    with _same_device(q, k, v, log_decay, state, state_out, out):
-        _lib.check("vsa_decay_attn_step", _lib.lib().vsa_decay_attn_step(
-            *_rows(q), *_rows(k, h, d, n), *_rows(v, h, d, n), _f32(log_decay, (h,)), _f32(state, (n, h, d, d)),
-            _f32(state_out, (n, h, d, d)), *_rows(out, h, d, n), d ** -0.5 if scale is None else scale, n, h, d,
-            _stream(stream)))
+    _run("vsa_decay_attn_step", stream, (q, k, v, log_decay, state, state_out, out),
+         *_rows(q, x), *_rows(k, x), *_rows(v, x), _f32(log_decay, (h,)), _f32(state, st), _f32(state_out, st),
+         *_rows(out, x), d ** -0.5 if scale is None else scale, n, h, d)
 
 
 def vsa_device_status(workspace, stream=None) -> int:
