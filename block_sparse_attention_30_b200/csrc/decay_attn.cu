@@ -117,27 +117,6 @@ __device__ __forceinline__ void split8(uint4& x, float w, uint4& lo) {
     split_pair(x.w, w, x.w, lo.w);
 }
 
-// Four lanes with four 16-byte units of a row each -> unit (lane & 3) of each
-// of the four rows, so that their stores fill 64 bytes of a row together.
-__device__ __forceinline__ void transpose_units(uint4 (&u)[4], int lane) {
-    uint32_t* x = reinterpret_cast<uint32_t*>(u);
-#pragma unroll
-    for (int m = 2; m > 0; m >>= 1) {
-        const bool up = lane & m;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (i & m) continue;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                uint32_t &a = x[4 * i + e], &b = x[4 * (i + m) + e];
-                const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? a : b, m);
-                if (up) a = got;
-                else b = got;
-            }
-        }
-    }
-}
-
 // ---------------------------------------------------------------- border sums
 template <int D>
 struct DecStateCfg {

@@ -5,6 +5,7 @@
 #include <cstdint>
 
 #include "common.cuh"
+#include "sm100.cuh"
 
 namespace vsa {
 
@@ -75,6 +76,137 @@ __device__ __forceinline__ SeqTile find_tile(const int32_t* __restrict__ cu, int
         base += __shfl_sync(0xffffffffu, incl, 31);
     }
     return {-1, 0};
+}
+
+// Four lanes with four 16-byte units of a row each -> unit (lane & 3) of each
+// of the four rows, so that their stores fill 64 bytes of a row together.
+__device__ __forceinline__ void transpose_units(uint4 (&u)[4], int lane) {
+    uint32_t* x = reinterpret_cast<uint32_t*>(u);
+#pragma unroll
+    for (int m = 2; m > 0; m >>= 1) {
+        const bool up = lane & m;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i & m) continue;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                uint32_t &a = x[4 * i + e], &b = x[4 * (i + m) + e];
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? a : b, m);
+                if (up) a = got;
+                else b = got;
+            }
+        }
+    }
+}
+
+// Where four lanes' rows start (elements), -1 for a row that is not stored; for
+// a warp whose lanes hold one row each.
+struct QuadRows {
+    long long at[4];
+    __device__ __forceinline__ QuadRows(long long own) {
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) at[e] = __shfl_sync(0xffffffffu, own, (lane & ~3) + e);
+    }
+};
+
+// 32 columns of every lane's row, as bf16 or fp32, 64 bytes of a row at a time
+// (a lane that stores 16 bytes of its own row touches 32 lines per warp; eight
+// such warps keep the load/store unit busy for 4000 cycles).
+__device__ __forceinline__ void store_rows(__nv_bfloat16* p, const QuadRows& rows, const float (&v)[32]) {
+    const int lane = threadIdx.x & 31;
+    uint4 u[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        u[e] = make_uint4(pack_bf16x2(v[8 * e], v[8 * e + 1]), pack_bf16x2(v[8 * e + 2], v[8 * e + 3]),
+                          pack_bf16x2(v[8 * e + 4], v[8 * e + 5]), pack_bf16x2(v[8 * e + 6], v[8 * e + 7]));
+    transpose_units(u, lane);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (rows.at[e] >= 0) *reinterpret_cast<uint4*>(p + rows.at[e] + (lane & 3) * 8) = u[e];
+}
+__device__ __forceinline__ void store_rows(float* p, const QuadRows& rows, const float (&v)[32]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int h = 0; h < 32; h += 16) {
+        uint4 u[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            u[e] = make_uint4(__float_as_uint(v[h + 4 * e]), __float_as_uint(v[h + 4 * e + 1]), __float_as_uint(v[h + 4 * e + 2]),
+                              __float_as_uint(v[h + 4 * e + 3]));
+        transpose_units(u, lane);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (rows.at[e] >= 0) *reinterpret_cast<uint4*>(p + rows.at[e] + h + (lane & 3) * 4) = u[e];
+    }
+}
+
+// A CTA's queue of work: one warp finds what the CTA is to do and hands it to
+// the other warps, two pieces ahead at most.  Where a CTA has an SM to itself
+// it then takes over CTAs that have not started yet from the grid (cluster
+// launch control): the latency of its start and end overlaps with the pieces
+// around it, and the hardware's own queue still balances long and short ones.
+// (Two CTAs on an SM hide each other's.)  W is a plain struct with an int
+// `seq`, -1 for the end.
+template <typename W>
+struct WorkQueue {
+    uint4 answer;
+    W slot[2];
+    uint64_t full[2], empty[2], asked;
+};
+
+template <typename W>
+__device__ __forceinline__ void queue_init(WorkQueue<W>* q, int consumer_warps) {
+    for (int x = 0; x < 2; ++x) { sm100::mbar_init(&q->full[x], 1); sm100::mbar_init(&q->empty[x], consumer_warps); }
+    sm100::mbar_init(&q->asked, 1);
+}
+
+// The producing warp's whole run; make(id) (whole warp) gives the work of CTA
+// `id`, which is left out if its seq is below 0.  False: a wait gave up.
+template <bool TAKE_OVER, typename W, typename F>
+__device__ __forceinline__ bool queue_produce(WorkQueue<W>* q, const volatile int* abort, F make) {
+    const int lane = threadIdx.x & 31;
+    int id = blockIdx.x, k = 0;
+    auto put = [&](const W& w) {
+        if (k >= 2 && !__all_sync(0xffffffffu, sm100::mbar_wait(&q->empty[k & 1], (k / 2 - 1) & 1, abort))) return false;
+        if (lane == 0) {
+            q->slot[k & 1] = w;
+            sm100::mbar_arrive(&q->full[k & 1]);
+        }
+        __syncwarp();
+        ++k;
+        return true;
+    };
+    bool ok = true;
+    for (int asked = 0; id >= 0 && ok; ++asked) {
+        if (TAKE_OVER && lane == 0) {
+            sm100::mbar_arrive_expect_tx(&q->asked, 16);
+            sm100::try_cancel(&q->answer, &q->asked);
+        }
+        __syncwarp();
+        const W w = make(id);
+        if (w.seq >= 0) ok = put(w);
+        if (!TAKE_OVER) break;
+        // an answer on its way has to arrive before the CTA leaves
+        const bool here = __all_sync(0xffffffffu, sm100::wait_noabort(&q->asked, asked & 1));
+        if (!here) return false;
+        id = sm100::cancelled_ctaid(&q->answer);
+        __syncwarp();
+        sm100::fence_proxy_async_smem();             // read before the next answer is written
+    }
+    W end{};
+    end.seq = -1;
+    return ok && put(end);
+}
+
+// Piece k of the queue (whole warp); false: a wait gave up.
+template <typename W>
+__device__ __forceinline__ bool queue_get(WorkQueue<W>* q, int k, const volatile int* abort, W& w) {
+    if (!__all_sync(0xffffffffu, sm100::mbar_wait(&q->full[k & 1], (k / 2) & 1, abort))) return false;
+    w = q->slot[k & 1];
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) sm100::mbar_arrive(&q->empty[k & 1]);
+    return true;
 }
 
 }  // namespace vsa

@@ -56,7 +56,7 @@ struct PackCfg {
     static constexpr int TILE = NCH * CHUNK;             // 128 rows of one tensor
     static constexpr int NST = (NT == 2 ? 5 : 2) * 128 / D;   // K/V ring stages
     static constexpr int BAR_OFF = (NT + NST) * TILE;
-    static constexpr int SMEM = BAR_OFF + 512;
+    static constexpr int SMEM = BAR_OFF + 1024;
     static constexpr int THREADS = 128 * (NT + 1);       // softmax warpgroups and the loads' and MMAs'
     // registers a thread: 168 at launch, 72 + 2 * 216 = 3 * 168; 128 at launch, 56 + 200 = 2 * 128
     static constexpr int REG_LOAD = NT == 2 ? 72 : 56, REG_SOFT = NT == 2 ? 216 : 200;
@@ -67,32 +67,38 @@ struct PackCfg {
 static_assert(PackCfg<128, 2>::SMEM <= 232448 && PackCfg<64, 2>::SMEM <= 232448, "shared memory");
 static_assert(PackCfg<128, 1>::SMEM <= 115712 && PackCfg<64, 1>::SMEM <= 115712, "shared memory of two CTAs");
 
-template <int D, int NT>
-struct PackBars {
-    uint64_t q_full[2];
-    uint64_t full[PackCfg<D, NT>::NST], empty[PackCfg<D, NT>::NST];
-    uint64_t s_full[2], p_half[2], p_full[2], o_full[2];
-    uint64_t mma_done;                   // every MMA of the CTA finished
-    uint32_t tmem_base;
-    int abort;
-};
-static_assert(sizeof(PackBars<64, 2>) <= 512, "barrier block");
-
-// What one CTA works on: rows of the tile pair and its key blocks.
+// What a CTA works on: the rows of its tiles and their key blocks.
 struct PackWork {
     int seq;             // -1: nothing
     int q0, nq;          // the sequence's first query row and query count
     int k0, nk;
     int tok[2];          // first token (within the sequence) of each tile
     int nb[2];           // key blocks each tile needs (0: none visible)
-    int lo, hi;          // this CTA's share of the blocks [lo, hi)
+    int lo, hi;          // its share of the blocks [lo, hi)
+    int kvh, split;
 };
 
+template <int D, int NT>
+struct PackBars {
+    WorkQueue<PackWork> queue;
+    uint64_t q_full[2], q_empty;
+    uint64_t full[PackCfg<D, NT>::NST], empty[PackCfg<D, NT>::NST];
+    uint64_t s_full[2], p_half[2], p_full[2], o_full[2], o_free[2];
+    uint64_t mma_done;                   // every MMA of the CTA finished
+    uint32_t tmem_base;
+    int abort;
+};
+static_assert(sizeof(PackBars<64, 2>) <= 1024, "barrier block");
+
 __device__ __forceinline__ PackWork pack_work(const int32_t* __restrict__ cu_q, const int32_t* __restrict__ cu_k,
-                                              const PackedShape& s, int nt, int tok_per_tile, int tiles, int t,
-                                              int causal, int n_splits, int split, int* status) {
-    PackWork w;
-    const SeqTile at = find_tile(cu_q, s.n_seq, s.total_q, nt * tok_per_tile, tiles - 1 - t, status);
+                                              const PackedShape& s, int nt, int tok_per_tile, int tiles, int id,
+                                              int causal, int n_splits, int* status) {
+    PackWork w{};
+    // the shares of a tile start together, so that long sequences come first as a whole
+    w.split = id % n_splits;
+    id /= n_splits;
+    w.kvh = id % s.heads_kv;
+    const SeqTile at = find_tile(cu_q, s.n_seq, s.total_q, nt * tok_per_tile, tiles - 1 - id / s.heads_kv, status);
     w.seq = at.seq;
     if (at.seq < 0) return w;
     const SeqRange q = seq_range(cu_q, at.seq, s.total_q, status), k = seq_range(cu_k, at.seq, s.total_k, status);
@@ -106,7 +112,7 @@ __device__ __forceinline__ PackWork pack_work(const int32_t* __restrict__ cu_q, 
     }
     const int nb = max(w.nb[0], w.nb[1]);
     const int per = (nb + n_splits - 1) / n_splits;
-    w.lo = min(nb, split * per);
+    w.lo = min(nb, w.split * per);
     w.hi = min(nb, w.lo + per);
     return w;
 }
@@ -125,27 +131,25 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
         if (threadIdx.x == 0) report(status, kStatusMisaligned);
         return;
     }
-    const int tid = threadIdx.x, warp = warp_uniform(tid >> 5);
+    const int tid = threadIdx.x, warp = warp_uniform(tid >> 5), lane = tid & 31;
     const int group = sh.heads_q / sh.heads_kv;
-    // the shares of a tile start together, so that long sequences come first as a whole
-    const int split = blockIdx.x % n_splits, item = blockIdx.x / n_splits;
-    const int kvh = item % sh.heads_kv;
-    const PackWork w = pack_work(cu_q, cu_k, sh, NT, tok_per_tile, tiles, item / sh.heads_kv, causal, n_splits, split, status);
-    if (w.seq < 0) return;                               // uniform over the CTA
     uint8_t* sQ = smem;
     uint8_t* ring = smem + NT * C::TILE;
     PackBars<D, NT>* bars = reinterpret_cast<PackBars<D, NT>*>(smem + C::BAR_OFF);
     volatile int* abort_flag = &bars->abort;
     if (tid == 0) {
         bars->abort = 0;
+        queue_init(&bars->queue, 4 * NT + 2);
         for (int x = 0; x < NT; ++x) {
             mbar_init(&bars->q_full[x], 1);
             mbar_init(&bars->s_full[x], 1);
             mbar_init(&bars->p_half[x], 128);
             mbar_init(&bars->p_full[x], 128);
             mbar_init(&bars->o_full[x], 1);
+            mbar_init(&bars->o_free[x], 128);
         }
         for (int x = 0; x < C::NST; ++x) { mbar_init(&bars->full[x], 1); mbar_init(&bars->empty[x], 1); }
+        mbar_init(&bars->q_empty, 1);
         mbar_init(&bars->mma_done, 1);
         fence_barrier_init();
     }
@@ -155,56 +159,81 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
     tc_fence_after();
     const uint32_t tbase = warp_uniform(bars->tmem_base);
     auto fail = [&]() { *abort_flag = 1; report(status, kStatusTimeout); };
-    const int n = warp_uniform(w.hi - w.lo);             // blocks hi - 1 down to lo: step t is block hi - 1 - t
-    // tile x takes part from step first[x] on
-    const int first[2] = {warp_uniform(max(0, w.hi - w.nb[0])), warp_uniform(max(0, w.hi - w.nb[1]))};
+    // Every role walks the queue.  Of work with n = hi - lo > 0 blocks, step t
+    // is block hi - 1 - t, and tile x takes part from step first(x) on (with
+    // fewer steps than that, not at all).  Phases and ring items are counted
+    // on from work to work.
+    auto first_step = [](const PackWork& w, int x) { return max(0, w.hi - w.nb[x]); };
 
     if (warp >= 4 * NT) {
       reg_dec<C::REG_LOAD>();
-      if (warp == 4 * NT) {
-        if (elect_one()) {
-            // ------------------------------------------------------ loads
-            // ring item 2 t is K of step t, item 2 t + 1 its V
-            bool q_issued[2] = {false, false};
-            for (int x = 0; x < NT && n > 0; ++x) {
-                if (w.tok[x] >= w.nq) continue;
-                mbar_arrive_expect_tx(&bars->q_full[x], C::NCH * tok_per_tile * group * 128);
-                for (int c = 0; c < C::NCH; ++c)
-                    tma_load_3d(sQ + x * C::TILE + c * C::CHUNK, &mq, &bars->q_full[x], 64 * c, kvh * group,
-                                w.q0 + w.tok[x]);
-                q_issued[x] = true;
+      if (warp == 4 * NT + 2) {
+        if (!queue_produce<NT == 2>(&bars->queue, abort_flag, [&](int id) {
+                return pack_work(cu_q, cu_k, sh, NT, tok_per_tile, tiles, id, causal, n_splits, status);
+            }))
+            fail();
+      } else if (warp == 4 * NT) {
+        // ---------------------------------------------------------- loads
+        // ring item r0 + 2 t is K of step t, r0 + 2 t + 1 its V
+        int r0 = 0, works = 0, issued = 0, q_count[2] = {0, 0};
+        bool ok = true;
+        for (int k = 0; ok; ++k) {
+            PackWork w;
+            if (!(ok = queue_get(&bars->queue, k, abort_flag, w)) || w.seq < 0) break;
+            const int n = w.hi - w.lo;
+            if (n == 0) continue;
+            // Q's place is free once the last scores of the work before are finished
+            if (works > 0 && !(ok = __all_sync(0xffffffffu, mbar_wait(&bars->q_empty, (works - 1) & 1, abort_flag)))) break;
+            ++works;
+            if (lane == 0) {
+                for (int x = 0; x < NT; ++x) {
+                    if (first_step(w, x) >= n) continue;
+                    mbar_arrive_expect_tx(&bars->q_full[x], C::NCH * tok_per_tile * group * 128);
+                    for (int c = 0; c < C::NCH; ++c)
+                        tma_load_3d(sQ + x * C::TILE + c * C::CHUNK, &mq, &bars->q_full[x], 64 * c, w.kvh * group, w.q0 + w.tok[x]);
+                    ++q_count[x];
+                }
+                for (int i = 0; i < 2 * n; ++i) {
+                    const int r = r0 + i, st = r % C::NST;
+                    if (r >= C::NST && !(ok = mbar_wait(&bars->empty[st], ((r / C::NST) - 1) & 1, abort_flag))) break;
+                    mbar_arrive_expect_tx(&bars->full[st], C::TILE);
+                    for (int c = 0; c < C::NCH; ++c)
+                        tma_load_3d(ring + st * C::TILE + c * C::CHUNK, (i & 1) ? &mv : &mk, &bars->full[st], 64 * c, w.kvh,
+                                    w.k0 + 128 * (w.hi - 1 - (i >> 1)));
+                    ++issued;
+                }
             }
-            int issued = 0;
-            for (int i = 0; i < 2 * n; ++i) {
-                const int st = i % C::NST;
-                if (i >= C::NST && !mbar_wait(&bars->empty[st], ((i / C::NST) - 1) & 1, abort_flag)) { fail(); break; }
-                const int row = w.k0 + 128 * (w.hi - 1 - (i >> 1));
-                const CUtensorMap* map = (i & 1) ? &mv : &mk;
-                mbar_arrive_expect_tx(&bars->full[st], C::TILE);
-                for (int c = 0; c < C::NCH; ++c)
-                    tma_load_3d(ring + st * C::TILE + c * C::CHUNK, map, &bars->full[st], 64 * c, kvh, row);
-                ++issued;
-            }
-            if (*abort_flag) {
-                // drain: every load must land before the CTA's shared memory is given up
-                for (int x = 0; x < NT; ++x) if (q_issued[x]) wait_noabort(&bars->q_full[x], 0);
-                for (int i = max(0, issued - C::NST); i < issued; ++i)
-                    wait_noabort(&bars->full[i % C::NST], (i / C::NST) & 1);
-            }
+            __syncwarp();
+            ok = __all_sync(0xffffffffu, ok);
+            r0 += 2 * n;
+        }
+        if (!ok) fail();
+        if (lane == 0 && *abort_flag) {
+            // drain: every load must land before the CTA's shared memory is given up
+            for (int x = 0; x < NT; ++x)
+                if (q_count[x]) wait_noabort(&bars->q_full[x], (q_count[x] - 1) & 1);
+            for (int i = max(0, issued - C::NST); i < issued; ++i) wait_noabort(&bars->full[i % C::NST], (i / C::NST) & 1);
         }
       } else if (warp == 4 * NT + 1) {
-        if (n > 0) {
-            // ------------------------------------------------------- MMAs
-            // (the whole warp walks the loop, so that every branch and value is
-            // uniform; one elected lane issues)
-            const uint32_t id_s = idesc_bf16_f32(128, 128, false, false);
-            const uint32_t id_o = idesc_bf16_f32(128, D, false, true);
-            const uint64_t q_desc = smem_desc_sw128(smem_u32(sQ), 16, 1024);
-            const uint64_t k_desc = smem_desc_sw128(smem_u32(ring), 16, 1024), v_desc = smem_desc_sw128(smem_u32(ring), C::CHUNK, 1024);
-            auto wait = [&](uint64_t* bar, int parity) { return __all_sync(0xffffffffu, mma_wait(bar, parity, abort_flag)) != 0; };
-            auto item = [&](int i) { return wait(&bars->full[i % C::NST], (i / C::NST) & 1); };
+        // ----------------------------------------------------------- MMAs
+        // (the whole warp walks the loop, so that every branch and value is
+        // uniform; one elected lane issues)
+        const uint32_t id_s = idesc_bf16_f32(128, 128, false, false);
+        const uint32_t id_o = idesc_bf16_f32(128, D, false, true);
+        const uint64_t q_desc = smem_desc_sw128(smem_u32(sQ), 16, 1024);
+        const uint64_t k_desc = smem_desc_sw128(smem_u32(ring), 16, 1024), v_desc = smem_desc_sw128(smem_u32(ring), C::CHUNK, 1024);
+        auto wait = [&](uint64_t* bar, int parity) { return __all_sync(0xffffffffu, mma_wait(bar, parity, abort_flag)) != 0; };
+        int r0 = 0, steps[2] = {0, 0}, parts[2] = {0, 0};
+        bool ok = true;
+        for (int k = 0; ok; ++k) {
+            PackWork w;
+            if (!(ok = queue_get(&bars->queue, k, abort_flag, w)) || w.seq < 0) break;
+            const int n = warp_uniform(w.hi - w.lo);
+            if (n == 0) continue;
+            const int first[2] = {warp_uniform(first_step(w, 0)), warp_uniform(first_step(w, 1))};
+            auto item = [&](int i) { return wait(&bars->full[(r0 + i) % C::NST], ((r0 + i) / C::NST) & 1); };
             auto issue_s = [&](int x, int t) {
-                const uint64_t a0 = desc_add(q_desc, x * C::TILE), b0 = desc_add(k_desc, ((2 * t) % C::NST) * C::TILE);
+                const uint64_t a0 = desc_add(q_desc, x * C::TILE), b0 = desc_add(k_desc, ((r0 + 2 * t) % C::NST) * C::TILE);
                 if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
@@ -216,7 +245,7 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
                 __syncwarp();
             };
             auto issue_o = [&](int x, int t, int half) {     // 64 keys
-                const uint64_t b0 = desc_add(v_desc, ((2 * t + 1) % C::NST) * C::TILE);
+                const uint64_t b0 = desc_add(v_desc, ((r0 + 2 * t + 1) % C::NST) * C::TILE);
                 if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)           // 16 keys per MMA
@@ -226,9 +255,8 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
                 }
                 __syncwarp();
             };
-            bool ok = true;
             for (int x = 0; x < NT && ok; ++x)
-                if (first[x] < n) ok = wait(&bars->q_full[x], 0);
+                if (first[x] < n) ok = wait(&bars->q_full[x], parts[x] & 1);
             // step t: P V of step t, then S of step t + 1 over the same columns
             // (MMAs of one thread run in issue order); step -1 has only the S
             for (int t = -1; t < n && ok; ++t) {
@@ -237,10 +265,13 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
                 for (int x = 0; x < NT; ++x) {
                     if (t >= first[x] && t >= 0) {
                         if (!have_v) { ok = item(2 * t + 1); have_v = true; }
-                        if (!ok || !(ok = wait(&bars->p_half[x], (t - first[x]) & 1))) break;
+                        // the work before has left O
+                        if (ok && t == first[x] && parts[x] > 0) ok = wait(&bars->o_free[x], (parts[x] - 1) & 1);
+                        const int parity = (steps[x] + t - first[x]) & 1;
+                        if (!ok || !(ok = wait(&bars->p_half[x], parity))) break;
                         tc_fence_after();
                         issue_o(x, t, 0);
-                        if (!(ok = wait(&bars->p_full[x], (t - first[x]) & 1))) break;
+                        if (!(ok = wait(&bars->p_full[x], parity))) break;
                         tc_fence_after();
                         issue_o(x, t, 1);
                     }
@@ -253,169 +284,174 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
                 }
                 if (!ok) break;
                 if (elect_one()) {
-                    if (t >= 0) mma_commit(&bars->empty[(2 * t + 1) % C::NST]);
-                    if (t + 1 < n) mma_commit(&bars->empty[(2 * t + 2) % C::NST]);
+                    if (t >= 0) mma_commit(&bars->empty[(r0 + 2 * t + 1) % C::NST]);
+                    if (t + 1 < n) mma_commit(&bars->empty[(r0 + 2 * t + 2) % C::NST]);
+                    if (t + 2 == n) mma_commit(&bars->q_empty);
                 }
                 __syncwarp();
             }
-            if (!ok) fail();
-            if (elect_one()) mma_commit(&bars->mma_done);
-            __syncwarp();
-            wait_noabort(&bars->mma_done, 0);
+            r0 += 2 * n;
+#pragma unroll
+            for (int x = 0; x < NT; ++x)
+                if (first[x] < n) { steps[x] += n - first[x]; ++parts[x]; }
         }
+        if (!ok) fail();
+        if (elect_one()) mma_commit(&bars->mma_done);
+        __syncwarp();
+        wait_noabort(&bars->mma_done, 0);
       }
     } else {
         reg_inc<C::REG_SOFT>();
         // ------------------------------------------------------- softmax
         const int x = warp >> 2;                         // tile
         const int r = tid & 127;                         // row of the tile
-        const int tok = w.tok[x] + r / group;            // token within the sequence
-        const bool valid = r < tok_per_tile * group && tok < w.nq;
-        const int head = kvh * group + r % group;
-        const int lim = valid ? seen_keys(tok, w.nq, w.nk, causal) : 0;
-        const int lim_min = seen_keys(w.tok[x], w.nq, w.nk, causal);   // of the tile's first token: the smallest
         const uint32_t lane_base = tbase + ((uint32_t)(32 * (warp & 3)) << 16);
         const uint32_t tS = lane_base + C::S_COL + 128 * x, tO = lane_base + C::O_COL + D * x;
-        float m_run = -CUDART_INF_F, l_run = 0.f;
+        int r0 = 0, steps = 0, parts = 0;
         bool ok = true;
-        const int f = first[x];
-        // a warp without rows has nothing to compute: what it leaves in its
-        // rows of P only reaches its own rows of O, which are not stored
-        const bool idle = !__any_sync(0xffffffffu, valid);
-        for (int t = f; t < n; ++t) {
-            const int key0 = 128 * (w.hi - 1 - t);
-            if (key0 + 128 > w.nk) {
-                // the sequence's last, partial block (step 0): zero V's rows behind it
-                if (!__all_sync(0xffffffffu, mbar_wait(&bars->full[(2 * t + 1) % C::NST], ((2 * t + 1) / C::NST) & 1, abort_flag))) { ok = false; break; }
-                uint8_t* v = ring + ((2 * t + 1) % C::NST) * C::TILE;
-                const int z0 = w.nk - key0;
-                for (int u = r; u < (128 - z0) * 8 * C::NCH; u += 128)
-                    *reinterpret_cast<uint4*>(v + (u % C::NCH) * C::CHUNK + z0 * 128 + (u / C::NCH) * 16) = make_uint4(0, 0, 0, 0);
-                fence_proxy_async_smem();
-            }
-            if (!__all_sync(0xffffffffu, mbar_wait(&bars->s_full[x], (t - f) & 1, abort_flag))) { ok = false; break; }
-            if (idle) {
-                mbar_arrive(&bars->p_half[x]);
-                mbar_arrive(&bars->p_full[x]);
-                continue;
-            }
-            tc_fence_after();
-            float s[128];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(tS + 32 * c, *reinterpret_cast<float(*)[32]>(&s[32 * c]));
-            tmem_wait_ld();
-            if (key0 + 128 > lim_min) {                  // uniform over the tile
-                const int seen = lim - key0;
-#pragma unroll
-                for (int e = 0; e < 128; ++e)
-                    if (e >= seen) s[e] = -CUDART_INF_F;
-            }
-            float m0 = s[0], m1 = s[1], m2 = s[2], m3 = s[3];
-#pragma unroll
-            for (int e = 4; e < 124; e += 8) {
-                m0 = max3f(m0, s[e], s[e + 1]);
-                m1 = max3f(m1, s[e + 2], s[e + 3]);
-                m2 = max3f(m2, s[e + 4], s[e + 5]);
-                m3 = max3f(m3, s[e + 6], s[e + 7]);
-            }
-            m0 = max3f(m0, s[124], s[125]);
-            m1 = max3f(m1, s[126], s[127]);
-            const float mx = fmaxf(max3f(m0, m1, m2), m3) * scale_log2;
-            const bool raise = mx > m_run + 8.f;
-            const float alpha = raise ? ex2(m_run - mx) : 1.f;   // 0 from -inf
-            if (raise) m_run = mx;
-            l_run *= alpha;
-            // P V of the step before is finished (s_full was committed behind
-            // it), so O can be rescaled here; step f has no O yet
-            if (t > f && __any_sync(0xffffffffu, raise)) {
-#pragma unroll
-                for (int c = 0; c < D; c += 32) {
-                    float o[32];
-                    tmem_ld_32x32b_x32(tO + c, o);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] *= alpha;
-                    tmem_st_32x32b_x32f(tO + c, o);
+        for (int k = 0; ok; ++k) {
+            PackWork w;
+            if (!(ok = queue_get(&bars->queue, k, abort_flag, w)) || w.seq < 0) break;
+            const int n = w.hi - w.lo, f = first_step(w, x);
+            const int tok = w.tok[x] + r / group;        // token within the sequence
+            const bool valid = r < tok_per_tile * group && tok < w.nq;
+            const int head = w.kvh * group + r % group;
+            const int lim = valid ? seen_keys(tok, w.nq, w.nk, causal) : 0;
+            const int lim_min = seen_keys(w.tok[x], w.nq, w.nk, causal);   // of the tile's first token: the smallest
+            float m_run = -CUDART_INF_F, l_run = 0.f;
+            // a warp without rows has nothing to compute: what it leaves in its
+            // rows of P only reaches its own rows of O, which are not stored
+            const bool idle = !__any_sync(0xffffffffu, valid);
+            for (int t = f; t < n; ++t) {
+                const int key0 = 128 * (w.hi - 1 - t);
+                if (key0 + 128 > w.nk) {
+                    // the sequence's last, partial block (step 0): zero V's rows behind it
+                    const int i = r0 + 2 * t + 1;
+                    if (!__all_sync(0xffffffffu, mbar_wait(&bars->full[i % C::NST], (i / C::NST) & 1, abort_flag))) { ok = false; break; }
+                    uint8_t* v = ring + (i % C::NST) * C::TILE;
+                    const int z0 = w.nk - key0;
+                    for (int u = r; u < (128 - z0) * 8 * C::NCH; u += 128)
+                        *reinterpret_cast<uint4*>(v + (u % C::NCH) * C::CHUNK + z0 * 128 + (u / C::NCH) * 16) = make_uint4(0, 0, 0, 0);
+                    fence_proxy_async_smem();
                 }
-            }
-            const float m_sub = m_run == -CUDART_INF_F ? 0.f : m_run;
-            const uint64_t sc2 = f32x2(scale_log2, scale_log2), nm2 = f32x2(-m_sub, -m_sub);
-            uint64_t acc0 = 0, acc1 = 0;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                uint32_t pk[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    float t0, t1;
-                    unf32x2(fma_f32x2(f32x2(s[32 * c + 2 * e], s[32 * c + 2 * e + 1]), sc2, nm2), t0, t1);
-                    const float p0 = ex2(t0), p1 = ex2(t1);
-                    pk[e] = pack_bf16x2(p0, p1);
-                    if (e & 1) acc1 = add_f32x2(acc1, f32x2(p0, p1));
-                    else acc0 = add_f32x2(acc0, f32x2(p0, p1));
-                }
-                tmem_st_32x32b_x16(tS + 16 * c, pk);
-                if (c == 1) {                            // P V starts on the first half of the keys
-                    tmem_wait_st();
-                    tc_fence_before();
+                if (!__all_sync(0xffffffffu, mbar_wait(&bars->s_full[x], (steps + t - f) & 1, abort_flag))) { ok = false; break; }
+                if (idle) {
                     mbar_arrive(&bars->p_half[x]);
+                    mbar_arrive(&bars->p_full[x]);
+                    continue;
                 }
+                tc_fence_after();
+                float s[128];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(tS + 32 * c, *reinterpret_cast<float(*)[32]>(&s[32 * c]));
+                tmem_wait_ld();
+                if (key0 + 128 > lim_min) {              // uniform over the tile
+                    const int seen = lim - key0;
+#pragma unroll
+                    for (int e = 0; e < 128; ++e)
+                        if (e >= seen) s[e] = -CUDART_INF_F;
+                }
+                float m0 = s[0], m1 = s[1], m2 = s[2], m3 = s[3];
+#pragma unroll
+                for (int e = 4; e < 124; e += 8) {
+                    m0 = max3f(m0, s[e], s[e + 1]);
+                    m1 = max3f(m1, s[e + 2], s[e + 3]);
+                    m2 = max3f(m2, s[e + 4], s[e + 5]);
+                    m3 = max3f(m3, s[e + 6], s[e + 7]);
+                }
+                m0 = max3f(m0, s[124], s[125]);
+                m1 = max3f(m1, s[126], s[127]);
+                const float mx = fmaxf(max3f(m0, m1, m2), m3) * scale_log2;
+                const bool raise = mx > m_run + 8.f;
+                const float alpha = raise ? ex2(m_run - mx) : 1.f;   // 0 from -inf
+                if (raise) m_run = mx;
+                l_run *= alpha;
+                // P V of the step before is finished (s_full was committed behind
+                // it), so O can be rescaled here; step f has no O yet
+                if (t > f && __any_sync(0xffffffffu, raise)) {
+#pragma unroll
+                    for (int c = 0; c < D; c += 32) {
+                        float o[32];
+                        tmem_ld_32x32b_x32(tO + c, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] *= alpha;
+                        tmem_st_32x32b_x32f(tO + c, o);
+                    }
+                }
+                const float m_sub = m_run == -CUDART_INF_F ? 0.f : m_run;
+                const uint64_t sc2 = f32x2(scale_log2, scale_log2), nm2 = f32x2(-m_sub, -m_sub);
+                uint64_t acc0 = 0, acc1 = 0;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        float t0, t1;
+                        unf32x2(fma_f32x2(f32x2(s[32 * c + 2 * e], s[32 * c + 2 * e + 1]), sc2, nm2), t0, t1);
+                        const float p0 = ex2(t0), p1 = ex2(t1);
+                        pk[e] = pack_bf16x2(p0, p1);
+                        if (e & 1) acc1 = add_f32x2(acc1, f32x2(p0, p1));
+                        else acc0 = add_f32x2(acc0, f32x2(p0, p1));
+                    }
+                    tmem_st_32x32b_x16(tS + 16 * c, pk);
+                    if (c == 1) {                        // P V starts on the first half of the keys
+                        tmem_wait_st();
+                        tc_fence_before();
+                        mbar_arrive(&bars->p_half[x]);
+                    }
+                }
+                float a0, a1, b0, b1;
+                unf32x2(acc0, a0, a1);
+                unf32x2(acc1, b0, b1);
+                l_run += (a0 + a1) + (b0 + b1);
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(&bars->p_full[x]);
             }
-            float a0, a1, b0, b1;
-            unf32x2(acc0, a0, a1);
-            unf32x2(acc1, b0, b1);
-            l_run += (a0 + a1) + (b0 + b1);
-            tmem_wait_st();
-            tc_fence_before();
-            mbar_arrive(&bars->p_full[x]);
-        }
-        if (ok && f < n && !__all_sync(0xffffffffu, mbar_wait(&bars->o_full[x], 0, abort_flag))) ok = false;
-        if (!ok) fail();
-        if (ok) {
-            tc_fence_after();
+            if (!ok) break;
+            const bool took = f < n;                     // uniform over the tile
+            if (took) {
+                if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_full[x], parts & 1, abort_flag)))) break;
+                tc_fence_after();
+                steps += n - f;
+                ++parts;
+            }
+            r0 += 2 * n;
             const bool none = l_run == 0.f;               // the row saw no key (of this share)
             const float inv = none ? 0.f : 1.f / l_run;
             const float row_lse = none ? -CUDART_INF_F : m_run + log2f(l_run);
             const long long row = (long long)w.q0 + tok;
             if (n_splits > 1) {
                 // partial result of this share, joined by combine_kernel
-                if (valid) part_lse[((long long)split * sh.heads_q + head) * sh.total_q + row] = row_lse;
-                float* po = part_o + (((long long)split * sh.total_q + row) * sh.heads_q + head) * D;
-#pragma unroll
-                for (int c = 0; c < D; c += 32) {
-                    float o[32];
-                    if (f < n) { tmem_ld_32x32b_x32(tO + c, o); tmem_wait_ld(); }
-                    if (valid && !none) {
-#pragma unroll
-                        for (int e = 0; e < 32; e += 4)
-                            *reinterpret_cast<float4*>(po + c + e) = make_float4(o[e] * inv, o[e + 1] * inv, o[e + 2] * inv, o[e + 3] * inv);
-                    }
-                }
+                if (valid) part_lse[((long long)w.split * sh.heads_q + head) * sh.total_q + row] = row_lse;
             } else {
                 if (valid && lse) lse[(long long)head * sh.total_q + row] = row_lse;
+            }
+            // where this row goes: 16-bit and 32-bit output, or the share's partial one
+            const long long dense = (row * sh.heads_q + head) * D;
+            const QuadRows rows_b(valid && n_splits == 1 ? row * out_stride + (long long)head * D : -1);
+            const QuadRows rows_f(n_splits > 1 ? (valid && !none ? (long long)w.split * sh.total_q * sh.heads_q * D + dense : -1)
+                                               : (valid && out32 ? dense : -1));
+            float* pf = n_splits > 1 ? part_o : out32;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+                float o[32];
 #pragma unroll
-                for (int c = 0; c < D; c += 32) {
-                    float o[32];
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = 0.f;
-                    if (f < n) { tmem_ld_32x32b_x32(tO + c, o); tmem_wait_ld(); }
-                    if (valid) {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = none ? 0.f : o[e] * inv;
-                        __nv_bfloat16* po = out + row * out_stride + (long long)head * D + c;
-#pragma unroll
-                        for (int e = 0; e < 32; e += 8)
-                            *reinterpret_cast<uint4*>(po + e) = make_uint4(pack_bf16x2(o[e], o[e + 1]), pack_bf16x2(o[e + 2], o[e + 3]),
-                                                                           pack_bf16x2(o[e + 4], o[e + 5]), pack_bf16x2(o[e + 6], o[e + 7]));
-                        if (out32) {
-                            float* p32 = out32 + (row * sh.heads_q + head) * D + c;
-#pragma unroll
-                            for (int e = 0; e < 32; e += 4)
-                                *reinterpret_cast<float4*>(p32 + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-                        }
-                    }
+                for (int e = 0; e < 32; ++e) o[e] = 0.f;
+                if (took) { tmem_ld_32x32b_x32(tO + c, o); tmem_wait_ld(); }
+                if (took && c + 32 == D) {
+                    tc_fence_before();
+                    mbar_arrive(&bars->o_free[x]);
                 }
+                if (idle) continue;
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = none ? 0.f : o[e] * inv;
+                if (n_splits == 1) store_rows(out + c, rows_b, o);
+                if (pf) store_rows(pf + c, rows_f, o);
             }
         }
+        if (!ok) fail();
     }
     tc_fence_before();
     __syncthreads();
