@@ -350,8 +350,9 @@ struct DecOutCfg {
     static constexpr int X_OFF = LO_OFF + TILE;          // the state as bf16: 128 rows (d = 64: hi rows, lo rows) x D
     static constexpr int UNITS = 4 * NCH;                // 16-byte units of the weighted operand per thread pair,
     static constexpr int UNITS_P = D == 128 ? 5 : 2;     // of which the score warps split so many
-    static constexpr int POW_OFF = X_OFF + TILE;         // powers of lam, see the weights: 64 floats, and again one float on
-    static constexpr int BAR_OFF = POW_OFF + 2 * 256 + 16;
+    static constexpr int POW_OFF = X_OFF + TILE;         // powers of lam, see the weights: 64 floats, and again one float on; of two walks
+    static constexpr int POW_FLOATS = 132;
+    static constexpr int BAR_OFF = POW_OFF + 2 * POW_FLOATS * 4;
     static constexpr int SMEM = BAR_OFF + 512;
     static constexpr int THREADS = 768;                  // warpgroups: 2 scores, 2 state, outputs, loads and MMAs; 80 registers a thread
     static constexpr int REG_SCORE = 72, REG_STATE = 104, REG_OUT = 80, REG_LOAD = 48;   // 2 * 72 + 2 * 104 + 80 + 48 = 6 * 80
@@ -359,18 +360,28 @@ struct DecOutCfg {
 };
 static_assert(DecOutCfg<128>::SMEM <= 232448 && DecOutCfg<64>::SMEM <= 232448, "shared memory");
 
+// What decay_out_kernel walks: one segment of one head for one pass.
+struct DecayWork {
+    int seq, pass, head;
+    int begin, len;              // first row and rows
+    int off, rest;               // tokens of the sequence before it and from its first on
+};
+
 template <int D>
 struct DecOutBars {
+    WorkQueue<DecayWork> queue;
     uint64_t b_full[DecOutCfg<D>::NB], ac_full[DecOutCfg<D>::NAC];
     uint64_t u_done[DecOutCfg<D>::NB];   // every product of a step in this slot of B
     uint64_t s_full, p_ready, x_ready, w_ready, o_full, o_free, mma_done;
+    uint64_t pow_ready, lo_ready, lo_free;
     uint32_t tmem_base;
     int abort;
 };
-static_assert(sizeof(DecOutBars<64>) <= 512, "barrier block");
+static_assert(sizeof(DecOutBars<64>) <= 512 && sizeof(DecOutBars<128>) <= 512, "barrier block");
 
 // grid (passes x segments x heads: the passes over one segment run side by
-// side and share its tiles in L2)
+// side and share its tiles in L2).  Every role takes walk after walk from the
+// CTA's queue; steps (chunks), items and phases are counted on from walk to walk.
 template <int D>
 __global__ void __launch_bounds__(DecOutCfg<D>::THREADS, 1)
 decay_out_kernel(const __grid_constant__ DecayPasses passes, const int n_passes, const DecayShape sh,
@@ -382,34 +393,13 @@ decay_out_kernel(const __grid_constant__ DecayPasses passes, const int n_passes,
         return;
     }
     const int tid = threadIdx.x, warp = warp_uniform(tid >> 5), lane = tid & 31;
-    const DecayPass& ps = passes.p[blockIdx.x % n_passes];
-    const int item = blockIdx.x / n_passes, head = item % sh.heads;
-    const bool back = ps.back;
-    const Piece g = find_piece(cu, sh, sh.seg, item / sh.heads, status);
-    if (g.seq < 0) return;
-    const bool g_first = g.off == 0, g_last = g.rest <= sh.seg;
-    const int n = warp_uniform((g.len + 127) / 128);                   // chunks; step t is chunk t, or n - 1 - t backwards
-    auto chunk_of = [&](int t) { return back ? n - 1 - t : t; };
-    const long long own = ((long long)g.seq * sh.heads + head) * D * D;
-    const bool ends = back ? g_first : g_last;           // this CTA reaches the end of the walk
-    float* last = ends && ps.last ? ps.last + own : nullptr;
-    const float* x0 = nullptr;                           // the state before step 0
-    if (back ? g_last : g_first) x0 = ps.first ? ps.first + own : nullptr;
-    else x0 = ps.border + ((long long)((back ? g.begin + sh.seg : g.begin) - sh.part) / sh.part * sh.heads + head) * D * D;
-    if (n == 0) {                                        // an empty sequence: the state goes through
-        if (last)
-            for (int e = tid; e < D * D; e += C::THREADS) last[e] = x0 ? x0[e] : 0.f;
-        return;
-    }
-    const int updates = warp_uniform(last ? n : n - 1);                // steps whose update of the state is needed
     uint8_t* sLo = smem + C::LO_OFF;
     uint8_t* sX = smem + C::X_OFF;
-    float* sPow = reinterpret_cast<float*>(smem + C::POW_OFF);
     DecOutBars<D>* bars = reinterpret_cast<DecOutBars<D>*>(smem + C::BAR_OFF);
     volatile int* abort_flag = &bars->abort;
-    const float l2 = decay_log2(log_decay, head);
     if (tid == 0) {
         bars->abort = 0;
+        queue_init(&bars->queue, 22);
         for (int x = 0; x < C::NB; ++x) { mbar_init(&bars->b_full[x], 1); mbar_init(&bars->u_done[x], 1); }
         for (int x = 0; x < C::NAC; ++x) mbar_init(&bars->ac_full[x], 1);
         mbar_init(&bars->s_full, 1);
@@ -419,13 +409,10 @@ decay_out_kernel(const __grid_constant__ DecayPasses passes, const int n_passes,
         mbar_init(&bars->o_full, 1);
         mbar_init(&bars->o_free, 128);
         mbar_init(&bars->mma_done, 1);
+        mbar_init(&bars->pow_ready, 64);
+        mbar_init(&bars->lo_ready, 128);
+        mbar_init(&bars->lo_free, 128);
         fence_barrier_init();
-    }
-    // forward lam^31 .. lam^0 and zeros, backwards zeros and lam^0 .. lam^31
-    if (tid < 64) {
-        const float y = (back ? tid >= 32 : tid < 32) ? ex2((float)(back ? tid - 32 : 31 - tid) * l2) : 0.f;
-        sPow[tid] = y;
-        sPow[64 + 1 + tid] = y;                          // for pairs that start at an odd place
     }
     if (warp == 21) { tmem_alloc(&bars->tmem_base, 512); tmem_relinquish(); }
     tc_fence_before();
@@ -434,21 +421,28 @@ decay_out_kernel(const __grid_constant__ DecayPasses passes, const int n_passes,
     const uint32_t tbase = warp_uniform(bars->tmem_base);
     auto fail = [&]() { *abort_flag = 1; report(status, kStatusTimeout); };
     // B of step t, and item i of the A and C tiles (A of step t at 2 t, C at 2 t + 1)
-    auto b_slot = [&](int t) { return smem + (t % C::NB) * C::TILE; };
+    auto b_slot = [&](int t) { return (t % C::NB) * C::TILE; };
     auto b_wait = [&](int t) { return mma_wait(&bars->b_full[t % C::NB], (t / C::NB) & 1, abort_flag); };
-    auto ac_slot = [&](int i) { return smem + C::AC_OFF + (i % C::NAC) * C::TILE; };
+    auto ac_slot = [&](int i) { return C::AC_OFF + (i % C::NAC) * C::TILE; };
     auto ac_wait = [&](int i) { return mma_wait(&bars->ac_full[i % C::NAC], (i / C::NAC) & 1, abort_flag); };
     auto u_wait = [&](int t) { return mbar_wait(&bars->u_done[t % C::NB], (t / C::NB) & 1, abort_flag); };
+    // the walk's chunks (step t is chunk t, or chunks - 1 - t backwards), and
+    // whether it reaches the end of its sequence and writes the state there
+    auto chunks = [](const DecayWork& w) { return (w.len + 127) / 128; };
+    auto token = [](const DecayWork& w, bool back, int t) { return 128 * (back ? (w.len + 127) / 128 - 1 - t : t); };
+    auto writes_state = [&](const DecayWork& w) { return passes.p[w.pass].last && (passes.p[w.pass].back ? w.off == 0 : w.rest <= sh.seg); };
+    // steps whose update of the state is needed
+    auto updates_of = [&](const DecayWork& w) { return max(0, chunks(w) - (writes_state(w) ? 0 : 1)); };
 
     // hi and lo of B w for the units [i0, i1) of this one of 256 threads
-    auto split_units = [&](int t, int id, int i0, int i1, int rows) {
+    auto split_units = [&](int t, int id, int i0, int i1, int rows, bool back, float w_scale, float l2) {
         if (!__all_sync(0xffffffffu, b_wait(t))) return false;     // (long done: the scores are)
-        uint8_t* b = b_slot(t);
+        uint8_t* b = smem + b_slot(t);
 #pragma unroll
         for (int i = i0; i < i1; ++i) {
             const int r = id / 8 + 32 * (i & 3);         // token of the chunk
             uint4 y = *reinterpret_cast<const uint4*>(b + id * 16 + 4096 * i), lo;
-            split8(y, ps.w_scale * ex2((float)(back ? r + 1 : rows - 1 - r) * l2), lo);
+            split8(y, w_scale * ex2((float)(back ? r + 1 : rows - 1 - r) * l2), lo);
             if (r >= rows) y = lo = make_uint4(0, 0, 0, 0);
             *reinterpret_cast<uint4*>(b + id * 16 + 4096 * i) = y;
             *reinterpret_cast<uint4*>(sLo + id * 16 + 4096 * i) = lo;
@@ -460,111 +454,160 @@ decay_out_kernel(const __grid_constant__ DecayPasses passes, const int n_passes,
 
     if (warp >= 20) {
       reg_dec<C::REG_LOAD>();
-      if (warp == 20) {
-        if (elect_one()) {
-            // ---------------------------------------------------------- loads
-            // When step t - NB has finished, so has what was in the slots of
-            // B and A (d = 64: and C) of step t; at d = 128 C takes the slot
-            // of A of step t - 1, free with that step's outputs.
-            int nb = 0, nac = 0;
-            auto load = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* full, int t) {
-                const int row = g.begin + 128 * chunk_of(t);
-                mbar_arrive_expect_tx(full, C::TILE);
-                for (int c = 0; c < C::NCH; ++c) tma_load_3d(dst + c * C::CHUNK, map, full, 64 * c, head, row);
-            };
-            auto load_ac = [&](const CUtensorMap* map, int t) {
-                load(ac_slot(nac), map, &bars->ac_full[nac % C::NAC], t);
-                ++nac;
-            };
-            static_assert(D == 128 ? C::NB == 2 && C::NAC == 3 : C::NAC == 2 * C::NB, "which products free a slot");
-            bool ok = true;
-            for (int t = 0; t < n && ok; ++t) {
-                if (t >= C::NB && !(ok = u_wait(t - C::NB))) break;
-                load(b_slot(t), &ps.b, &bars->b_full[t % C::NB], t);
-                ++nb;
-                load_ac(&ps.a, t);
-                if (D == 128 && t > 0 && !(ok = mbar_wait(&bars->o_full, (t - 1) & 1, abort_flag))) break;
-                load_ac(&ps.c, t);
+      if (warp == 22) {
+        const bool ok = queue_produce<true>(&bars->queue, abort_flag, [&](int id) {
+            DecayWork w{};
+            w.pass = id % n_passes;
+            id /= n_passes;
+            w.head = id % sh.heads;
+            const Piece g = find_piece(cu, sh, sh.seg, id / sh.heads, status);
+            w.seq = g.seq;
+            w.begin = g.begin; w.len = g.len; w.off = g.off; w.rest = g.rest;
+            return w;
+        });
+        if (!ok) fail();
+      } else if (warp == 20) {
+        // -------------------------------------------------------------- loads
+        // When step t - NB has finished, so has what was in the slots of B and
+        // A (d = 64: and C) of step t; at d = 128 C takes the slot of A of
+        // step t - 1, free with that step's outputs.
+        static_assert(D == 128 ? C::NB == 2 && C::NAC == 3 : C::NAC == 2 * C::NB, "which products free a slot");
+        int s0 = 0, nb = 0, nac = 0;
+        bool ok = true;
+        for (int k = 0; ok; ++k) {
+            DecayWork w;
+            if (!(ok = queue_get(&bars->queue, k, abort_flag, w)) || w.seq < 0) break;
+            const DecayPass& ps = passes.p[w.pass];
+            const int n = chunks(w);
+            if (lane == 0) {
+                auto load = [&](int dst, const CUtensorMap* map, uint64_t* full, int t) {
+                    const int row = w.begin + token(w, ps.back, t);
+                    mbar_arrive_expect_tx(full, C::TILE);
+                    for (int c = 0; c < C::NCH; ++c) tma_load_3d(smem + dst + c * C::CHUNK, map, full, 64 * c, w.head, row);
+                };
+                auto load_ac = [&](const CUtensorMap* map, int t) {
+                    load(ac_slot(nac), map, &bars->ac_full[nac % C::NAC], t);
+                    ++nac;
+                };
+                for (int t = 0; t < n; ++t) {
+                    const int step = s0 + t;
+                    if (step >= C::NB && !(ok = u_wait(step - C::NB))) break;
+                    load(b_slot(step), &ps.b, &bars->b_full[step % C::NB], t);
+                    ++nb;
+                    load_ac(&ps.a, t);
+                    if (D == 128 && step > 0 && !(ok = mbar_wait(&bars->o_full, (step - 1) & 1, abort_flag))) break;
+                    load_ac(&ps.c, t);
+                }
             }
-            if (!ok) fail();
-            if (*abort_flag) {
-                for (int i = max(0, nb - C::NB); i < nb; ++i) wait_noabort(&bars->b_full[i % C::NB], (i / C::NB) & 1);
-                for (int i = max(0, nac - C::NAC); i < nac; ++i) wait_noabort(&bars->ac_full[i % C::NAC], (i / C::NAC) & 1);
-            }
+            __syncwarp();
+            ok = __all_sync(0xffffffffu, ok);
+            s0 += n;
+        }
+        if (!ok) fail();
+        if (lane == 0 && *abort_flag) {
+            // drain: every load must land before the CTA's shared memory is given up
+            for (int i = max(0, nb - C::NB); i < nb; ++i) wait_noabort(&bars->b_full[i % C::NB], (i / C::NB) & 1);
+            for (int i = max(0, nac - C::NAC); i < nac; ++i) wait_noabort(&bars->ac_full[i % C::NAC], (i / C::NAC) & 1);
         }
       } else if (warp == 21) {
-        if (elect_one()) {
-            // ----------------------------------------------------------- MMAs
-            constexpr uint32_t id_s = idesc_bf16_f32(128, 128, false, false);
-            constexpr uint32_t id_o = idesc_bf16_f32(128, D, false, true);
-            constexpr uint32_t id_x = idesc_bf16_f32(128, D, true, true);
-            const uint32_t lo = smem_u32(sLo), xs = smem_u32(sX);
-            auto issue_s = [&](int t) {
-                tc_fence_after();
-                const uint32_t b = smem_u32(b_slot(t)), a = smem_u32(ac_slot(2 * t));
+        // --------------------------------------------------------------- MMAs
+        // (the whole warp walks the loop, so that every branch and value is
+        // uniform; one elected lane issues)
+        constexpr uint32_t id_s = idesc_bf16_f32(128, 128, false, false);
+        constexpr uint32_t id_o = idesc_bf16_f32(128, D, false, true);
+        constexpr uint32_t id_x = idesc_bf16_f32(128, D, true, true);
+        const uint32_t base = smem_u32(smem);
+        const uint64_t k_major = smem_desc_sw128(base, 16, 1024), mn_major = smem_desc_sw128(base, C::CHUNK, 1024);
+        auto all = [](bool x) { return __all_sync(0xffffffffu, x) != 0; };
+        auto issue_s = [&](int t) {
+            const uint64_t b = desc_add(k_major, b_slot(t)), a = desc_add(k_major, ac_slot(2 * t));
+            tc_fence_after();
+            if (elect_one()) {
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                     const uint32_t o = (kk >> 2) * C::CHUNK + (kk & 3) * 32;
-                    mma_bf16_ss(tbase + C::S_COL, smem_desc_sw128(a + o, 16, 1024), smem_desc_sw128(b + o, 16, 1024), id_s, kk > 0);
+                    mma_bf16_ss(tbase + C::S_COL, desc_add(a, o), desc_add(b, o), id_s, kk > 0);
                 }
                 mma_commit(&bars->s_full);
-            };
-            bool ok = b_wait(0) && ac_wait(0);
-            if (ok) issue_s(0);
+            }
+            __syncwarp();
+        };
+        int s0 = 0, w0 = 0;
+        bool ok = true;
+        for (int k = 0; ok; ++k) {
+            DecayWork w;
+            if (!(ok = queue_get(&bars->queue, k, abort_flag, w)) || w.seq < 0) break;
+            const int n = warp_uniform(chunks(w)), updates = warp_uniform(updates_of(w));
+            if (n == 0) continue;
+            if (!(ok = all(b_wait(s0) && ac_wait(2 * s0)))) break;
+            issue_s(s0);
             for (int t = 0; t < n && ok; ++t) {
-                const uint32_t b = smem_u32(b_slot(t)), a = smem_u32(ac_slot(2 * t)), c = smem_u32(ac_slot(2 * t + 1));
+                const int step = s0 + t;
+                const uint64_t a = desc_add(k_major, ac_slot(2 * step)), c = desc_add(mn_major, ac_slot(2 * step + 1));
                 // O1 = P C
-                if (!(ok = (t == 0 || mma_wait(&bars->o_free, (t - 1) & 1, abort_flag)) && ac_wait(2 * t + 1) &&
-                           mma_wait(&bars->p_ready, t & 1, abort_flag)))
+                if (!(ok = all((step == 0 || mma_wait(&bars->o_free, (step - 1) & 1, abort_flag)) && ac_wait(2 * step + 1) &&
+                               mma_wait(&bars->p_ready, step & 1, abort_flag))))
                     break;
                 tc_fence_after();
+                if (elect_one()) {
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk)           // P: 64 tokens in 32 columns, each half where its scores were
-                    mma_bf16_ts(tbase + C::O1_COL, tbase + C::S_COL + (kk >> 2) * 64 + (kk & 3) * 8,
-                                smem_desc_sw128(c + kk * 2048, C::CHUNK, 1024), id_o, kk > 0);
-                // O2 = A X
-                if (!(ok = mma_wait(&bars->x_ready, t & 1, abort_flag))) break;
-                tc_fence_after();
-#pragma unroll
-                for (int kk = 0; kk < 8; ++kk) {         // d = 64: the features twice, over hi and lo rows
-                    const int f = kk % (D / 16);
-                    mma_bf16_ss(tbase + C::O2_COL, smem_desc_sw128(a + (f >> 2) * C::CHUNK + (f & 3) * 32, 16, 1024),
-                                smem_desc_sw128(xs + kk * 2048, C::CHUNK, 1024), id_o, kk > 0);
+                    for (int kk = 0; kk < 8; ++kk)       // P: 64 tokens in 32 columns, each half where its scores were
+                        mma_bf16_ts(tbase + C::O1_COL, tbase + C::S_COL + (kk >> 2) * 64 + (kk & 3) * 8, desc_add(c, kk * 2048), id_o, kk > 0);
                 }
-                mma_commit(&bars->o_full);
-                // the scores of step t + 1 and U of step t, as their inputs arrive
+                __syncwarp();
+                // O2 = A X
+                if (!(ok = all(mma_wait(&bars->x_ready, step & 1, abort_flag)))) break;
+                tc_fence_after();
+                if (elect_one()) {
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk) {     // d = 64: the features twice, over hi and lo rows
+                        const int f = kk % (D / 16);
+                        mma_bf16_ss(tbase + C::O2_COL, desc_add(a, (f >> 2) * C::CHUNK + (f & 3) * 32),
+                                    desc_add(mn_major, C::X_OFF + kk * 2048), id_o, kk > 0);
+                    }
+                    mma_commit(&bars->o_full);
+                    if (t >= updates) mma_commit(&bars->u_done[step % C::NB]);
+                }
+                __syncwarp();
+                // the scores of the next step and U of this one, as their inputs arrive
                 bool s_next = t + 1 < n, u_next = t < updates;
                 const unsigned long long t0 = clock64();
                 while (s_next || u_next) {
-                    if (s_next && mbar_test_wait(&bars->b_full[(t + 1) % C::NB], ((t + 1) / C::NB) & 1) &&
-                               mbar_test_wait(&bars->ac_full[(2 * t + 2) % C::NAC], ((2 * t + 2) / C::NAC) & 1)) {
-                        issue_s(t + 1);
+                    if (s_next && all(mbar_test_wait(&bars->b_full[(step + 1) % C::NB], ((step + 1) / C::NB) & 1) &&
+                                      mbar_test_wait(&bars->ac_full[(2 * step + 2) % C::NAC], ((2 * step + 2) / C::NAC) & 1))) {
+                        issue_s(step + 1);
                         s_next = false;
-                    } else if (u_next && mbar_test_wait(&bars->w_ready, t & 1)) {
-                        tc_fence_after();
+                    } else if (u_next && all(mbar_test_wait(&bars->w_ready, (w0 + t) & 1))) {
                         // U = (B w)^T C
+                        const uint64_t lo = desc_add(mn_major, C::LO_OFF);
+                        // d = 64: hi and lo are the two 64-feature chunks of one operand
+                        const uint64_t b = D == 128 ? desc_add(mn_major, b_slot(step))
+                                                    : smem_desc_sw128(base + b_slot(step), C::LO_OFF - b_slot(step), 1024);
+                        tc_fence_after();
+                        if (elect_one()) {
 #pragma unroll
-                        for (int kk = 0; kk < 8; ++kk) {
-                            const uint64_t cd = smem_desc_sw128(c + kk * 2048, C::CHUNK, 1024);
-                            if (D == 128) {
-                                mma_bf16_ss(tbase + C::U_COL, smem_desc_sw128(b + kk * 2048, C::CHUNK, 1024), cd, id_x, kk > 0);
-                                mma_bf16_ss(tbase + C::U_COL, smem_desc_sw128(lo + kk * 2048, C::CHUNK, 1024), cd, id_x, 1);
-                            } else {
-                                mma_bf16_ss(tbase + C::U_COL, smem_desc_sw128(b + kk * 2048, lo - b, 1024), cd, id_x, kk > 0);
+                            for (int kk = 0; kk < 8; ++kk) {
+                                const uint64_t cd = desc_add(c, kk * 2048);
+                                mma_bf16_ss(tbase + C::U_COL, desc_add(b, kk * 2048), cd, id_x, kk > 0);
+                                if (D == 128) mma_bf16_ss(tbase + C::U_COL, desc_add(lo, kk * 2048), cd, id_x, 1);
                             }
+                            mma_commit(&bars->u_done[step % C::NB]);
                         }
-                        mma_commit(&bars->u_done[t % C::NB]);
+                        __syncwarp();
                         u_next = false;
-                    } else if (*abort_flag || clock64() - t0 > VSA_WAIT_LIMIT_CYCLES) {
+                    } else if (!all(!*abort_flag && clock64() - t0 <= VSA_WAIT_LIMIT_CYCLES)) {
                         ok = false;
                         break;
                     }
                 }
             }
-            if (!ok) fail();
-            mma_commit(&bars->mma_done);
-            wait_noabort(&bars->mma_done, 0);
+            s0 += n;
+            w0 += updates;
         }
+        if (!ok) fail();
+        if (elect_one()) mma_commit(&bars->mma_done);
+        __syncwarp();
+        wait_noabort(&bars->mma_done, 0);
       }
     } else if (warp < 8) {
         reg_dec<C::REG_SCORE>();
@@ -575,100 +618,119 @@ decay_out_kernel(const __grid_constant__ DecayPasses passes, const int n_passes,
         // lam^|i-j| is lam^(to the near end of j's block of 32) times
         // lam^(within the block), both factors at most 1; in the diagonal block
         // it is a table's entry at j - i, 0 on the masked side.
+        int s0 = 0;
         bool ok = true;
-        for (int t = 0; t < n; ++t) {
-            const int rows = min(128, g.len - 128 * chunk_of(t));
-            if (rows < 128) {
-                // C's rows behind the sequence are another one's: zeros
-                if (!__all_sync(0xffffffffu, ac_wait(2 * t + 1))) { ok = false; break; }
-                uint8_t* c = ac_slot(2 * t + 1);
-                for (int u = tid; u < (128 - rows) * 8 * C::NCH; u += 256)
-                    *reinterpret_cast<uint4*>(c + (u % C::NCH) * C::CHUNK + rows * 128 + (u / C::NCH) * 16) = make_uint4(0, 0, 0, 0);
-                fence_proxy_async_smem();
+        for (int k = 0; ok; ++k) {
+            DecayWork w;
+            if (!(ok = queue_get(&bars->queue, k, abort_flag, w)) || w.seq < 0) break;
+            const DecayPass& ps = passes.p[w.pass];
+            const bool back = ps.back;
+            const float l2 = decay_log2(log_decay, w.head);
+            // forward lam^31 .. lam^0 and zeros, backwards zeros and lam^0 .. lam^31
+            float* sPow = reinterpret_cast<float*>(smem + C::POW_OFF) + (k & 1) * C::POW_FLOATS;
+            if (tid < 64) {
+                const float y = (back ? tid >= 32 : tid < 32) ? ex2((float)(back ? tid - 32 : 31 - tid) * l2) : 0.f;
+                sPow[tid] = y;
+                sPow[64 + 1 + tid] = y;                  // for pairs that start at an odd place
+                mbar_arrive(&bars->pow_ready);
             }
-            if (!__all_sync(0xffffffffu, mbar_wait(&bars->s_full, t & 1, abort_flag))) { ok = false; break; }
-            tc_fence_after();
-            // P over the scores, 32 columns at a time (a loop: the kernel's
-            // roles have to share the instruction cache)
-#pragma unroll 1
-            for (int h = 0; h < 2; ++h) {
-                const int blk = 2 * hf + h;
-                uint32_t pk[16];
-                if (back ? blk >= quarter : blk <= quarter) {
-                    const int far = blk == quarter ? 0 : back ? 32 * blk - r : r - 32 * blk - 31;
-                    const int at = blk == quarter ? (back ? 32 : 31) - lane : back ? 32 : 0;
-                    const uint64_t* y = reinterpret_cast<const uint64_t*>(sPow + (at & 1 ? 64 + 1 + at : at));
-                    const float f = ps.p_scale * ex2((float)far * l2);
-                    float s[32];
-                    tmem_ld_32x32b_x32(tS + 32 * h, s);
-                    tmem_wait_ld();
-                    const uint64_t f2 = f32x2(f, f);
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2)
-                        unf32x2(mul_f32x2(f32x2(s[e], s[e + 1]), mul_f32x2(f2, y[e / 2])), s[e], s[e + 1]);
-                    if (rows < 128) {                    // scores of rows behind the sequence may be anything
-                        const int lo = back && blk == quarter ? lane : 0;
-                        const int hi = min(rows - 32 * blk, !back && blk == quarter ? lane + 1 : 32);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) s[e] = e >= lo && e < hi ? s[e] : 0.f;
-                    }
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) pk[e] = pack_bf16x2(s[2 * e], s[2 * e + 1]);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) pk[e] = 0;
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bars->pow_ready, k & 1, abort_flag)))) break;
+            const int n = chunks(w), updates = updates_of(w);
+            for (int t = 0; t < n; ++t) {
+                const int step = s0 + t, rows = min(128, w.len - token(w, back, t));
+                if (rows < 128) {
+                    // C's rows behind the sequence are another one's: zeros
+                    if (!__all_sync(0xffffffffu, ac_wait(2 * step + 1))) { ok = false; break; }
+                    uint8_t* c = smem + ac_slot(2 * step + 1);
+                    for (int u = tid; u < (128 - rows) * 8 * C::NCH; u += 256)
+                        *reinterpret_cast<uint4*>(c + (u % C::NCH) * C::CHUNK + rows * 128 + (u / C::NCH) * 16) = make_uint4(0, 0, 0, 0);
+                    fence_proxy_async_smem();
                 }
-                tmem_st_32x32b_x16(tS + 16 * h, pk);     // (over scores of this thread's that are read or masked)
+                if (!__all_sync(0xffffffffu, mbar_wait(&bars->s_full, step & 1, abort_flag))) { ok = false; break; }
+                tc_fence_after();
+                // P over the scores, 32 columns at a time (a loop: the kernel's
+                // roles have to share the instruction cache)
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {
+                    const int blk = 2 * hf + h;
+                    uint32_t pk[16];
+                    if (back ? blk >= quarter : blk <= quarter) {
+                        const int far = blk == quarter ? 0 : back ? 32 * blk - r : r - 32 * blk - 31;
+                        const int at = blk == quarter ? (back ? 32 : 31) - lane : back ? 32 : 0;
+                        const uint64_t* y = reinterpret_cast<const uint64_t*>(sPow + (at & 1 ? 64 + 1 + at : at));
+                        const float f = ps.p_scale * ex2((float)far * l2);
+                        float s[32];
+                        tmem_ld_32x32b_x32(tS + 32 * h, s);
+                        tmem_wait_ld();
+                        const uint64_t f2 = f32x2(f, f);
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2)
+                            unf32x2(mul_f32x2(f32x2(s[e], s[e + 1]), mul_f32x2(f2, y[e / 2])), s[e], s[e + 1]);
+                        if (rows < 128) {                // scores of rows behind the sequence may be anything
+                            const int lo = back && blk == quarter ? lane : 0;
+                            const int hi = min(rows - 32 * blk, !back && blk == quarter ? lane + 1 : 32);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) s[e] = e >= lo && e < hi ? s[e] : 0.f;
+                        }
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) pk[e] = pack_bf16x2(s[2 * e], s[2 * e + 1]);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) pk[e] = 0;
+                    }
+                    tmem_st_32x32b_x16(tS + 16 * h, pk); // (over scores of this thread's that are read or masked)
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(&bars->p_ready);
+                if (t < updates) {
+                    // the products that read the last step's lo part have finished
+                    if (step > 0 && !__all_sync(0xffffffffu, u_wait(step - 1))) { ok = false; break; }
+                    if (!split_units(step, tid, 0, C::UNITS_P, rows, back, ps.w_scale, l2)) { ok = false; break; }
+                }
             }
-            tmem_wait_st();
-            tc_fence_before();
-            mbar_arrive(&bars->p_ready);
-            if (t < updates) {
-                // the products that read the last step's lo part have finished
-                if (t > 0 && !__all_sync(0xffffffffu, u_wait(t - 1))) { ok = false; break; }
-                if (!split_units(t, tid, 0, C::UNITS_P, rows)) { ok = false; break; }
-            }
+            s0 += n;
         }
         if (!ok) fail();
     } else if (warp >= 16) {
         // -------------------------------------------------------- the outputs
         const int quarter = warp & 3, r = 32 * quarter + lane;
         const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
-        const float f_full = ps.s_scale * ex2((float)(back ? 127 - r : r + 1) * l2);
+        int s0 = 0;
         bool ok = true;
-        for (int t = 0; t < n; ++t) {
-            const int tok = 128 * chunk_of(t), rows = min(128, g.len - tok);
-            const float f = back && rows < 128 ? ps.s_scale * ex2((float)(rows - 1 - r) * l2) : f_full;
-            // lane l stores units l & 3 of the rows of its four lanes
-            __nv_bfloat16* po = ps.out + (long long)(g.begin + tok + (r & ~3)) * ps.out_stride + (long long)head * D + (lane & 3) * 8;
-            if (!__all_sync(0xffffffffu, mbar_wait(&bars->o_full, t & 1, abort_flag))) { ok = false; break; }
-            tc_fence_after();
+        for (int k = 0; ok; ++k) {
+            DecayWork w;
+            if (!(ok = queue_get(&bars->queue, k, abort_flag, w)) || w.seq < 0) break;
+            const DecayPass& ps = passes.p[w.pass];
+            const bool back = ps.back;
+            const float l2 = decay_log2(log_decay, w.head), f_full = ps.s_scale * ex2((float)(back ? 127 - r : r + 1) * l2);
+            const int n = chunks(w);
+            for (int t = 0; t < n; ++t) {
+                const int tok = token(w, back, t), rows = min(128, w.len - tok);
+                const float f = back && rows < 128 ? ps.s_scale * ex2((float)(rows - 1 - r) * l2) : f_full;
+                const QuadRows at(r < rows ? (long long)(w.begin + tok + r) * ps.out_stride + (long long)w.head * D : -1);
+                if (!__all_sync(0xffffffffu, mbar_wait(&bars->o_full, (s0 + t) & 1, abort_flag))) { ok = false; break; }
+                tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-                float o[32];
-                uint4 u[4];
-                {
-                    float x[32];
-                    tmem_ld_32x32b_x32(tbase + lanes + C::O1_COL + c, o);
-                    tmem_ld_32x32b_x32(tbase + lanes + C::O2_COL + c, x);
-                    tmem_wait_ld();
-                    const uint64_t f2 = f32x2(f, f);
+                for (int c = 0; c < D; c += 32) {
+                    float o[32];
+                    {
+                        float x[32];
+                        tmem_ld_32x32b_x32(tbase + lanes + C::O1_COL + c, o);
+                        tmem_ld_32x32b_x32(tbase + lanes + C::O2_COL + c, x);
+                        tmem_wait_ld();
+                        const uint64_t f2 = f32x2(f, f);
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) unf32x2(fma_f32x2(f2, f32x2(x[e], x[e + 1]), f32x2(o[e], o[e + 1])), o[e], o[e + 1]);
+                        for (int e = 0; e < 32; e += 2) unf32x2(fma_f32x2(f2, f32x2(x[e], x[e + 1]), f32x2(o[e], o[e + 1])), o[e], o[e + 1]);
+                    }
+                    if (c + 32 == D) {
+                        tc_fence_before();
+                        mbar_arrive(&bars->o_free);
+                    }
+                    store_rows(ps.out + c, at, o);
                 }
-                if (c + 32 == D) {
-                    tc_fence_before();
-                    mbar_arrive(&bars->o_free);
-                }
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    u[e] = make_uint4(pack_bf16x2(o[8 * e], o[8 * e + 1]), pack_bf16x2(o[8 * e + 2], o[8 * e + 3]),
-                                      pack_bf16x2(o[8 * e + 4], o[8 * e + 5]), pack_bf16x2(o[8 * e + 6], o[8 * e + 7]));
-                transpose_units(u, lane);
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if ((r & ~3) + e < rows) *reinterpret_cast<uint4*>(po + e * ps.out_stride + c) = u[e];
             }
+            s0 += n;
         }
         if (!ok) fail();
     } else {
@@ -677,84 +739,116 @@ decay_out_kernel(const __grid_constant__ DecayPasses passes, const int n_passes,
         // in registers: a row (TMEM lane) and half of its columns
         const int id = tid - 256, hf = id >> 7, row = id & 127, feat = row & (D - 1);
         const uint32_t tU = tbase + ((uint32_t)(32 * (warp & 3)) << 16) + C::U_COL + hf * (D / 2);
+        int s0 = 0, written = 0;                         // states written so far (d = 64: phases of the lo part's exchange)
         bool ok = true;
-        float x[D / 2];
-        if (x0 && row < D) {
-#pragma unroll
-            for (int c = 0; c < D / 2; c += 4) {
-                const int col = hf * (D / 2) + c;
-                if (ps.trans) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) x[c + e] = __ldg(x0 + (long long)(col + e) * D + feat);
-                } else {
-                    const float4 y = __ldg(reinterpret_cast<const float4*>(x0 + (long long)feat * D + col));
-                    x[c] = y.x; x[c + 1] = y.y; x[c + 2] = y.z; x[c + 3] = y.w;
-                }
+        for (int k = 0; ok; ++k) {
+            DecayWork w;
+            if (!(ok = queue_get(&bars->queue, k, abort_flag, w)) || w.seq < 0) break;
+            const DecayPass& ps = passes.p[w.pass];
+            const bool back = ps.back;
+            const float l2 = decay_log2(log_decay, w.head);
+            const int n = chunks(w), updates = updates_of(w);
+            const long long own = ((long long)w.seq * sh.heads + w.head) * D * D;
+            float* last = writes_state(w) ? ps.last + own : nullptr;
+            const float* x0;                             // the state before step 0, or null: zeros
+            if (back ? w.rest <= sh.seg : w.off == 0) x0 = ps.first ? ps.first + own : nullptr;
+            else x0 = ps.border + ((long long)((back ? w.begin + sh.seg : w.begin) - sh.part) / sh.part * sh.heads + w.head) * D * D;
+            if (n == 0) {                                // an empty sequence: the state goes through
+                if (last)
+                    for (int e = id; e < D * D; e += 256) last[e] = x0 ? x0[e] : 0.f;
+                continue;
             }
-        } else {
+            float x[D / 2];
 #pragma unroll
             for (int c = 0; c < D / 2; ++c) x[c] = 0.f;
-        }
-        // X = lam^tokens X + U, once the products of step t have finished
-        auto update = [&](int t) {
-            if (!__all_sync(0xffffffffu, u_wait(t))) return false;
-            tc_fence_after();
-            const float f = ex2((float)min(128, g.len - 128 * chunk_of(t)) * l2);
+            if (x0 && row < D) {                         // (whole warps)
+                if (ps.trans) {
 #pragma unroll
-            for (int c = 0; c < D / 2; c += 32) {
-                float u[32];
-                tmem_ld_32x32b_x32(tU + c, u);
-                tmem_wait_ld();
+                    for (int c = 0; c < D / 2; ++c) x[c] = __ldg(x0 + (long long)(hf * (D / 2) + c) * D + feat);
+                } else {
 #pragma unroll
-                for (int e = 0; e < 32; ++e) x[c + e] = fmaf(f, x[c + e], u[e]);
-            }
-            tc_fence_before();
-            return true;
-        };
-        for (int t = 0; t < n; ++t) {
-            const int tok = 128 * chunk_of(t), rows = min(128, g.len - tok);
-            if (t > 0 && !update(t - 1)) { ok = false; break; }
-            uint8_t* xr = sX + row * 128;
+                    for (int c = 0; c < D / 2; c += 16) {
+                        uint4 u[4];
 #pragma unroll
-            for (int c = 0; c < D / 2; c += 8) {
-                const int col = hf * (D / 2) + c;
-                *reinterpret_cast<uint4*>(xr + (col >> 6) * C::CHUNK + ((((col & 63) >> 3) ^ (row & 7)) << 4)) =
-                    make_uint4(pack_bf16x2(x[c], x[c + 1]), pack_bf16x2(x[c + 2], x[c + 3]), pack_bf16x2(x[c + 4], x[c + 5]),
-                               pack_bf16x2(x[c + 6], x[c + 7]));
-            }
-            // (before x_ready: step t + 1's scores wait for that, so this phase cannot be missed)
-            if (!__all_sync(0xffffffffu, mbar_wait(&bars->s_full, t & 1, abort_flag))) { ok = false; break; }
-            fence_proxy_async_smem();
-            mbar_arrive(&bars->x_ready);
-            if (t < updates && !split_units(t, id, C::UNITS_P, C::UNITS, rows)) { ok = false; break; }
-        }
-        if (last) {
-            if (ok && !update(n - 1)) ok = false;
-            if (D == 64) {
-                // the last products have finished: the bf16 state's place holds the lo part for the hi part's threads
-                float* half = reinterpret_cast<float*>(sX) + hf * 32 * 64 + feat;
-                if (ok && row >= 64) {
+                        for (int e = 0; e < 4; ++e)
+                            u[e] = __ldg(reinterpret_cast<const uint4*>(x0 + (long long)((feat & ~3) + e) * D + hf * (D / 2) + c + (lane & 3) * 4));
+                        transpose_units(u, lane);
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) half[c * 64] = x[c];
-                }
-                asm volatile("bar.sync 1, 256;" ::: "memory");
-                if (ok && row < 64) {
-#pragma unroll
-                    for (int c = 0; c < 32; ++c) x[c] += half[c * 64];
-                }
-            }
-            if (ok && row < D) {
-#pragma unroll
-                for (int c = 0; c < D / 2; c += 4) {
-                    const int col = hf * (D / 2) + c;
-                    if (ps.trans) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) last[(long long)(col + e) * D + feat] = x[c + e];
-                    } else {
-                        *reinterpret_cast<float4*>(last + (long long)feat * D + col) = make_float4(x[c], x[c + 1], x[c + 2], x[c + 3]);
+                        for (int e = 0; e < 4; ++e) {
+                            x[c + 4 * e] = __uint_as_float(u[e].x); x[c + 4 * e + 1] = __uint_as_float(u[e].y);
+                            x[c + 4 * e + 2] = __uint_as_float(u[e].z); x[c + 4 * e + 3] = __uint_as_float(u[e].w);
+                        }
                     }
                 }
             }
+            // X = lam^tokens X + U, once the products of step t have finished
+            auto update = [&](int t) {
+                if (!__all_sync(0xffffffffu, u_wait(s0 + t))) return false;
+                tc_fence_after();
+                const float f = ex2((float)min(128, w.len - token(w, back, t)) * l2);
+#pragma unroll
+                for (int c = 0; c < D / 2; c += 32) {
+                    float u[32];
+                    tmem_ld_32x32b_x32(tU + c, u);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) x[c + e] = fmaf(f, x[c + e], u[e]);
+                }
+                tc_fence_before();
+                return true;
+            };
+            for (int t = 0; t < n; ++t) {
+                const int step = s0 + t, rows = min(128, w.len - token(w, back, t));
+                if (t > 0) {
+                    if (!update(t - 1)) { ok = false; break; }
+                } else {
+                    // the walk before has left the bf16 state's place
+                    if (step > 0 && !__all_sync(0xffffffffu, u_wait(step - 1))) { ok = false; break; }
+                    if (D == 64 && written > 0 && !__all_sync(0xffffffffu, mbar_wait(&bars->lo_free, (written - 1) & 1, abort_flag))) { ok = false; break; }
+                }
+                uint8_t* xr = sX + row * 128;
+#pragma unroll
+                for (int c = 0; c < D / 2; c += 8) {
+                    const int col = hf * (D / 2) + c;
+                    *reinterpret_cast<uint4*>(xr + (col >> 6) * C::CHUNK + ((((col & 63) >> 3) ^ (row & 7)) << 4)) =
+                        make_uint4(pack_bf16x2(x[c], x[c + 1]), pack_bf16x2(x[c + 2], x[c + 3]), pack_bf16x2(x[c + 4], x[c + 5]),
+                                   pack_bf16x2(x[c + 6], x[c + 7]));
+                }
+                // (before x_ready: the next step's scores wait for that, so this phase cannot be missed)
+                if (!__all_sync(0xffffffffu, mbar_wait(&bars->s_full, step & 1, abort_flag))) { ok = false; break; }
+                fence_proxy_async_smem();
+                mbar_arrive(&bars->x_ready);
+                if (t < updates && !split_units(step, id, C::UNITS_P, C::UNITS, rows, back, ps.w_scale, l2)) { ok = false; break; }
+            }
+            if (ok && last) {
+                if (!(ok = update(n - 1))) break;
+                if (D == 64) {
+                    // the walk's products have finished: the bf16 state's place takes the lo part to the hi part's threads
+                    float* half = reinterpret_cast<float*>(sX) + hf * 32 * 64 + feat;
+                    if (row >= 64) {
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) half[c * 64] = x[c];
+                        mbar_arrive(&bars->lo_ready);
+                    } else {
+                        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bars->lo_ready, written & 1, abort_flag)))) break;
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) x[c] += half[c * 64];
+                        mbar_arrive(&bars->lo_free);
+                    }
+                    ++written;
+                }
+                if (row < D) {
+                    if (ps.trans) {
+#pragma unroll
+                        for (int c = 0; c < D / 2; ++c) last[(long long)(hf * (D / 2) + c) * D + feat] = x[c];
+                    } else {
+                        const QuadRows at((long long)feat * D + hf * (D / 2));
+#pragma unroll
+                        for (int c = 0; c < D / 2; c += 32) store_rows(last + c, at, *reinterpret_cast<float(*)[32]>(&x[c]));
+                    }
+                }
+            }
+            s0 += n;
         }
         if (!ok) fail();
     }

@@ -142,12 +142,13 @@ __device__ __forceinline__ void store_rows(float* p, const QuadRows& rows, const
 }
 
 // A CTA's queue of work: one warp finds what the CTA is to do and hands it to
-// the other warps, two pieces ahead at most.  Where a CTA has an SM to itself
-// it then takes over CTAs that have not started yet from the grid (cluster
-// launch control): the latency of its start and end overlaps with the pieces
-// around it, and the hardware's own queue still balances long and short ones.
-// (Two CTAs on an SM hide each other's.)  W is a plain struct with an int
-// `seq`, -1 for the end.
+// the other warps.  Where a CTA has an SM to itself it then takes over CTAs that
+// have not started yet from the grid (cluster launch control): the latency of
+// its start and end overlaps with the pieces around it, and the hardware's own
+// queue still balances long and short ones (the next piece is asked for when
+// every warp has begun the last: one asked for earlier would wait here while
+// another SM runs dry).  Two CTAs on an SM hide each other's latency instead.
+// W is a plain struct with an int `seq`, -1 for the end.
 template <typename W>
 struct WorkQueue {
     uint4 answer;
@@ -166,37 +167,39 @@ __device__ __forceinline__ void queue_init(WorkQueue<W>* q, int consumer_warps) 
 template <bool TAKE_OVER, typename W, typename F>
 __device__ __forceinline__ bool queue_produce(WorkQueue<W>* q, const volatile int* abort, F make) {
     const int lane = threadIdx.x & 31;
-    int id = blockIdx.x, k = 0;
-    auto put = [&](const W& w) {
-        if (k >= 2 && !__all_sync(0xffffffffu, sm100::mbar_wait(&q->empty[k & 1], (k / 2 - 1) & 1, abort))) return false;
+    int k = 0;
+    auto put = [&](const W& w) {                         // slot k & 1 is free: the piece before the last has been begun
         if (lane == 0) {
             q->slot[k & 1] = w;
             sm100::mbar_arrive(&q->full[k & 1]);
         }
         __syncwarp();
         ++k;
-        return true;
     };
-    bool ok = true;
-    for (int asked = 0; id >= 0 && ok; ++asked) {
-        if (TAKE_OVER && lane == 0) {
+    auto begun = [&]() { return __all_sync(0xffffffffu, sm100::mbar_wait(&q->empty[(k - 1) & 1], ((k - 1) / 2) & 1, abort)) != 0; };
+    int id = blockIdx.x;
+    for (int asked = 0; id >= 0; ++asked) {
+        const W w = make(id);
+        if (w.seq >= 0) {
+            put(w);
+            if (!begun()) return false;
+        }
+        if (!TAKE_OVER) break;
+        if (lane == 0) {
             sm100::mbar_arrive_expect_tx(&q->asked, 16);
             sm100::try_cancel(&q->answer, &q->asked);
         }
         __syncwarp();
-        const W w = make(id);
-        if (w.seq >= 0) ok = put(w);
-        if (!TAKE_OVER) break;
-        // an answer on its way has to arrive before the CTA leaves
-        const bool here = __all_sync(0xffffffffu, sm100::wait_noabort(&q->asked, asked & 1));
-        if (!here) return false;
+        // (not given up early: the answer has to arrive before the CTA leaves)
+        if (!__all_sync(0xffffffffu, sm100::wait_noabort(&q->asked, asked & 1))) return false;
         id = sm100::cancelled_ctaid(&q->answer);
         __syncwarp();
-        sm100::fence_proxy_async_smem();             // read before the next answer is written
+        sm100::fence_proxy_async_smem();                 // read before the next answer is written
     }
     W end{};
     end.seq = -1;
-    return ok && put(end);
+    put(end);
+    return true;
 }
 
 // Piece k of the queue (whole warp); false: a wait gave up.
