@@ -498,6 +498,7 @@ decay_out_kernel(const __grid_constant__ DecayPasses passes, const int n_passes,
                     if (D == 128 && step > 0 && !(ok = mbar_wait(&bars->o_full, (step - 1) & 1, abort_flag))) break;
                     load_ac(&ps.c, t);
                 }
+                queue_ending(&bars->queue);
             }
             __syncwarp();
             ok = __all_sync(0xffffffffu, ok);

@@ -146,20 +146,29 @@ __device__ __forceinline__ void store_rows(float* p, const QuadRows& rows, const
 // have not started yet from the grid (cluster launch control): the latency of
 // its start and end overlaps with the pieces around it, and the hardware's own
 // queue still balances long and short ones (the next piece is asked for when
-// every warp has begun the last: one asked for earlier would wait here while
-// another SM runs dry).  Two CTAs on an SM hide each other's latency instead.
+// the last loads of this one are on their way: one asked for earlier would wait
+// here while another SM runs dry).  Two CTAs on an SM hide each other's latency
+// instead.
 // W is a plain struct with an int `seq`, -1 for the end.
 template <typename W>
 struct WorkQueue {
     uint4 answer;
     W slot[2];
-    uint64_t full[2], empty[2], asked;
+    uint64_t full[2], empty[2], asked, ending;
 };
 
 template <typename W>
 __device__ __forceinline__ void queue_init(WorkQueue<W>* q, int consumer_warps) {
     for (int x = 0; x < 2; ++x) { sm100::mbar_init(&q->full[x], 1); sm100::mbar_init(&q->empty[x], consumer_warps); }
     sm100::mbar_init(&q->asked, 1);
+    sm100::mbar_init(&q->ending, 1);
+}
+
+// By one thread, once for each piece that was not the end: its last loads are
+// on their way.
+template <typename W>
+__device__ __forceinline__ void queue_ending(WorkQueue<W>* q) {
+    sm100::mbar_arrive(&q->ending);
 }
 
 // The producing warp's whole run; make(id) (whole warp) gives the work of CTA
@@ -168,21 +177,22 @@ template <bool TAKE_OVER, typename W, typename F>
 __device__ __forceinline__ bool queue_produce(WorkQueue<W>* q, const volatile int* abort, F make) {
     const int lane = threadIdx.x & 31;
     int k = 0;
-    auto put = [&](const W& w) {                         // slot k & 1 is free: the piece before the last has been begun
+    auto put = [&](const W& w) {
+        if (k >= 2 && !__all_sync(0xffffffffu, sm100::mbar_wait(&q->empty[k & 1], (k / 2 - 1) & 1, abort))) return false;
         if (lane == 0) {
             q->slot[k & 1] = w;
             sm100::mbar_arrive(&q->full[k & 1]);
         }
         __syncwarp();
         ++k;
+        return true;
     };
-    auto begun = [&]() { return __all_sync(0xffffffffu, sm100::mbar_wait(&q->empty[(k - 1) & 1], ((k - 1) / 2) & 1, abort)) != 0; };
     int id = blockIdx.x;
     for (int asked = 0; id >= 0; ++asked) {
         const W w = make(id);
         if (w.seq >= 0) {
-            put(w);
-            if (!begun()) return false;
+            if (!put(w)) return false;
+            if (TAKE_OVER && !__all_sync(0xffffffffu, sm100::mbar_wait(&q->ending, (k - 1) & 1, abort))) return false;
         }
         if (!TAKE_OVER) break;
         if (lane == 0) {
@@ -198,8 +208,7 @@ __device__ __forceinline__ bool queue_produce(WorkQueue<W>* q, const volatile in
     }
     W end{};
     end.seq = -1;
-    put(end);
-    return true;
+    return put(end);
 }
 
 // Piece k of the queue (whole warp); false: a wait gave up.

@@ -181,7 +181,10 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
             PackWork w;
             if (!(ok = queue_get(&bars->queue, k, abort_flag, w)) || w.seq < 0) break;
             const int n = w.hi - w.lo;
-            if (n == 0) continue;
+            if (n == 0) {
+                if (lane == 0) queue_ending(&bars->queue);
+                continue;
+            }
             // Q's place is free once the last scores of the work before are finished
             if (works > 0 && !(ok = __all_sync(0xffffffffu, mbar_wait(&bars->q_empty, (works - 1) & 1, abort_flag)))) break;
             ++works;
@@ -202,6 +205,7 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
                                     w.k0 + 128 * (w.hi - 1 - (i >> 1)));
                     ++issued;
                 }
+                queue_ending(&bars->queue);
             }
             __syncwarp();
             ok = __all_sync(0xffffffffu, ok);
