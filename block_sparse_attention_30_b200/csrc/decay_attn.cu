@@ -123,17 +123,24 @@ struct DecStateCfg {
     static constexpr int NCH = D / 64;
     static constexpr int CHUNK = 64 * 128;               // 64 tokens of one 64-feature chunk
     static constexpr int TILE = NCH * CHUNK;
-    static constexpr int STAGE = 3 * TILE;               // b (hi in its place), c, lo
-    static constexpr int NST = D == 128 ? 2 : 4;         // (two CTAs per SM)
-    static constexpr int BAR_OFF = NST * STAGE;
+    static constexpr int NST = D == 128 ? 6 : 8;         // stages of b (hi in its place) and c
+    static constexpr int LO_OFF = NST * 2 * TILE;        // lo of even and odd steps
+    static constexpr int BAR_OFF = LO_OFF + 2 * TILE;
     static constexpr int SMEM = BAR_OFF + 512;
-    static constexpr int THREADS = 288;                  // 8 transform warps, loads and MMAs
+    static constexpr int THREADS = 512;                  // 8 split warps, 4 output warps, loads, MMAs, queue
+};
+static_assert(DecStateCfg<128>::SMEM <= 232448, "shared memory");
+
+struct DecayPart {
+    int seq, head, kind;
+    int begin, len;
 };
 
 template <int D>
 struct DecStateBars {
-    uint64_t full[DecStateCfg<D>::NST], ready[DecStateCfg<D>::NST], done[DecStateCfg<D>::NST];
-    uint64_t mma_done;
+    WorkQueue<DecayPart> queue;
+    uint64_t full[DecStateCfg<D>::NST], done[DecStateCfg<D>::NST];
+    uint64_t ready, sum_full[2], sum_free[2], half_full, half_free;
     uint32_t tmem_base;
     int abort;
 };
@@ -146,13 +153,15 @@ struct DecayStateArgs {
     float w_scale[2];
 };
 
-// grid (parts x heads, kinds of state).  Forward in time the sum of part p
-// goes to the border behind it, backwards that of part p + 1; parts of the
-// walk's last segment reach no border that is needed.
+// grid (kinds of state x parts x heads), from a queue per CTA.  Forward in time
+// the sum of part p goes to the border behind it, backwards that of part p + 1;
+// parts of the walk's last segment reach no border that is needed.  Steps of 64
+// tokens are counted on from part to part; a part's sum lies in one of two TMEM
+// accumulators, so that it is stored while the next part's is formed.
 template <int D>
-__global__ void __launch_bounds__(DecStateCfg<D>::THREADS, 2)
-decay_state_kernel(const __grid_constant__ DecayStateArgs args, const DecayShape sh, const int32_t* __restrict__ cu,
-                   const float* __restrict__ log_decay, int* status) {
+__global__ void __launch_bounds__(DecStateCfg<D>::THREADS, 1)
+decay_state_kernel(const __grid_constant__ DecayStateArgs args, const int kinds, const DecayShape sh,
+                   const int32_t* __restrict__ cu, const float* __restrict__ log_decay, int* status) {
     using C = DecStateCfg<D>;
     extern __shared__ __align__(1024) uint8_t smem[];
     if (smem_u32(smem) & 1023) {
@@ -160,138 +169,194 @@ decay_state_kernel(const __grid_constant__ DecayStateArgs args, const DecayShape
         return;
     }
     const int tid = threadIdx.x, warp = warp_uniform(tid >> 5), lane = tid & 31;
-    const int head = blockIdx.x % sh.heads, kind = blockIdx.y, back = args.back[kind];
-    const Piece g = find_piece(cu, sh, sh.part, blockIdx.x / sh.heads, status);
-    if (g.seq < 0 || (back ? g.off < sh.seg : g.rest <= sh.seg - g.off % sh.seg)) return;
     DecStateBars<D>* bars = reinterpret_cast<DecStateBars<D>*>(smem + C::BAR_OFF);
     volatile int* abort_flag = &bars->abort;
     if (tid == 0) {
         bars->abort = 0;
-        for (int x = 0; x < C::NST; ++x) { mbar_init(&bars->full[x], 1); mbar_init(&bars->ready[x], 256); mbar_init(&bars->done[x], 1); }
-        mbar_init(&bars->mma_done, 1);
+        queue_init(&bars->queue, 14);
+        for (int x = 0; x < C::NST; ++x) { mbar_init(&bars->full[x], 1); mbar_init(&bars->done[x], 1); }
+        mbar_init(&bars->ready, 256);
+        for (int x = 0; x < 2; ++x) { mbar_init(&bars->sum_full[x], 1); mbar_init(&bars->sum_free[x], 128); }
+        mbar_init(&bars->half_full, 64);
+        mbar_init(&bars->half_free, 64);
         fence_barrier_init();
     }
-    if (warp == 8) { tmem_alloc(&bars->tmem_base, 128); tmem_relinquish(); }
+    if (warp == 13) { tmem_alloc(&bars->tmem_base, 256); tmem_relinquish(); }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tbase = warp_uniform(bars->tmem_base);
     auto fail = [&]() { *abort_flag = 1; report(status, kStatusTimeout); };
-    // steps of 64 tokens, against the direction of decay_out_kernel's walk: what
-    // that reads first is what this one read last, and still in L2
-    const int n = warp_uniform((g.len + 63) / 64);
-    auto token_of = [&](int t) { return 64 * (back ? t : n - 1 - t); };
-    if (warp == 8) {
-        if (elect_one()) {
-            constexpr uint32_t id = idesc_bf16_f32(128, D, true, true);
-            int issued = 0;
-            auto load = [&](int t) {
-                uint8_t* st = smem + (t % C::NST) * C::STAGE;
-                uint64_t* bar = &bars->full[t % C::NST];
-                mbar_arrive_expect_tx(bar, 2 * C::TILE);
-                for (int c = 0; c < C::NCH; ++c) {
-                    tma_load_3d(st + c * C::CHUNK, &args.b[kind], bar, 64 * c, head, g.begin + token_of(t));
-                    tma_load_3d(st + C::TILE + c * C::CHUNK, &args.c[kind], bar, 64 * c, head, g.begin + token_of(t));
-                }
-                ++issued;
-            };
-            for (int t = 0; t < min(n, C::NST); ++t) load(t);
-            bool ok = true;
-            for (int t = 0; t < n && ok; ++t) {
-                // the stage of step t - 1 refills while step t's products run
-                if (!(ok = mma_wait(&bars->ready[t % C::NST], (t / C::NST) & 1, abort_flag))) break;
-                tc_fence_after();
-                const uint32_t s0 = smem_u32(smem + (t % C::NST) * C::STAGE);
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk) {         // 16 tokens per MMA
-                    const uint64_t c = smem_desc_sw128(s0 + C::TILE + kk * 2048, C::CHUNK, 1024);
-                    if (D == 128) {
-                        mma_bf16_ss(tbase, smem_desc_sw128(s0 + kk * 2048, C::CHUNK, 1024), c, id, t > 0 || kk > 0);
-                        mma_bf16_ss(tbase, smem_desc_sw128(s0 + 2 * C::TILE + kk * 2048, C::CHUNK, 1024), c, id, 1);
-                    } else {
-                        mma_bf16_ss(tbase, smem_desc_sw128(s0 + kk * 2048, 2 * C::TILE, 1024), c, id, t > 0 || kk > 0);
-                    }
-                }
-                mma_commit(&bars->done[t % C::NST]);
-                if (t >= 1 && t - 1 + C::NST < n) {
-                    if (!(ok = mma_wait(&bars->done[(t - 1) % C::NST], ((t - 1) / C::NST) & 1, abort_flag))) break;
-                    load(t - 1 + C::NST);
-                }
-            }
-            if (!ok) {
-                fail();
-                for (int t = max(0, issued - C::NST); t < issued; ++t) wait_noabort(&bars->full[t % C::NST], (t / C::NST) & 1);
-            }
-            mma_commit(&bars->mma_done);
-            wait_noabort(&bars->mma_done, 0);
-        }
-    } else {
-        const float l2 = decay_log2(log_decay, head), w0 = args.w_scale[kind];
-        bool ok = true;
-        for (int t = 0; t < n; ++t) {
-            if (!__all_sync(0xffffffffu, mbar_wait(&bars->full[t % C::NST], (t / C::NST) & 1, abort_flag))) { ok = false; break; }
-            uint8_t* st = smem + (t % C::NST) * C::STAGE;
-#pragma unroll
-            for (int u = tid; u < C::TILE / 16; u += 256) {
-                const int r = token_of(t) + (u & 511) / 8;   // token of the part
-                uint4 x = *reinterpret_cast<const uint4*>(st + u * 16), lo;
-                if (r < g.len) {
-                    split8(x, w0 * ex2((float)(back ? r + 1 : g.len - 1 - r) * l2), lo);
-                } else {                                 // another sequence's rows
-                    x = lo = make_uint4(0, 0, 0, 0);
-                    *reinterpret_cast<uint4*>(st + C::TILE + u * 16) = x;
-                }
-                *reinterpret_cast<uint4*>(st + u * 16) = x;
-                *reinterpret_cast<uint4*>(st + 2 * C::TILE + u * 16) = lo;
-            }
-            fence_proxy_async_smem();
-            mbar_arrive(&bars->ready[t % C::NST]);
-        }
-        if (ok && !__all_sync(0xffffffffu, mbar_wait(&bars->mma_done, 0, abort_flag))) ok = false;
+    auto full_wait = [&](int t) { return mbar_wait(&bars->full[t % C::NST], (t / C::NST) & 1, abort_flag); };
+    auto done_wait = [&](int t) { return mbar_wait(&bars->done[t % C::NST], (t / C::NST) & 1, abort_flag); };
+    auto steps = [](const DecayPart& w) { return (w.len + 63) / 64; };
+    // against the direction of decay_out_kernel's walk: what that reads first
+    // is what this one read last, and still in L2
+    auto token = [&](const DecayPart& w, int t) { return 64 * (args.back[w.kind] ? t : (w.len + 63) / 64 - 1 - t); };
+
+    if (warp == 14) {
+        const bool ok = queue_produce<true>(&bars->queue, abort_flag, [&](int id) {
+            DecayPart w{};
+            w.kind = id % kinds;
+            id /= kinds;
+            w.head = id % sh.heads;
+            const Piece g = find_piece(cu, sh, sh.part, id / sh.heads, status);
+            const bool needed = g.seq >= 0 && (args.back[w.kind] ? g.off >= sh.seg : g.rest > sh.seg - g.off % sh.seg);
+            w.seq = needed ? g.seq : -1;
+            w.begin = g.begin; w.len = g.len;
+            return w;
+        });
         if (!ok) fail();
-        tc_fence_after();
-        const int row = 32 * (warp & 3) + lane, hf = warp >> 2;   // feature of b (d = 64: of hi, lo), half of c's
-        const long long slot = (back ? g.begin - sh.part : g.begin) / sh.part;
-        float* dst = args.border[kind] + (slot * sh.heads + head) * D * D;
-        float x[D / 2];
-        if (ok) {
-#pragma unroll
-            for (int c = 0; c < D / 2; c += 32)
-                tmem_ld_32x32b_x32(tbase + ((uint32_t)(32 * (warp & 3)) << 16) + hf * (D / 2) + c, *reinterpret_cast<float(*)[32]>(&x[c]));
-            tmem_wait_ld();
-        }
-        if (D == 64) {
-            // every product has finished: stage 0 holds the lo part for the hi part's threads
-            float* half = reinterpret_cast<float*>(smem) + hf * 32 * 64 + (row & 63);
-            if (ok && row >= 64) {
-#pragma unroll
-                for (int c = 0; c < 32; ++c) half[c * 64] = x[c];
+    } else if (warp == 12) {
+        // -------------------------------------------------------------- loads
+        int s0 = 0, issued = 0;
+        bool ok = true;
+        for (int k = 0; ok; ++k) {
+            DecayPart w;
+            if (!(ok = queue_get(&bars->queue, k, abort_flag, w)) || w.seq < 0) break;
+            const int n = steps(w);
+            if (lane == 0) {
+                for (int t = 0; t < n; ++t) {
+                    const int st = (s0 + t) % C::NST, row = w.begin + token(w, t);
+                    if (s0 + t >= C::NST && !(ok = done_wait(s0 + t - C::NST))) break;
+                    uint8_t* p = smem + st * 2 * C::TILE;
+                    mbar_arrive_expect_tx(&bars->full[st], 2 * C::TILE);
+                    for (int c = 0; c < C::NCH; ++c) {
+                        tma_load_3d(p + c * C::CHUNK, &args.b[w.kind], &bars->full[st], 64 * c, w.head, row);
+                        tma_load_3d(p + C::TILE + c * C::CHUNK, &args.c[w.kind], &bars->full[st], 64 * c, w.head, row);
+                    }
+                    ++issued;
+                }
+                queue_ending(&bars->queue);
             }
-            asm volatile("bar.sync 1, 256;" ::: "memory");
-            if (ok && row < 64) {
+            __syncwarp();
+            ok = __all_sync(0xffffffffu, ok);
+            s0 += n;
+        }
+        if (!ok) fail();
+        if (lane == 0 && *abort_flag)                    // every load must land before the shared memory is given up
+            for (int i = max(0, issued - C::NST); i < issued; ++i) wait_noabort(&bars->full[i % C::NST], (i / C::NST) & 1);
+    } else if (warp == 13) {
+        // --------------------------------------------------------------- MMAs
+        constexpr uint32_t id_x = idesc_bf16_f32(128, D, true, true);
+        const uint32_t base = smem_u32(smem);
+        const uint64_t mn_major = smem_desc_sw128(base, C::CHUNK, 1024);
+        auto wait = [&](uint64_t* bar, int parity) { return __all_sync(0xffffffffu, mma_wait(bar, parity, abort_flag)) != 0; };
+        int s0 = 0, last_step = -1;
+        bool ok = true;
+        for (int k = 0; ok; ++k) {
+            DecayPart w;
+            if (!(ok = queue_get(&bars->queue, k, abort_flag, w)) || w.seq < 0) break;
+            const int n = warp_uniform(steps(w));
+            const uint32_t acc = tbase + 128 * (k & 1);
+            if (k >= 2 && !(ok = wait(&bars->sum_free[k & 1], (k / 2 - 1) & 1))) break;
+            for (int t = 0; t < n; ++t) {
+                const int step = s0 + t, at = (step % C::NST) * 2 * C::TILE, lo_at = C::LO_OFF + (step & 1) * C::TILE;
+                // d = 64: hi and lo are the two 64-feature chunks of one operand
+                const uint64_t b = D == 128 ? desc_add(mn_major, at) : smem_desc_sw128(base + at, lo_at - at, 1024);
+                const uint64_t lo = desc_add(mn_major, lo_at), c = desc_add(mn_major, at + C::TILE);
+                if (!(ok = wait(&bars->ready, step & 1))) break;
+                tc_fence_after();
+                if (elect_one()) {
 #pragma unroll
-                for (int c = 0; c < 32; ++c) x[c] += half[c * 64];
+                    for (int kk = 0; kk < 4; ++kk) {     // 16 tokens per MMA
+                        mma_bf16_ss(acc, desc_add(b, kk * 2048), desc_add(c, kk * 2048), id_x, t > 0 || kk > 0);
+                        if (D == 128) mma_bf16_ss(acc, desc_add(lo, kk * 2048), desc_add(c, kk * 2048), id_x, 1);
+                    }
+                    mma_commit(&bars->done[step % C::NST]);
+                    if (t == n - 1) mma_commit(&bars->sum_full[k & 1]);
+                }
+                __syncwarp();
+                last_step = step;
+            }
+            s0 += n;
+        }
+        if (!ok) fail();
+        // products in flight have to finish before the CTA leaves
+        if (last_step >= 0) wait_noabort(&bars->done[last_step % C::NST], (last_step / C::NST) & 1);
+    } else if (warp < 8) {
+        // -------------------------------------------------------------- split
+        int s0 = 0;
+        bool ok = true;
+        for (int k = 0; ok; ++k) {
+            DecayPart w;
+            if (!(ok = queue_get(&bars->queue, k, abort_flag, w)) || w.seq < 0) break;
+            const float l2 = decay_log2(log_decay, w.head), w0 = args.w_scale[w.kind];
+            const bool back = args.back[w.kind];
+            const int n = steps(w);
+            for (int t = 0; t < n; ++t) {
+                const int step = s0 + t, tok = token(w, t);
+                // lo's place is free with the products of two steps before
+                if (!__all_sync(0xffffffffu, full_wait(step) && (step < 2 || done_wait(step - 2)))) { ok = false; break; }
+                uint8_t* st = smem + (step % C::NST) * 2 * C::TILE;
+                uint8_t* sl = smem + C::LO_OFF + (step & 1) * C::TILE;
+#pragma unroll
+                for (int u = tid; u < C::TILE / 16; u += 256) {
+                    const int r = tok + (u & 511) / 8;   // token of the part
+                    uint4 x = *reinterpret_cast<const uint4*>(st + u * 16), lo;
+                    split8(x, w0 * ex2((float)(back ? r + 1 : w.len - 1 - r) * l2), lo);
+                    if (r >= w.len) {                    // another sequence's rows
+                        x = lo = make_uint4(0, 0, 0, 0);
+                        *reinterpret_cast<uint4*>(st + C::TILE + u * 16) = x;
+                    }
+                    *reinterpret_cast<uint4*>(st + u * 16) = x;
+                    *reinterpret_cast<uint4*>(sl + u * 16) = lo;
+                }
+                fence_proxy_async_smem();
+                mbar_arrive(&bars->ready);
+            }
+            s0 += n;
+        }
+        if (!ok) fail();
+    } else if (warp < 12) {
+        // ------------------------------------------------------------ outputs
+        // a TMEM lane per thread: a feature of b (d = 64: of hi and of lo,
+        // whose sums meet in the lo threads' place of shared memory)
+        const int row = 32 * (warp & 3) + lane, feat = row & (D - 1);
+        __shared__ float half[D == 64 ? 32 * 64 : 1];
+        int exchanges = 0;
+        bool ok = true;
+        for (int k = 0; ok; ++k) {
+            DecayPart w;
+            if (!(ok = queue_get(&bars->queue, k, abort_flag, w)) || w.seq < 0) break;
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bars->sum_full[k & 1], (k / 2) & 1, abort_flag)))) break;
+            tc_fence_after();
+            const bool back = args.back[w.kind];
+            const long long slot = (back ? w.begin - sh.part : w.begin) / sh.part;
+            float* dst = args.border[w.kind] + (slot * sh.heads + w.head) * D * D;
+            const QuadRows at((long long)feat * D);
+#pragma unroll 1
+            for (int c = 0; c < D && ok; c += 32) {
+                float x[32];
+                tmem_ld_32x32b_x32(tbase + 128 * (k & 1) + ((uint32_t)(32 * (warp & 3)) << 16) + c, x);
+                tmem_wait_ld();
+                if (c + 32 == D) {
+                    tc_fence_before();
+                    mbar_arrive(&bars->sum_free[k & 1]);
+                }
+                if (D == 64) {
+                    if (row >= 64) {
+                        if (exchanges > 0 && !(ok = __all_sync(0xffffffffu, mbar_wait(&bars->half_free, (exchanges - 1) & 1, abort_flag)))) break;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) half[e * 64 + feat] = x[e];
+                        mbar_arrive(&bars->half_full);
+                    } else {
+                        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bars->half_full, exchanges & 1, abort_flag)))) break;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) x[e] += half[e * 64 + feat];
+                        mbar_arrive(&bars->half_free);
+                    }
+                    ++exchanges;
+                }
+                if (row < D) store_rows(dst + c, at, x);
             }
         }
-        if (ok && row < D) {                             // (whole warps)
-#pragma unroll
-            for (int c = 0; c < D / 2; c += 16) {
-                uint4 u[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    u[e] = make_uint4(__float_as_uint(x[c + 4 * e]), __float_as_uint(x[c + 4 * e + 1]), __float_as_uint(x[c + 4 * e + 2]),
-                                      __float_as_uint(x[c + 4 * e + 3]));
-                transpose_units(u, lane);
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    *reinterpret_cast<uint4*>(dst + (long long)((row & ~3) + e) * D + hf * (D / 2) + c + (lane & 3) * 4) = u[e];
-            }
-        }
+        if (!ok) fail();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 8) tmem_dealloc(tbase, 128);
+    if (warp == 13) tmem_dealloc(tbase, 256);
 }
 
 struct DecayScanArgs {
@@ -930,7 +995,7 @@ static cudaError_t launch_decay(const DecayArgs& a, const DecayShape& sh, const 
     if (a.total > sh.seg) {                              // some sequence may have several segments
         e = cudaFuncSetAttribute(decay_state_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, DecStateCfg<D>::SMEM);
         if (e != cudaSuccess) return e;
-        decay_state_kernel<D><<<dim3(parts, kinds), DecStateCfg<D>::THREADS, DecStateCfg<D>::SMEM, stream>>>(st, sh, a.cu, a.log_decay, a.status);
+        decay_state_kernel<D><<<parts * kinds, DecStateCfg<D>::THREADS, DecStateCfg<D>::SMEM, stream>>>(st, kinds, sh, a.cu, a.log_decay, a.status);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
         decay_scan_kernel<D><<<dim3((unsigned)((long long)a.n_seq * a.heads), D * D / 1024, kinds), 256, 0, stream>>>(sc, sh, a.cu, a.log_decay, a.status);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
