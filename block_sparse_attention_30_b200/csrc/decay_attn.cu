@@ -371,8 +371,10 @@ template <int D>
 __global__ void __launch_bounds__(256)
 decay_scan_kernel(const __grid_constant__ DecayScanArgs args, const DecayShape sh, const int32_t* __restrict__ cu,
                   const float* __restrict__ log_decay, int* status) {
+    grid_dependents_launch();                            // decay_out_kernel may start: it waits for the borders itself
     const int head = blockIdx.x % sh.heads, seq = blockIdx.x / sh.heads, kind = blockIdx.z;
     const SeqRange r = seq_range(cu, seq, sh.total, status);
+    grid_dependency_wait();                              // (by every CTA: so decay_out_kernel's wait covers the sums' launch too)
     if (r.len <= sh.seg) return;
     const int back = args.back[kind];
     const int per = sh.seg / sh.part, parts = (r.len + sh.part - 1) / sh.part;
@@ -386,7 +388,7 @@ decay_scan_kernel(const __grid_constant__ DecayScanArgs args, const DecayShape s
     const int tail = r.len - (parts - 1) * sh.part;      // tokens of the last part
     const long long step = (long long)sh.heads * D * D;
     float* base = args.border[kind] + (r.begin / sh.part) * step + (long long)head * D * D + e;   // border 0
-    constexpr int AHEAD = 8;
+    constexpr int AHEAD = 12;
     for (int i0 = 0; i0 < n; i0 += AHEAD) {
         float4 u[AHEAD];
 #pragma unroll
@@ -421,7 +423,10 @@ struct DecOutCfg {
     static constexpr int SMEM = BAR_OFF + 512;
     static constexpr int THREADS = 768;                  // warpgroups: 2 scores, 2 state, outputs, loads and MMAs; 80 registers a thread
     static constexpr int REG_SCORE = 72, REG_STATE = 104, REG_OUT = 80, REG_LOAD = 48;   // 2 * 72 + 2 * 104 + 80 + 48 = 6 * 80
-    static constexpr int U_COL = 0, S_COL = 128, O1_COL = 256, O2_COL = 384;  // TMEM
+    // TMEM; at d = 64 the scores have two places, so that those of the next step
+    // are formed before the weights of this one are used up
+    static constexpr int NS = D == 128 ? 1 : 2;
+    static constexpr int U_COL = 0, S_COL = D == 128 ? 128 : 64, O1_COL = D == 128 ? 256 : 320, O2_COL = 384;
 };
 static_assert(DecOutCfg<128>::SMEM <= 232448 && DecOutCfg<64>::SMEM <= 232448, "shared memory");
 
@@ -437,7 +442,7 @@ struct DecOutBars {
     WorkQueue<DecayWork> queue;
     uint64_t b_full[DecOutCfg<D>::NB], ac_full[DecOutCfg<D>::NAC];
     uint64_t u_done[DecOutCfg<D>::NB];   // every product of a step in this slot of B
-    uint64_t s_full, p_ready, x_ready, w_ready, o_full, o_free, mma_done;
+    uint64_t s_full[2], p_ready, x_ready, w_ready, o_full, o_free, mma_done;
     uint64_t pow_ready, lo_ready, lo_free;
     uint32_t tmem_base;
     int abort;
@@ -467,7 +472,7 @@ decay_out_kernel(const __grid_constant__ DecayPasses passes, const int n_passes,
         queue_init(&bars->queue, 22);
         for (int x = 0; x < C::NB; ++x) { mbar_init(&bars->b_full[x], 1); mbar_init(&bars->u_done[x], 1); }
         for (int x = 0; x < C::NAC; ++x) mbar_init(&bars->ac_full[x], 1);
-        mbar_init(&bars->s_full, 1);
+        for (int x = 0; x < 2; ++x) mbar_init(&bars->s_full[x], 1);
         mbar_init(&bars->p_ready, 256);
         mbar_init(&bars->x_ready, 256);
         mbar_init(&bars->w_ready, 512);
@@ -491,6 +496,7 @@ decay_out_kernel(const __grid_constant__ DecayPasses passes, const int n_passes,
     auto ac_slot = [&](int i) { return C::AC_OFF + (i % C::NAC) * C::TILE; };
     auto ac_wait = [&](int i) { return mma_wait(&bars->ac_full[i % C::NAC], (i / C::NAC) & 1, abort_flag); };
     auto u_wait = [&](int t) { return mbar_wait(&bars->u_done[t % C::NB], (t / C::NB) & 1, abort_flag); };
+    auto s_wait = [&](int t) { return mbar_wait(&bars->s_full[t % C::NS], (t / C::NS) & 1, abort_flag); };
     // the walk's chunks (step t is chunk t, or chunks - 1 - t backwards), and
     // whether it reaches the end of its sequence and writes the state there
     auto chunks = [](const DecayWork& w) { return (w.len + 127) / 128; };
@@ -592,9 +598,9 @@ decay_out_kernel(const __grid_constant__ DecayPasses passes, const int n_passes,
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                     const uint32_t o = (kk >> 2) * C::CHUNK + (kk & 3) * 32;
-                    mma_bf16_ss(tbase + C::S_COL, desc_add(a, o), desc_add(b, o), id_s, kk > 0);
+                    mma_bf16_ss(tbase + C::S_COL + 128 * (t % C::NS), desc_add(a, o), desc_add(b, o), id_s, kk > 0);
                 }
-                mma_commit(&bars->s_full);
+                mma_commit(&bars->s_full[t % C::NS]);
             }
             __syncwarp();
         };
@@ -610,6 +616,10 @@ decay_out_kernel(const __grid_constant__ DecayPasses passes, const int n_passes,
             for (int t = 0; t < n && ok; ++t) {
                 const int step = s0 + t;
                 const uint64_t a = desc_add(k_major, ac_slot(2 * step)), c = desc_add(mn_major, ac_slot(2 * step + 1));
+                if (C::NS == 2 && t + 1 < n) {
+                    if (!(ok = all(b_wait(step + 1) && ac_wait(2 * step + 2)))) break;
+                    issue_s(step + 1);
+                }
                 // O1 = P C
                 if (!(ok = all((step == 0 || mma_wait(&bars->o_free, (step - 1) & 1, abort_flag)) && ac_wait(2 * step + 1) &&
                                mma_wait(&bars->p_ready, step & 1, abort_flag))))
@@ -618,7 +628,8 @@ decay_out_kernel(const __grid_constant__ DecayPasses passes, const int n_passes,
                 if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < 8; ++kk)       // P: 64 tokens in 32 columns, each half where its scores were
-                        mma_bf16_ts(tbase + C::O1_COL, tbase + C::S_COL + (kk >> 2) * 64 + (kk & 3) * 8, desc_add(c, kk * 2048), id_o, kk > 0);
+                        mma_bf16_ts(tbase + C::O1_COL, tbase + C::S_COL + 128 * (step % C::NS) + (kk >> 2) * 64 + (kk & 3) * 8,
+                                    desc_add(c, kk * 2048), id_o, kk > 0);
                 }
                 __syncwarp();
                 // O2 = A X
@@ -636,7 +647,7 @@ decay_out_kernel(const __grid_constant__ DecayPasses passes, const int n_passes,
                 }
                 __syncwarp();
                 // the scores of the next step and U of this one, as their inputs arrive
-                bool s_next = t + 1 < n, u_next = t < updates;
+                bool s_next = C::NS == 1 && t + 1 < n, u_next = t < updates;
                 const unsigned long long t0 = clock64();
                 while (s_next || u_next) {
                     if (s_next && all(mbar_test_wait(&bars->b_full[(step + 1) % C::NB], ((step + 1) / C::NB) & 1) &&
@@ -712,8 +723,9 @@ decay_out_kernel(const __grid_constant__ DecayPasses passes, const int n_passes,
                         *reinterpret_cast<uint4*>(c + (u % C::NCH) * C::CHUNK + rows * 128 + (u / C::NCH) * 16) = make_uint4(0, 0, 0, 0);
                     fence_proxy_async_smem();
                 }
-                if (!__all_sync(0xffffffffu, mbar_wait(&bars->s_full, step & 1, abort_flag))) { ok = false; break; }
+                if (!__all_sync(0xffffffffu, s_wait(step))) { ok = false; break; }
                 tc_fence_after();
+                const uint32_t tP = tS + 128 * (step % C::NS);
                 // P over the scores, 32 columns at a time (a loop: the kernel's
                 // roles have to share the instruction cache)
 #pragma unroll 1
@@ -726,7 +738,7 @@ decay_out_kernel(const __grid_constant__ DecayPasses passes, const int n_passes,
                         const uint64_t* y = reinterpret_cast<const uint64_t*>(sPow + (at & 1 ? 64 + 1 + at : at));
                         const float f = ps.p_scale * ex2((float)far * l2);
                         float s[32];
-                        tmem_ld_32x32b_x32(tS + 32 * h, s);
+                        tmem_ld_32x32b_x32(tP + 32 * h, s);
                         tmem_wait_ld();
                         const uint64_t f2 = f32x2(f, f);
 #pragma unroll
@@ -744,7 +756,7 @@ decay_out_kernel(const __grid_constant__ DecayPasses passes, const int n_passes,
 #pragma unroll
                         for (int e = 0; e < 16; ++e) pk[e] = 0;
                     }
-                    tmem_st_32x32b_x16(tS + 16 * h, pk); // (over scores of this thread's that are read or masked)
+                    tmem_st_32x32b_x16(tP + 16 * h, pk); // (over scores of this thread's that are read or masked)
                 }
                 tmem_wait_st();
                 tc_fence_before();
@@ -802,6 +814,7 @@ decay_out_kernel(const __grid_constant__ DecayPasses passes, const int n_passes,
     } else {
         reg_inc<C::REG_STATE>();
         // ---------------------------------------------------------- the state
+        grid_dependency_wait();                          // the borders; nothing else here depends on the launches before
         // in registers: a row (TMEM lane) and half of its columns
         const int id = tid - 256, hf = id >> 7, row = id & 127, feat = row & (D - 1);
         const uint32_t tU = tbase + ((uint32_t)(32 * (warp & 3)) << 16) + C::U_COL + hf * (D / 2);
@@ -880,8 +893,8 @@ decay_out_kernel(const __grid_constant__ DecayPasses passes, const int n_passes,
                         make_uint4(pack_bf16x2(x[c], x[c + 1]), pack_bf16x2(x[c + 2], x[c + 3]), pack_bf16x2(x[c + 4], x[c + 5]),
                                    pack_bf16x2(x[c + 6], x[c + 7]));
                 }
-                // (before x_ready: the next step's scores wait for that, so this phase cannot be missed)
-                if (!__all_sync(0xffffffffu, mbar_wait(&bars->s_full, step & 1, abort_flag))) { ok = false; break; }
+                // (before x_ready: the scores that would follow in the same place wait for that, so this phase cannot be missed)
+                if (!__all_sync(0xffffffffu, s_wait(step))) { ok = false; break; }
                 fence_proxy_async_smem();
                 mbar_arrive(&bars->x_ready);
                 if (t < updates && !split_units(step, id, C::UNITS_P, C::UNITS, rows, back, ps.w_scale, l2)) { ok = false; break; }
@@ -961,13 +974,13 @@ static DecayShape decay_shape(int n_seq, int total, int heads, int d, int passes
     };
     for (int pieces = 1; pieces <= 12; ++pieces) consider(pieces);
     for (int rounds = 1; rounds <= 4; ++rounds) consider((long long)(148 * rounds / walks));
-    // parts of a segment: rounds of two CTAs per SM, 2.5 chunks for a start and end
-    const double cuts = std::max(1.0, n_seq == 1 ? (double)((chunks + best - 1) / best - 1) : (double)chunks / best);
+    // parts of a segment: rounds of CTAs, one chunk for a start and end
+    const double cuts = n_seq == 1 ? (double)((chunks + best - 1) / best - 1) : best < longest ? (double)chunks / best : 0.0;
     long long part = best, k = 1;
     best_cost = 1e300;
-    for (int i = 1; i <= 4; ++i) {
+    for (int i = 1; i <= 4 && cuts > 0; ++i) {
         const long long len = (best + i - 1) / i;
-        const double cost = std::ceil(cuts * i * sums / 296) * (len + 2.5);
+        const double cost = std::ceil(cuts * i * sums / 148) * (len + 1.0);
         if (cost < best_cost) { best_cost = cost; part = len; k = i; }
     }
     return {n_seq, total, heads, (int)(128 * part * k), (int)(128 * part)};
@@ -997,8 +1010,11 @@ static cudaError_t launch_decay(const DecayArgs& a, const DecayShape& sh, const 
         if (e != cudaSuccess) return e;
         decay_state_kernel<D><<<parts * kinds, DecStateCfg<D>::THREADS, DecStateCfg<D>::SMEM, stream>>>(st, kinds, sh, a.cu, a.log_decay, a.status);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
-        decay_scan_kernel<D><<<dim3((unsigned)((long long)a.n_seq * a.heads), D * D / 1024, kinds), 256, 0, stream>>>(sc, sh, a.cu, a.log_decay, a.status);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        e = launch_overlapped(decay_scan_kernel<D>, dim3((unsigned)((long long)a.n_seq * a.heads), D * D / 1024, kinds), 256, 0, stream,
+                              sc, sh, a.cu, a.log_decay, a.status);
+        if (e != cudaSuccess) return e;
+        return launch_overlapped(decay_out_kernel<D>, dim3(segs * n_passes), DecOutCfg<D>::THREADS, DecOutCfg<D>::SMEM, stream, passes,
+                                 n_passes, sh, a.cu, a.log_decay, a.status);
     }
     decay_out_kernel<D><<<segs * n_passes, DecOutCfg<D>::THREADS, DecOutCfg<D>::SMEM, stream>>>(passes, n_passes, sh, a.cu, a.log_decay, a.status);
     return cudaGetLastError();

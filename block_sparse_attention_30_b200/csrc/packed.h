@@ -10,6 +10,23 @@
 
 namespace vsa {
 
+// Launch a kernel that may start before the one before it in the stream has
+// ended; it waits (grid_dependency_wait) before it touches what that writes.
+template <typename... P, typename... A>
+cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t stream, A&&... args) {
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t c{};
+    c.gridDim = grid;
+    c.blockDim = dim3(threads);
+    c.dynamicSmemBytes = smem;
+    c.stream = stream;
+    c.attrs = &at;
+    c.numAttrs = 1;
+    return cudaLaunchKernelEx(&c, kernel, static_cast<P>(args)...);
+}
+
 // One bf16 tensor [rows][heads][d]: heads and features contiguous, rows
 // `stride` elements apart.
 struct PackedTensor {
