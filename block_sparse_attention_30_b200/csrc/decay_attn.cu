@@ -56,7 +56,6 @@ struct DecayPass {
     __nv_bfloat16* out;
     long long out_stride;
     const float* first;          // [n_seq][heads][d][d]: the state the walk starts with, or null (zeros)
-    float* last;                 // the state it ends with, or null
     const float* border;         // [slots][heads][d][d]: the states between segments
     int back;                    // walk backwards in time
     int trans;                   // the states in memory are c^T b
@@ -110,6 +109,28 @@ __device__ __forceinline__ void split_pair(uint32_t x, float w, uint32_t& hi, ui
     lo = pack_bf16x2(x0, x1);
 }
 
+// ... as hi + mid + lo.
+__device__ __forceinline__ void split_pair3(uint32_t x, float w, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
+    const uint64_t p = mul_f32x2(f32x2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u)), f32x2(w, w));
+    const uint64_t neg = f32x2(-1.f, -1.f);
+    float x0, x1;
+    unf32x2(p, x0, x1);
+    hi = pack_bf16x2(x0, x1);
+    // what hi leaves, exactly
+    const uint64_t r = fma_f32x2(f32x2(__uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u)), neg, p);
+    unf32x2(r, x0, x1);
+    mid = pack_bf16x2(x0, x1);
+    unf32x2(fma_f32x2(f32x2(__uint_as_float(mid << 16), __uint_as_float(mid & 0xffff0000u)), neg, r), x0, x1);
+    lo = pack_bf16x2(x0, x1);
+}
+
+__device__ __forceinline__ void split8(uint4& x, float w, uint4& mid, uint4& lo) {
+    split_pair3(x.x, w, x.x, mid.x, lo.x);
+    split_pair3(x.y, w, x.y, mid.y, lo.y);
+    split_pair3(x.z, w, x.z, mid.z, lo.z);
+    split_pair3(x.w, w, x.w, mid.w, lo.w);
+}
+
 __device__ __forceinline__ void split8(uint4& x, float w, uint4& lo) {
     split_pair(x.x, w, x.x, lo.x);
     split_pair(x.y, w, x.y, lo.y);
@@ -123,9 +144,10 @@ struct DecStateCfg {
     static constexpr int NCH = D / 64;
     static constexpr int CHUNK = 64 * 128;               // 64 tokens of one 64-feature chunk
     static constexpr int TILE = NCH * CHUNK;
-    static constexpr int NST = D == 128 ? 6 : 8;         // stages of b (hi in its place) and c
-    static constexpr int LO_OFF = NST * 2 * TILE;        // lo of even and odd steps
-    static constexpr int BAR_OFF = LO_OFF + 2 * TILE;
+    static constexpr int NST = D == 128 ? 5 : 8;         // stages of b (hi in its place) and c
+    static constexpr int ZERO_OFF = NST * 2 * TILE;      // d = 64: a tile of zeros
+    static constexpr int LO_OFF = ZERO_OFF + (D == 64 ? TILE : 0);   // mid and lo of even and odd steps
+    static constexpr int BAR_OFF = LO_OFF + 4 * TILE;
     static constexpr int SMEM = BAR_OFF + 512;
     static constexpr int THREADS = 512;                  // 8 split warps, 4 output warps, loads, MMAs, queue
 };
@@ -134,13 +156,14 @@ static_assert(DecStateCfg<128>::SMEM <= 232448, "shared memory");
 struct DecayPart {
     int seq, head, kind;
     int begin, len;
+    int ends;                    // the walk's last part
 };
 
 template <int D>
 struct DecStateBars {
     WorkQueue<DecayPart> queue;
     uint64_t full[DecStateCfg<D>::NST], done[DecStateCfg<D>::NST];
-    uint64_t ready, sum_full[2], sum_free[2], half_full, half_free;
+    uint64_t ready[2], sum_full[2], sum_free[2], half_full, half_free;
     uint32_t tmem_base;
     int abort;
 };
@@ -149,15 +172,23 @@ static_assert(sizeof(DecStateBars<64>) <= 512, "barrier block");
 struct DecayStateArgs {
     CUtensorMap b[2], c[2];
     float* border[2];
+    float* last[2];              // [n_seq][heads][d][d]: the walk's last part, for the scan to finish; or null
     int back[2];
     float w_scale[2];
 };
 
 // grid (kinds of state x parts x heads), from a queue per CTA.  Forward in time
 // the sum of part p goes to the border behind it, backwards that of part p + 1;
-// parts of the walk's last segment reach no border that is needed.  Steps of 64
-// tokens are counted on from part to part; a part's sum lies in one of two TMEM
-// accumulators, so that it is stored while the next part's is formed.
+// the walk's last part's to `last`, and without that the parts of its last
+// segment are not needed.  Steps of 64 tokens are counted on from part to part;
+// a part's sum lies in one of two TMEM accumulators (d = 128: pairs of them), so
+// that it is stored while the next part's is formed.
+//
+// The states leave the library, so the sums are good to fp32: the weighted
+// operand is split into three bf16 parts (all 24 bits), and the products of the
+// two small ones have an accumulator of their own.  The tensor cores' fp32
+// accumulation loses about 6e-9 of a sum per step of 16 tokens (measured), which
+// is why a part has 12 chunks at most: 6e-7.
 template <int D>
 __global__ void __launch_bounds__(DecStateCfg<D>::THREADS, 1)
 decay_state_kernel(const __grid_constant__ DecayStateArgs args, const int kinds, const DecayShape sh,
@@ -175,13 +206,17 @@ decay_state_kernel(const __grid_constant__ DecayStateArgs args, const int kinds,
         bars->abort = 0;
         queue_init(&bars->queue, 14);
         for (int x = 0; x < C::NST; ++x) { mbar_init(&bars->full[x], 1); mbar_init(&bars->done[x], 1); }
-        mbar_init(&bars->ready, 256);
+        for (int x = 0; x < 2; ++x) mbar_init(&bars->ready[x], 256);
         for (int x = 0; x < 2; ++x) { mbar_init(&bars->sum_full[x], 1); mbar_init(&bars->sum_free[x], 128); }
         mbar_init(&bars->half_full, 64);
         mbar_init(&bars->half_free, 64);
         fence_barrier_init();
     }
-    if (warp == 13) { tmem_alloc(&bars->tmem_base, 256); tmem_relinquish(); }
+    if (warp == 13) { tmem_alloc(&bars->tmem_base, 512); tmem_relinquish(); }
+    if (D == 64) {
+        for (int u = tid; u < C::TILE / 16; u += C::THREADS) *reinterpret_cast<uint4*>(smem + C::ZERO_OFF + u * 16) = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -201,9 +236,10 @@ decay_state_kernel(const __grid_constant__ DecayStateArgs args, const int kinds,
             id /= kinds;
             w.head = id % sh.heads;
             const Piece g = find_piece(cu, sh, sh.part, id / sh.heads, status);
-            const bool needed = g.seq >= 0 && (args.back[w.kind] ? g.off >= sh.seg : g.rest > sh.seg - g.off % sh.seg);
+            const bool needed = args.last[w.kind] ? g.len > 0 : args.back[w.kind] ? g.off >= sh.seg : g.rest > sh.seg - g.off % sh.seg;
             w.seq = needed ? g.seq : -1;
             w.begin = g.begin; w.len = g.len;
+            w.ends = args.back[w.kind] ? g.off == 0 : g.rest <= sh.part;
             return w;
         });
         if (!ok) fail();
@@ -251,17 +287,22 @@ decay_state_kernel(const __grid_constant__ DecayStateArgs args, const int kinds,
             const uint32_t acc = tbase + 128 * (k & 1);
             if (k >= 2 && !(ok = wait(&bars->sum_free[k & 1], (k / 2 - 1) & 1))) break;
             for (int t = 0; t < n; ++t) {
-                const int step = s0 + t, at = (step % C::NST) * 2 * C::TILE, lo_at = C::LO_OFF + (step & 1) * C::TILE;
-                // d = 64: hi and lo are the two 64-feature chunks of one operand
-                const uint64_t b = D == 128 ? desc_add(mn_major, at) : smem_desc_sw128(base + at, lo_at - at, 1024);
-                const uint64_t lo = desc_add(mn_major, lo_at), c = desc_add(mn_major, at + C::TILE);
-                if (!(ok = wait(&bars->ready, step & 1))) break;
+                const int step = s0 + t, at = (step % C::NST) * 2 * C::TILE, mid_at = C::LO_OFF + (step & 1) * 2 * C::TILE;
+                const int lo_at = mid_at + C::TILE;
+                const uint64_t c = desc_add(mn_major, at + C::TILE);
+                // d = 64: hi and mid, and zeros and lo, are the two 64-feature chunks of one operand
+                const uint64_t hi = D == 128 ? desc_add(mn_major, at) : smem_desc_sw128(base + at, mid_at - at, 1024);
+                const uint64_t mid = desc_add(mn_major, mid_at);
+                const uint64_t lo = D == 128 ? desc_add(mn_major, lo_at) : smem_desc_sw128(base + C::ZERO_OFF, lo_at - C::ZERO_OFF, 1024);
+                if (!(ok = wait(&bars->ready[step & 1], (step >> 1) & 1))) break;
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk) {     // 16 tokens per MMA
-                        mma_bf16_ss(acc, desc_add(b, kk * 2048), desc_add(c, kk * 2048), id_x, t > 0 || kk > 0);
-                        if (D == 128) mma_bf16_ss(acc, desc_add(lo, kk * 2048), desc_add(c, kk * 2048), id_x, 1);
+                        const uint64_t cd = desc_add(c, kk * 2048);
+                        mma_bf16_ss(acc, desc_add(hi, kk * 2048), cd, id_x, t > 0 || kk > 0);
+                        if (D == 128) mma_bf16_ss(acc + 256, desc_add(mid, kk * 2048), cd, id_x, t > 0 || kk > 0);
+                        mma_bf16_ss(D == 128 ? acc + 256 : acc, desc_add(lo, kk * 2048), cd, id_x, 1);
                     }
                     mma_commit(&bars->done[step % C::NST]);
                     if (t == n - 1) mma_commit(&bars->sum_full[k & 1]);
@@ -286,32 +327,33 @@ decay_state_kernel(const __grid_constant__ DecayStateArgs args, const int kinds,
             const int n = steps(w);
             for (int t = 0; t < n; ++t) {
                 const int step = s0 + t, tok = token(w, t);
-                // lo's place is free with the products of two steps before
+                // mid's and lo's place is free with the products of two steps before
                 if (!__all_sync(0xffffffffu, full_wait(step) && (step < 2 || done_wait(step - 2)))) { ok = false; break; }
                 uint8_t* st = smem + (step % C::NST) * 2 * C::TILE;
-                uint8_t* sl = smem + C::LO_OFF + (step & 1) * C::TILE;
+                uint8_t* sl = smem + C::LO_OFF + (step & 1) * 2 * C::TILE;
 #pragma unroll
                 for (int u = tid; u < C::TILE / 16; u += 256) {
                     const int r = tok + (u & 511) / 8;   // token of the part
-                    uint4 x = *reinterpret_cast<const uint4*>(st + u * 16), lo;
-                    split8(x, w0 * ex2((float)(back ? r + 1 : w.len - 1 - r) * l2), lo);
+                    uint4 x = *reinterpret_cast<const uint4*>(st + u * 16), mid, lo;
+                    split8(x, w0 * ex2((float)(back ? r + 1 : w.len - 1 - r) * l2), mid, lo);
                     if (r >= w.len) {                    // another sequence's rows
-                        x = lo = make_uint4(0, 0, 0, 0);
+                        x = mid = lo = make_uint4(0, 0, 0, 0);
                         *reinterpret_cast<uint4*>(st + C::TILE + u * 16) = x;
                     }
                     *reinterpret_cast<uint4*>(st + u * 16) = x;
-                    *reinterpret_cast<uint4*>(sl + u * 16) = lo;
+                    *reinterpret_cast<uint4*>(sl + u * 16) = mid;
+                    *reinterpret_cast<uint4*>(sl + C::TILE + u * 16) = lo;
                 }
                 fence_proxy_async_smem();
-                mbar_arrive(&bars->ready);
+                mbar_arrive(&bars->ready[step & 1]);
             }
             s0 += n;
         }
         if (!ok) fail();
     } else if (warp < 12) {
         // ------------------------------------------------------------ outputs
-        // a TMEM lane per thread: a feature of b (d = 64: of hi and of lo,
-        // whose sums meet in the lo threads' place of shared memory)
+        // a TMEM lane per thread: a feature of b (d = 64: of hi, and of mid and
+        // lo, whose sums meet in shared memory)
         const int row = 32 * (warp & 3) + lane, feat = row & (D - 1);
         __shared__ float half[D == 64 ? 32 * 64 : 1];
         int exchanges = 0;
@@ -323,13 +365,22 @@ decay_state_kernel(const __grid_constant__ DecayStateArgs args, const int kinds,
             tc_fence_after();
             const bool back = args.back[w.kind];
             const long long slot = (back ? w.begin - sh.part : w.begin) / sh.part;
-            float* dst = args.border[w.kind] + (slot * sh.heads + w.head) * D * D;
+            float* dst = w.ends ? args.last[w.kind] + ((long long)w.seq * sh.heads + w.head) * D * D
+                                : args.border[w.kind] + (slot * sh.heads + w.head) * D * D;
             const QuadRows at((long long)feat * D);
 #pragma unroll 1
             for (int c = 0; c < D && ok; c += 32) {
                 float x[32];
-                tmem_ld_32x32b_x32(tbase + 128 * (k & 1) + ((uint32_t)(32 * (warp & 3)) << 16) + c, x);
+                const uint32_t acc = tbase + 128 * (k & 1) + ((uint32_t)(32 * (warp & 3)) << 16) + c;
+                tmem_ld_32x32b_x32(acc, x);
                 tmem_wait_ld();
+                if (D == 128) {
+                    float y[32];
+                    tmem_ld_32x32b_x32(acc + 256, y);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) x[e] += y[e];
+                }
                 if (c + 32 == D) {
                     tc_fence_before();
                     mbar_arrive(&bars->sum_free[k & 1]);
@@ -356,16 +407,18 @@ decay_state_kernel(const __grid_constant__ DecayStateArgs args, const int kinds,
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 13) tmem_dealloc(tbase, 256);
+    if (warp == 13) tmem_dealloc(tbase, 512);
 }
 
 struct DecayScanArgs {
     float* border[2];
     const float* first[2];
+    float* last[2];              // or null
     int back[2];
 };
 
-// Border sums -> states at the borders, in place.  grid (sequences x heads,
+// Border sums -> states at the borders, in place, and the last part's sum in
+// `last` -> the state that the walk ends with.  grid (sequences x heads,
 // D^2 / 1024, kinds of state), 4 elements per thread.
 template <int D>
 __global__ void __launch_bounds__(256)
@@ -375,11 +428,13 @@ decay_scan_kernel(const __grid_constant__ DecayScanArgs args, const DecayShape s
     const int head = blockIdx.x % sh.heads, seq = blockIdx.x / sh.heads, kind = blockIdx.z;
     const SeqRange r = seq_range(cu, seq, sh.total, status);
     grid_dependency_wait();                              // (by every CTA: so decay_out_kernel's wait covers the sums' launch too)
-    if (r.len <= sh.seg) return;
+    float* last = args.last[kind];
+    if (r.len <= sh.seg && !last) return;
     const int back = args.back[kind];
     const int per = sh.seg / sh.part, parts = (r.len + sh.part - 1) / sh.part;
-    // border b lies behind part b: forward those up to the last segment's, backwards from the last one down to the first segment's
-    const int n = back ? parts - per : (r.len - 1) / sh.seg * per, b0 = back ? parts - 2 : 0;
+    // border b lies behind part b; without `last`, forward those up to the last
+    // segment's, backwards from the last one down to the first segment's
+    const int n = last ? max(0, parts - 1) : back ? parts - per : (r.len - 1) / sh.seg * per, b0 = back ? parts - 2 : 0;
     const int e = (blockIdx.y * 256 + threadIdx.x) * 4;
     const float l2 = decay_log2(log_decay, head);
     const float full = ex2((float)sh.part * l2);
@@ -401,6 +456,17 @@ decay_scan_kernel(const __grid_constant__ DecayScanArgs args, const DecayShape s
             s.x = fmaf(f, s.x, u[j].x); s.y = fmaf(f, s.y, u[j].y); s.z = fmaf(f, s.z, u[j].z); s.w = fmaf(f, s.w, u[j].w);
             *reinterpret_cast<float4*>(base + (back ? b0 - i0 - j : i0 + j) * step) = s;
         }
+    }
+    if (last) {
+        float4* p = reinterpret_cast<float4*>(last + ((long long)seq * sh.heads + head) * D * D + e);
+        if (r.len > 0) {
+            // the walk's last part: forward the sequence's last, backwards its first (the only one, or a full one);
+            // before it n = 0 borders mean that it is the first of the walk as well
+            const float f = ex2((float)(back ? min(r.len, sh.part) : tail) * l2);
+            const float4 u = *p;
+            s.x = fmaf(f, s.x, u.x); s.y = fmaf(f, s.y, u.y); s.z = fmaf(f, s.z, u.z); s.w = fmaf(f, s.w, u.w);
+        }
+        *p = s;                                          // (an empty sequence's state goes through)
     }
 }
 
@@ -442,8 +508,7 @@ struct DecOutBars {
     WorkQueue<DecayWork> queue;
     uint64_t b_full[DecOutCfg<D>::NB], ac_full[DecOutCfg<D>::NAC];
     uint64_t u_done[DecOutCfg<D>::NB];   // every product of a step in this slot of B
-    uint64_t s_full[2], p_ready, x_ready, w_ready, o_full, o_free, mma_done;
-    uint64_t pow_ready, lo_ready, lo_free;
+    uint64_t s_full[2], p_ready[2], x_ready, w_ready, o_full, o_free, mma_done, pow_ready;
     uint32_t tmem_base;
     int abort;
 };
@@ -473,15 +538,13 @@ decay_out_kernel(const __grid_constant__ DecayPasses passes, const int n_passes,
         for (int x = 0; x < C::NB; ++x) { mbar_init(&bars->b_full[x], 1); mbar_init(&bars->u_done[x], 1); }
         for (int x = 0; x < C::NAC; ++x) mbar_init(&bars->ac_full[x], 1);
         for (int x = 0; x < 2; ++x) mbar_init(&bars->s_full[x], 1);
-        mbar_init(&bars->p_ready, 256);
+        for (int x = 0; x < 2; ++x) mbar_init(&bars->p_ready[x], 256);
         mbar_init(&bars->x_ready, 256);
         mbar_init(&bars->w_ready, 512);
         mbar_init(&bars->o_full, 1);
         mbar_init(&bars->o_free, 128);
         mbar_init(&bars->mma_done, 1);
         mbar_init(&bars->pow_ready, 64);
-        mbar_init(&bars->lo_ready, 128);
-        mbar_init(&bars->lo_free, 128);
         fence_barrier_init();
     }
     if (warp == 21) { tmem_alloc(&bars->tmem_base, 512); tmem_relinquish(); }
@@ -497,13 +560,10 @@ decay_out_kernel(const __grid_constant__ DecayPasses passes, const int n_passes,
     auto ac_wait = [&](int i) { return mma_wait(&bars->ac_full[i % C::NAC], (i / C::NAC) & 1, abort_flag); };
     auto u_wait = [&](int t) { return mbar_wait(&bars->u_done[t % C::NB], (t / C::NB) & 1, abort_flag); };
     auto s_wait = [&](int t) { return mbar_wait(&bars->s_full[t % C::NS], (t / C::NS) & 1, abort_flag); };
-    // the walk's chunks (step t is chunk t, or chunks - 1 - t backwards), and
-    // whether it reaches the end of its sequence and writes the state there
+    // the walk's chunks: step t is chunk t, or chunks - 1 - t backwards; the
+    // state is updated after each but the last
     auto chunks = [](const DecayWork& w) { return (w.len + 127) / 128; };
     auto token = [](const DecayWork& w, bool back, int t) { return 128 * (back ? (w.len + 127) / 128 - 1 - t : t); };
-    auto writes_state = [&](const DecayWork& w) { return passes.p[w.pass].last && (passes.p[w.pass].back ? w.off == 0 : w.rest <= sh.seg); };
-    // steps whose update of the state is needed
-    auto updates_of = [&](const DecayWork& w) { return max(0, chunks(w) - (writes_state(w) ? 0 : 1)); };
 
     // hi and lo of B w for the units [i0, i1) of this one of 256 threads
     auto split_units = [&](int t, int id, int i0, int i1, int rows, bool back, float w_scale, float l2) {
@@ -532,7 +592,7 @@ decay_out_kernel(const __grid_constant__ DecayPasses passes, const int n_passes,
             id /= n_passes;
             w.head = id % sh.heads;
             const Piece g = find_piece(cu, sh, sh.seg, id / sh.heads, status);
-            w.seq = g.seq;
+            w.seq = g.len > 0 ? g.seq : -1;
             w.begin = g.begin; w.len = g.len; w.off = g.off; w.rest = g.rest;
             return w;
         });
@@ -609,8 +669,7 @@ decay_out_kernel(const __grid_constant__ DecayPasses passes, const int n_passes,
         for (int k = 0; ok; ++k) {
             DecayWork w;
             if (!(ok = queue_get(&bars->queue, k, abort_flag, w)) || w.seq < 0) break;
-            const int n = warp_uniform(chunks(w)), updates = warp_uniform(updates_of(w));
-            if (n == 0) continue;
+            const int n = warp_uniform(chunks(w));
             if (!(ok = all(b_wait(s0) && ac_wait(2 * s0)))) break;
             issue_s(s0);
             for (int t = 0; t < n && ok; ++t) {
@@ -622,7 +681,7 @@ decay_out_kernel(const __grid_constant__ DecayPasses passes, const int n_passes,
                 }
                 // O1 = P C
                 if (!(ok = all((step == 0 || mma_wait(&bars->o_free, (step - 1) & 1, abort_flag)) && ac_wait(2 * step + 1) &&
-                               mma_wait(&bars->p_ready, step & 1, abort_flag))))
+                               mma_wait(&bars->p_ready[step % C::NS], (step / C::NS) & 1, abort_flag))))
                     break;
                 tc_fence_after();
                 if (elect_one()) {
@@ -643,11 +702,11 @@ decay_out_kernel(const __grid_constant__ DecayPasses passes, const int n_passes,
                                     desc_add(mn_major, C::X_OFF + kk * 2048), id_o, kk > 0);
                     }
                     mma_commit(&bars->o_full);
-                    if (t >= updates) mma_commit(&bars->u_done[step % C::NB]);
+                    if (t == n - 1) mma_commit(&bars->u_done[step % C::NB]);
                 }
                 __syncwarp();
                 // the scores of the next step and U of this one, as their inputs arrive
-                bool s_next = C::NS == 1 && t + 1 < n, u_next = t < updates;
+                bool s_next = C::NS == 1 && t + 1 < n, u_next = t + 1 < n;
                 const unsigned long long t0 = clock64();
                 while (s_next || u_next) {
                     if (s_next && all(mbar_test_wait(&bars->b_full[(step + 1) % C::NB], ((step + 1) / C::NB) & 1) &&
@@ -679,7 +738,7 @@ decay_out_kernel(const __grid_constant__ DecayPasses passes, const int n_passes,
                 }
             }
             s0 += n;
-            w0 += updates;
+            w0 += n - 1;
         }
         if (!ok) fail();
         if (elect_one()) mma_commit(&bars->mma_done);
@@ -712,7 +771,7 @@ decay_out_kernel(const __grid_constant__ DecayPasses passes, const int n_passes,
                 mbar_arrive(&bars->pow_ready);
             }
             if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bars->pow_ready, k & 1, abort_flag)))) break;
-            const int n = chunks(w), updates = updates_of(w);
+            const int n = chunks(w);
             for (int t = 0; t < n; ++t) {
                 const int step = s0 + t, rows = min(128, w.len - token(w, back, t));
                 if (rows < 128) {
@@ -760,8 +819,8 @@ decay_out_kernel(const __grid_constant__ DecayPasses passes, const int n_passes,
                 }
                 tmem_wait_st();
                 tc_fence_before();
-                mbar_arrive(&bars->p_ready);
-                if (t < updates) {
+                mbar_arrive(&bars->p_ready[step % C::NS]);
+                if (t + 1 < n) {
                     // the products that read the last step's lo part have finished
                     if (step > 0 && !__all_sync(0xffffffffu, u_wait(step - 1))) { ok = false; break; }
                     if (!split_units(step, tid, 0, C::UNITS_P, rows, back, ps.w_scale, l2)) { ok = false; break; }
@@ -818,7 +877,7 @@ decay_out_kernel(const __grid_constant__ DecayPasses passes, const int n_passes,
         // in registers: a row (TMEM lane) and half of its columns
         const int id = tid - 256, hf = id >> 7, row = id & 127, feat = row & (D - 1);
         const uint32_t tU = tbase + ((uint32_t)(32 * (warp & 3)) << 16) + C::U_COL + hf * (D / 2);
-        int s0 = 0, written = 0;                         // states written so far (d = 64: phases of the lo part's exchange)
+        int s0 = 0;
         bool ok = true;
         for (int k = 0; ok; ++k) {
             DecayWork w;
@@ -826,17 +885,10 @@ decay_out_kernel(const __grid_constant__ DecayPasses passes, const int n_passes,
             const DecayPass& ps = passes.p[w.pass];
             const bool back = ps.back;
             const float l2 = decay_log2(log_decay, w.head);
-            const int n = chunks(w), updates = updates_of(w);
-            const long long own = ((long long)w.seq * sh.heads + w.head) * D * D;
-            float* last = writes_state(w) ? ps.last + own : nullptr;
+            const int n = chunks(w);
             const float* x0;                             // the state before step 0, or null: zeros
-            if (back ? w.rest <= sh.seg : w.off == 0) x0 = ps.first ? ps.first + own : nullptr;
+            if (back ? w.rest <= sh.seg : w.off == 0) x0 = ps.first ? ps.first + ((long long)w.seq * sh.heads + w.head) * D * D : nullptr;
             else x0 = ps.border + ((long long)((back ? w.begin + sh.seg : w.begin) - sh.part) / sh.part * sh.heads + w.head) * D * D;
-            if (n == 0) {                                // an empty sequence: the state goes through
-                if (last)
-                    for (int e = id; e < D * D; e += 256) last[e] = x0 ? x0[e] : 0.f;
-                continue;
-            }
             float x[D / 2];
 #pragma unroll
             for (int c = 0; c < D / 2; ++c) x[c] = 0.f;
@@ -883,7 +935,6 @@ decay_out_kernel(const __grid_constant__ DecayPasses passes, const int n_passes,
                 } else {
                     // the walk before has left the bf16 state's place
                     if (step > 0 && !__all_sync(0xffffffffu, u_wait(step - 1))) { ok = false; break; }
-                    if (D == 64 && written > 0 && !__all_sync(0xffffffffu, mbar_wait(&bars->lo_free, (written - 1) & 1, abort_flag))) { ok = false; break; }
                 }
                 uint8_t* xr = sX + row * 128;
 #pragma unroll
@@ -897,35 +948,7 @@ decay_out_kernel(const __grid_constant__ DecayPasses passes, const int n_passes,
                 if (!__all_sync(0xffffffffu, s_wait(step))) { ok = false; break; }
                 fence_proxy_async_smem();
                 mbar_arrive(&bars->x_ready);
-                if (t < updates && !split_units(step, id, C::UNITS_P, C::UNITS, rows, back, ps.w_scale, l2)) { ok = false; break; }
-            }
-            if (ok && last) {
-                if (!(ok = update(n - 1))) break;
-                if (D == 64) {
-                    // the walk's products have finished: the bf16 state's place takes the lo part to the hi part's threads
-                    float* half = reinterpret_cast<float*>(sX) + hf * 32 * 64 + feat;
-                    if (row >= 64) {
-#pragma unroll
-                        for (int c = 0; c < 32; ++c) half[c * 64] = x[c];
-                        mbar_arrive(&bars->lo_ready);
-                    } else {
-                        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bars->lo_ready, written & 1, abort_flag)))) break;
-#pragma unroll
-                        for (int c = 0; c < 32; ++c) x[c] += half[c * 64];
-                        mbar_arrive(&bars->lo_free);
-                    }
-                    ++written;
-                }
-                if (row < D) {
-                    if (ps.trans) {
-#pragma unroll
-                        for (int c = 0; c < D / 2; ++c) last[(long long)(hf * (D / 2) + c) * D + feat] = x[c];
-                    } else {
-                        const QuadRows at((long long)feat * D + hf * (D / 2));
-#pragma unroll
-                        for (int c = 0; c < D / 2; c += 32) store_rows(last + c, at, *reinterpret_cast<float(*)[32]>(&x[c]));
-                    }
-                }
+                if (t + 1 < n && !split_units(step, id, C::UNITS_P, C::UNITS, rows, back, ps.w_scale, l2)) { ok = false; break; }
             }
             s0 += n;
         }
@@ -974,11 +997,12 @@ static DecayShape decay_shape(int n_seq, int total, int heads, int d, int passes
     };
     for (int pieces = 1; pieces <= 12; ++pieces) consider(pieces);
     for (int rounds = 1; rounds <= 4; ++rounds) consider((long long)(148 * rounds / walks));
-    // parts of a segment: rounds of CTAs, one chunk for a start and end
-    const double cuts = n_seq == 1 ? (double)((chunks + best - 1) / best - 1) : best < longest ? (double)chunks / best : 0.0;
+    // parts of a segment: at most 12 chunks, by rounds of CTAs and one chunk for a start and end
+    const double cuts = std::max(1.0, (double)chunks / best);
     long long part = best, k = 1;
     best_cost = 1e300;
-    for (int i = 1; i <= 4 && cuts > 0; ++i) {
+    const long long least = (best + 11) / 12;
+    for (long long i = least; i < least + 4 && i <= best; ++i) {
         const long long len = (best + i - 1) / i;
         const double cost = std::ceil(cuts * i * sums / 148) * (len + 1.0);
         if (cost < best_cost) { best_cost = cost; part = len; k = i; }
@@ -1005,7 +1029,7 @@ static cudaError_t launch_decay(const DecayArgs& a, const DecayShape& sh, const 
     const unsigned parts = (unsigned)(((long long)sh.total / sh.part + sh.n_seq) * a.heads);
     cudaError_t e = cudaFuncSetAttribute(decay_out_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, DecOutCfg<D>::SMEM);
     if (e != cudaSuccess) return e;
-    if (a.total > sh.seg) {                              // some sequence may have several segments
+    if (a.total > sh.seg || st.last[0] || st.last[1]) {  // some sequence may have several segments, or states are wanted
         e = cudaFuncSetAttribute(decay_state_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, DecStateCfg<D>::SMEM);
         if (e != cudaSuccess) return e;
         decay_state_kernel<D><<<parts * kinds, DecStateCfg<D>::THREADS, DecStateCfg<D>::SMEM, stream>>>(st, kinds, sh, a.cu, a.log_decay, a.status);
@@ -1032,14 +1056,15 @@ cudaError_t launch_decay_fwd(const DecayArgs& a, cudaStream_t stream) {
     p.out = static_cast<__nv_bfloat16*>(a.out.p);
     p.out_stride = a.out.stride;
     p.first = a.state_in;
-    p.last = a.state_out;
     p.border = border;
     p.w_scale = 1.f;
     p.p_scale = p.s_scale = a.scale;
     st.border[0] = border;
+    st.last[0] = a.state_out;
     st.w_scale[0] = 1.f;
     DecayScanArgs sc{};
     sc.border[0] = border;
+    sc.last[0] = a.state_out;
     sc.first[0] = a.state_in;
     return a.d == 128 ? launch_decay<128>(a, sh, ps, 1, st, sc, 1, stream) : launch_decay<64>(a, sh, ps, 1, st, sc, 1, stream);
 }
@@ -1072,12 +1097,12 @@ cudaError_t launch_decay_bwd(const DecayArgs& a, cudaStream_t stream) {
     ps.p[0] = pass(mg, mv, mk, a.dq, false, true);
     ps.p[1] = pass(mv, mg, mq, a.dk, true, true);
     ps.p[2] = pass(mk, mq, mg, a.dv, true, false);
-    ps.p[2].last = a.dstate_in;
     st.w_scale[0] = 1.f;
     st.w_scale[1] = a.scale;
     DecayScanArgs sc{};
     sc.first[0] = a.state_in;
     sc.first[1] = a.dstate_out;
+    st.last[1] = sc.last[1] = a.dstate_in;
     for (int i = 0; i < 2; ++i) st.border[i] = sc.border[i] = border[i], st.back[i] = sc.back[i] = i;
     return a.d == 128 ? launch_decay<128>(a, sh, ps, 3, st, sc, 2, stream) : launch_decay<64>(a, sh, ps, 3, st, sc, 2, stream);
 }
