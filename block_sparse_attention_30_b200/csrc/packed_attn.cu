@@ -328,8 +328,11 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
             const bool idle = !__any_sync(0xffffffffu, valid);
             for (int t = f; t < n; ++t) {
                 const int key0 = 128 * (w.hi - 1 - t);
+                if (!__all_sync(0xffffffffu, mbar_wait(&bars->s_full[x], (steps + t - f) & 1, abort_flag))) { ok = false; break; }
                 if (key0 + 128 > w.nk) {
-                    // the sequence's last, partial block (step 0): zero V's rows behind it
+                    // the sequence's last, partial block (step 0): zero V's rows behind it.
+                    // (After its scores: a tile that sat out the work before may be a
+                    // round of the ring ahead, where the phase would be another one's.)
                     const int i = r0 + 2 * t + 1;
                     if (!__all_sync(0xffffffffu, mbar_wait(&bars->full[i % C::NST], (i / C::NST) & 1, abort_flag))) { ok = false; break; }
                     uint8_t* v = ring + (i % C::NST) * C::TILE;
@@ -338,7 +341,6 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
                         *reinterpret_cast<uint4*>(v + (u % C::NCH) * C::CHUNK + z0 * 128 + (u / C::NCH) * 16) = make_uint4(0, 0, 0, 0);
                     fence_proxy_async_smem();
                 }
-                if (!__all_sync(0xffffffffu, mbar_wait(&bars->s_full[x], (steps + t - f) & 1, abort_flag))) { ok = false; break; }
                 if (idle) {
                     mbar_arrive(&bars->p_half[x]);
                     mbar_arrive(&bars->p_full[x]);

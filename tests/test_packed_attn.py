@@ -202,3 +202,21 @@ def test_forward_on_another_stream_and_repeatable(ops):
     ops.vsa_packed_attn_fwd(q, k, v, cu, cu, out, ws, stream=s)
     s.synchronize()
     assert torch.equal(out, want[0])
+
+
+def test_forward_repeats_its_bits_with_many_short_works_per_cta(ops):
+    """Sequences whose last pair of tiles has rows in one tile only, with longer ones around them: a tile that sits one
+    piece of work out must not touch the other's operands.  (A fault of timing: the same call a few hundred times.)"""
+    lens = [340, 22, 552, 76, 395, 207, 1056]
+    q, k, v = randn(1, sum(lens), 24, 128), randn(2, sum(lens), 8, 128), randn(3, sum(lens), 8, 128)
+    cu = cu_of(lens).cuda()
+    ws = workspace(ops, q, k, cu)
+    want = forward(ops, q, k, v, cu, cu, ws=ws)
+    r = attention(q.cpu(), k.cpu(), v.cpu(), cu.cpu(), cu.cpu(), True)
+    check(want[0], r["out"], r["out_tol"], "out")
+    out, lse = torch.empty_like(want[0]), torch.empty_like(want[2])
+    differ = torch.zeros((), dtype=torch.bool, device="cuda")
+    for _ in range(600):
+        ops.vsa_packed_attn_fwd(q, k, v, cu, cu, out, ws, lse=lse)
+        differ |= (out != want[0]).any() | (lse != want[2]).any()
+    assert not differ and ops.vsa_device_status(ws) == 0
