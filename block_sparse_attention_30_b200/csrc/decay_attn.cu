@@ -149,7 +149,9 @@ struct DecStateCfg {
     static constexpr int LO_OFF = ZERO_OFF + (D == 64 ? TILE : 0);   // mid and lo of even and odd steps
     static constexpr int BAR_OFF = LO_OFF + 4 * TILE;
     static constexpr int SMEM = BAR_OFF + 512;
-    static constexpr int THREADS = 512;                  // 8 split warps, 4 output warps, loads, MMAs, queue
+    static constexpr int GROUP = 8;                      // steps that one TMEM accumulator sums
+    static constexpr int THREADS = 512;                  // warpgroups: 2 split, sums, loads and MMAs and queue; 128 registers a thread
+    static constexpr int REG_SPLIT = 104, REG_SUM = 208, REG_LOAD = 96;      // 2 * 104 + 208 + 96 = 4 * 128
 };
 static_assert(DecStateCfg<128>::SMEM <= 232448, "shared memory");
 
@@ -180,15 +182,14 @@ struct DecayStateArgs {
 // grid (kinds of state x parts x heads), from a queue per CTA.  Forward in time
 // the sum of part p goes to the border behind it, backwards that of part p + 1;
 // the walk's last part's to `last`, and without that the parts of its last
-// segment are not needed.  Steps of 64 tokens are counted on from part to part;
-// a part's sum lies in one of two TMEM accumulators (d = 128: pairs of them), so
-// that it is stored while the next part's is formed.
+// segment are not needed.  Steps of 64 tokens are counted on from part to part.
 //
-// The states leave the library, so the sums are good to fp32: the weighted
-// operand is split into three bf16 parts (all 24 bits), and the products of the
-// two small ones have an accumulator of their own.  The tensor cores' fp32
-// accumulation loses about 6e-9 of a sum per step of 16 tokens (measured), which
-// is why a part has 12 chunks at most: 6e-7.
+// Where states leave the library (`last`) the sums are good to fp32: the
+// weighted operand is split into three bf16 parts (all 24 bits) instead of two,
+// and the products of the small ones have an accumulator of their own.  The
+// tensor cores' accumulation cuts off (a sum over 88 products of 16 tokens came
+// out 1.4e-6 off), so that one accumulator sums 8 steps and fp32 registers sum
+// those, one of two accumulators being read while the other is filled.
 template <int D>
 __global__ void __launch_bounds__(DecStateCfg<D>::THREADS, 1)
 decay_state_kernel(const __grid_constant__ DecayStateArgs args, const int kinds, const DecayShape sh,
@@ -229,7 +230,9 @@ decay_state_kernel(const __grid_constant__ DecayStateArgs args, const int kinds,
     // is what this one read last, and still in L2
     auto token = [&](const DecayPart& w, int t) { return 64 * (args.back[w.kind] ? t : (w.len + 63) / 64 - 1 - t); };
 
-    if (warp == 14) {
+    if (warp >= 12) {
+      reg_dec<C::REG_LOAD>();
+      if (warp == 14) {
         const bool ok = queue_produce<true>(&bars->queue, abort_flag, [&](int id) {
             DecayPart w{};
             w.kind = id % kinds;
@@ -243,7 +246,7 @@ decay_state_kernel(const __grid_constant__ DecayStateArgs args, const int kinds,
             return w;
         });
         if (!ok) fail();
-    } else if (warp == 12) {
+      } else if (warp == 12) {
         // -------------------------------------------------------------- loads
         int s0 = 0, issued = 0;
         bool ok = true;
@@ -272,21 +275,23 @@ decay_state_kernel(const __grid_constant__ DecayStateArgs args, const int kinds,
         if (!ok) fail();
         if (lane == 0 && *abort_flag)                    // every load must land before the shared memory is given up
             for (int i = max(0, issued - C::NST); i < issued; ++i) wait_noabort(&bars->full[i % C::NST], (i / C::NST) & 1);
-    } else if (warp == 13) {
+      } else if (warp == 13) {
         // --------------------------------------------------------------- MMAs
         constexpr uint32_t id_x = idesc_bf16_f32(128, D, true, true);
         const uint32_t base = smem_u32(smem);
         const uint64_t mn_major = smem_desc_sw128(base, C::CHUNK, 1024);
         auto wait = [&](uint64_t* bar, int parity) { return __all_sync(0xffffffffu, mma_wait(bar, parity, abort_flag)) != 0; };
-        int s0 = 0, last_step = -1;
+        int s0 = 0, group = -1, last_step = -1;
         bool ok = true;
         for (int k = 0; ok; ++k) {
             DecayPart w;
             if (!(ok = queue_get(&bars->queue, k, abort_flag, w)) || w.seq < 0) break;
             const int n = warp_uniform(steps(w));
-            const uint32_t acc = tbase + 128 * (k & 1);
-            if (k >= 2 && !(ok = wait(&bars->sum_free[k & 1], (k / 2 - 1) & 1))) break;
+            const bool three = args.last[warp_uniform(w.kind)] != nullptr;
             for (int t = 0; t < n; ++t) {
+                const bool fresh = t % C::GROUP == 0;
+                if (fresh && ++group >= 2 && !(ok = wait(&bars->sum_free[group & 1], (group / 2 - 1) & 1))) break;
+                const uint32_t acc = tbase + 128 * (group & 1);
                 const int step = s0 + t, at = (step % C::NST) * 2 * C::TILE, mid_at = C::LO_OFF + (step & 1) * 2 * C::TILE;
                 const int lo_at = mid_at + C::TILE;
                 const uint64_t c = desc_add(mn_major, at + C::TILE);
@@ -300,12 +305,12 @@ decay_state_kernel(const __grid_constant__ DecayStateArgs args, const int kinds,
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk) {     // 16 tokens per MMA
                         const uint64_t cd = desc_add(c, kk * 2048);
-                        mma_bf16_ss(acc, desc_add(hi, kk * 2048), cd, id_x, t > 0 || kk > 0);
-                        if (D == 128) mma_bf16_ss(acc + 256, desc_add(mid, kk * 2048), cd, id_x, t > 0 || kk > 0);
-                        mma_bf16_ss(D == 128 ? acc + 256 : acc, desc_add(lo, kk * 2048), cd, id_x, 1);
+                        mma_bf16_ss(acc, desc_add(hi, kk * 2048), cd, id_x, !fresh || kk > 0);
+                        if (D == 128) mma_bf16_ss(acc + 256, desc_add(mid, kk * 2048), cd, id_x, !fresh || kk > 0);
+                        if (three) mma_bf16_ss(D == 128 ? acc + 256 : acc, desc_add(lo, kk * 2048), cd, id_x, 1);
                     }
                     mma_commit(&bars->done[step % C::NST]);
-                    if (t == n - 1) mma_commit(&bars->sum_full[k & 1]);
+                    if (t == n - 1 || t % C::GROUP == C::GROUP - 1) mma_commit(&bars->sum_full[group & 1]);
                 }
                 __syncwarp();
                 last_step = step;
@@ -315,7 +320,9 @@ decay_state_kernel(const __grid_constant__ DecayStateArgs args, const int kinds,
         if (!ok) fail();
         // products in flight have to finish before the CTA leaves
         if (last_step >= 0) wait_noabort(&bars->done[last_step % C::NST], (last_step / C::NST) & 1);
+      }
     } else if (warp < 8) {
+        reg_dec<C::REG_SPLIT>();
         // -------------------------------------------------------------- split
         int s0 = 0;
         bool ok = true;
@@ -323,7 +330,7 @@ decay_state_kernel(const __grid_constant__ DecayStateArgs args, const int kinds,
             DecayPart w;
             if (!(ok = queue_get(&bars->queue, k, abort_flag, w)) || w.seq < 0) break;
             const float l2 = decay_log2(log_decay, w.head), w0 = args.w_scale[w.kind];
-            const bool back = args.back[w.kind];
+            const bool back = args.back[w.kind], three = args.last[w.kind] != nullptr;
             const int n = steps(w);
             for (int t = 0; t < n; ++t) {
                 const int step = s0 + t, tok = token(w, t);
@@ -335,14 +342,16 @@ decay_state_kernel(const __grid_constant__ DecayStateArgs args, const int kinds,
                 for (int u = tid; u < C::TILE / 16; u += 256) {
                     const int r = tok + (u & 511) / 8;   // token of the part
                     uint4 x = *reinterpret_cast<const uint4*>(st + u * 16), mid, lo;
-                    split8(x, w0 * ex2((float)(back ? r + 1 : w.len - 1 - r) * l2), mid, lo);
+                    const float wr = w0 * ex2((float)(back ? r + 1 : w.len - 1 - r) * l2);
+                    if (three) split8(x, wr, mid, lo);
+                    else split8(x, wr, mid);
                     if (r >= w.len) {                    // another sequence's rows
                         x = mid = lo = make_uint4(0, 0, 0, 0);
                         *reinterpret_cast<uint4*>(st + C::TILE + u * 16) = x;
                     }
                     *reinterpret_cast<uint4*>(st + u * 16) = x;
                     *reinterpret_cast<uint4*>(sl + u * 16) = mid;
-                    *reinterpret_cast<uint4*>(sl + C::TILE + u * 16) = lo;
+                    if (three) *reinterpret_cast<uint4*>(sl + C::TILE + u * 16) = lo;
                 }
                 fence_proxy_async_smem();
                 mbar_arrive(&bars->ready[step & 1]);
@@ -350,56 +359,67 @@ decay_state_kernel(const __grid_constant__ DecayStateArgs args, const int kinds,
             s0 += n;
         }
         if (!ok) fail();
-    } else if (warp < 12) {
-        // ------------------------------------------------------------ outputs
+    } else {
+        reg_inc<C::REG_SUM>();
+        // --------------------------------------------------------------- sums
         // a TMEM lane per thread: a feature of b (d = 64: of hi, and of mid and
         // lo, whose sums meet in shared memory)
         const int row = 32 * (warp & 3) + lane, feat = row & (D - 1);
         __shared__ float half[D == 64 ? 32 * 64 : 1];
-        int exchanges = 0;
+        int group = 0, exchanges = 0;
         bool ok = true;
         for (int k = 0; ok; ++k) {
             DecayPart w;
             if (!(ok = queue_get(&bars->queue, k, abort_flag, w)) || w.seq < 0) break;
-            if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bars->sum_full[k & 1], (k / 2) & 1, abort_flag)))) break;
-            tc_fence_after();
-            const bool back = args.back[w.kind];
-            const long long slot = (back ? w.begin - sh.part : w.begin) / sh.part;
+            float x[D];
+#pragma unroll
+            for (int c = 0; c < D; ++c) x[c] = 0.f;
+            const int n = steps(w);
+            for (int t = 0; t < n; t += C::GROUP, ++group) {
+                if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bars->sum_full[group & 1], (group / 2) & 1, abort_flag)))) break;
+                tc_fence_after();
+                const uint32_t acc = tbase + 128 * (group & 1) + ((uint32_t)(32 * (warp & 3)) << 16);
+#pragma unroll
+                for (int c = 0; c < D; c += 32) {
+                    float y[32];
+                    tmem_ld_32x32b_x32(acc + c, y);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) x[c + e] += y[e];
+                    if (D == 128) {
+                        tmem_ld_32x32b_x32(acc + 256 + c, y);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) x[c + e] += y[e];
+                    }
+                }
+                tc_fence_before();
+                mbar_arrive(&bars->sum_free[group & 1]);
+            }
+            if (!ok) break;
+            const long long slot = (args.back[w.kind] ? w.begin - sh.part : w.begin) / sh.part;
             float* dst = w.ends ? args.last[w.kind] + ((long long)w.seq * sh.heads + w.head) * D * D
                                 : args.border[w.kind] + (slot * sh.heads + w.head) * D * D;
             const QuadRows at((long long)feat * D);
-#pragma unroll 1
-            for (int c = 0; c < D && ok; c += 32) {
-                float x[32];
-                const uint32_t acc = tbase + 128 * (k & 1) + ((uint32_t)(32 * (warp & 3)) << 16) + c;
-                tmem_ld_32x32b_x32(acc, x);
-                tmem_wait_ld();
-                if (D == 128) {
-                    float y[32];
-                    tmem_ld_32x32b_x32(acc + 256, y);
-                    tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) x[e] += y[e];
-                }
-                if (c + 32 == D) {
-                    tc_fence_before();
-                    mbar_arrive(&bars->sum_free[k & 1]);
-                }
+            for (int c = 0; c < D; c += 32) {
+                float(&v)[32] = *reinterpret_cast<float(*)[32]>(&x[c]);
                 if (D == 64) {
+                    if (!ok) break;
                     if (row >= 64) {
                         if (exchanges > 0 && !(ok = __all_sync(0xffffffffu, mbar_wait(&bars->half_free, (exchanges - 1) & 1, abort_flag)))) break;
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) half[e * 64 + feat] = x[e];
+                        for (int e = 0; e < 32; ++e) half[e * 64 + feat] = v[e];
                         mbar_arrive(&bars->half_full);
                     } else {
                         if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bars->half_full, exchanges & 1, abort_flag)))) break;
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) x[e] += half[e * 64 + feat];
+                        for (int e = 0; e < 32; ++e) v[e] += half[e * 64 + feat];
                         mbar_arrive(&bars->half_free);
                     }
                     ++exchanges;
                 }
-                if (row < D) store_rows(dst + c, at, x);
+                if (row < D) store_rows(dst + c, at, v);
             }
         }
         if (!ok) fail();
@@ -997,12 +1017,11 @@ static DecayShape decay_shape(int n_seq, int total, int heads, int d, int passes
     };
     for (int pieces = 1; pieces <= 12; ++pieces) consider(pieces);
     for (int rounds = 1; rounds <= 4; ++rounds) consider((long long)(148 * rounds / walks));
-    // parts of a segment: at most 12 chunks, by rounds of CTAs and one chunk for a start and end
+    // parts of a segment: rounds of CTAs, one chunk for a start and end
     const double cuts = std::max(1.0, (double)chunks / best);
     long long part = best, k = 1;
     best_cost = 1e300;
-    const long long least = (best + 11) / 12;
-    for (long long i = least; i < least + 4 && i <= best; ++i) {
+    for (long long i = 1; i <= 4 && i <= best; ++i) {
         const long long len = (best + i - 1) / i;
         const double cost = std::ceil(cuts * i * sums / 148) * (len + 1.0);
         if (cost < best_cost) { best_cost = cost; part = len; k = i; }
