@@ -167,21 +167,36 @@ __device__ __forceinline__ void zero_rows(uint8_t* tile, int from, int tid) {
 }
 
 // Half a row (D/2 features) of an accumulator, times `scale`, as bf16; zeros
-// where the accumulator was never written.
+// where the accumulator was never written.  `rows`: where the quad's rows start.
 template <int D>
-__device__ __forceinline__ void store_grad(uint32_t acc, bool written, float scale, __nv_bfloat16* dst, bool valid) {
+__device__ __forceinline__ void store_grad(uint32_t acc, bool written, float scale, __nv_bfloat16* dst, const QuadRows& rows) {
 #pragma unroll
     for (int c = 0; c < D / 2; c += 32) {
         float o[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) o[e] = 0.f;
         if (written) { tmem_ld_32x32b_x32(acc + c, o); tmem_wait_ld(); }
-        if (valid) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 8)
-                *reinterpret_cast<uint4*>(dst + c + e) =
-                    make_uint4(pack_bf16x2(o[e] * scale, o[e + 1] * scale), pack_bf16x2(o[e + 2] * scale, o[e + 3] * scale),
-                               pack_bf16x2(o[e + 4] * scale, o[e + 5] * scale), pack_bf16x2(o[e + 6] * scale, o[e + 7] * scale));
+        for (int e = 0; e < 32; ++e) o[e] *= scale;
+        store_rows(dst + c, rows, o);
+    }
+}
+
+// A cluster's CTAs sum the blocks' shares of one accumulator each; this puts
+// half a row of one (fp32, 16-byte units swizzled against bank conflicts) into
+// the CTA's own shared memory for the others.
+template <int D>
+__device__ __forceinline__ void share_grad(uint32_t acc, bool written, float* image, int row, int hf) {
+#pragma unroll
+    for (int c = 0; c < D / 2; c += 32) {
+        float o[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = 0.f;
+        if (written) { tmem_ld_32x32b_x32(acc + c, o); tmem_wait_ld(); }
+#pragma unroll
+        for (int e = 0; e < 32; e += 4) {
+            const int unit = (hf * (D / 2) + c + e) / 4;
+            *reinterpret_cast<float4*>(image + row * D + (unit ^ (row & 7)) * 4) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
         }
     }
 }
@@ -205,10 +220,10 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
     const int group = sh.heads_q / sh.heads_kv;
     const int kvh = blockIdx.x % sh.heads_kv;
     // the last tiles of a sequence see the most keys: they start first
-    const SeqTile at = find_tile(cu_q, sh.n_seq, sh.total_q, tok_per_tile, tiles - 1 - blockIdx.x / sh.heads_kv, status);
-    if (at.seq < 0) return;
-    const SeqRange qr = seq_range(cu_q, at.seq, sh.total_q, status), kr = seq_range(cu_k, at.seq, sh.total_k, status);
-    const int tok0 = at.tile * tok_per_tile;
+    const SeqTile tile = find_tile(cu_q, sh.n_seq, sh.total_q, tok_per_tile, tiles - 1 - blockIdx.x / sh.heads_kv, status);
+    if (tile.seq < 0) return;
+    const SeqRange qr = seq_range(cu_q, tile.seq, sh.total_q, status), kr = seq_range(cu_k, tile.seq, sh.total_k, status);
+    const int tok0 = tile.tile * tok_per_tile;
     const int n = warp_uniform((seen_keys(min(tok0 + tok_per_tile, qr.len) - 1, qr.len, kr.len, causal) + 127) / 128);   // key blocks
     uint8_t* sQ = smem;
     uint8_t* sG = smem + C::TILE;
@@ -348,8 +363,8 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
         if (!ok) fail();
         if (ok) {
             tc_fence_after();
-            store_grad<D>(tAcc + lane_base + hf * (D / 2), n > 0, scale,
-                          dq + ((long long)qr.begin + tok) * dq_stride + (long long)(kvh * group + r % group) * D + hf * (D / 2), valid);
+            const QuadRows at(valid ? ((long long)qr.begin + tok) * dq_stride + (long long)(kvh * group + r % group) * D : -1);
+            store_grad<D>(tAcc + lane_base + hf * (D / 2), n > 0, scale, dq + hf * (D / 2), at);
         }
     }
     tc_fence_before();
@@ -363,7 +378,7 @@ template <int D>
 __global__ void __launch_bounds__(PackBwdCfg<D>::THREADS, 1)
 packed_dkdv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                    const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mg, const PackedShape sh,
-                   const int tok_per_tile, const int32_t* __restrict__ cu_q, const int32_t* __restrict__ cu_k,
+                   const int tok_per_tile, const int shares, const int32_t* __restrict__ cu_q, const int32_t* __restrict__ cu_k,
                    const int causal, const float scale_log2, const float scale, const float2* __restrict__ terms,
                    __nv_bfloat16* __restrict__ dk, const long long dk_stride, __nv_bfloat16* __restrict__ dv,
                    const long long dv_stride, int* status) {
@@ -375,17 +390,21 @@ packed_dkdv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
     }
     const int tid = threadIdx.x, warp = warp_uniform(tid >> 5), lane = tid & 31;
     const int group = sh.heads_q / sh.heads_kv;
-    const int kvh = blockIdx.x % sh.heads_kv;
+    // a cluster of `shares` CTAs per tile of keys, each with its share of the row blocks
+    const int share = blockIdx.x % shares, item = blockIdx.x / shares;
+    const int kvh = item % sh.heads_kv;
     // the first tiles of a sequence are seen by the most queries: they start first
-    const SeqTile at = find_tile(cu_k, sh.n_seq, sh.total_k, 128, blockIdx.x / sh.heads_kv, status);
-    if (at.seq < 0) return;
-    const SeqRange qr = seq_range(cu_q, at.seq, sh.total_q, status), kr = seq_range(cu_k, at.seq, sh.total_k, status);
-    const int key0 = 128 * at.tile;
+    const SeqTile tile = find_tile(cu_k, sh.n_seq, sh.total_k, 128, item / sh.heads_kv, status);
+    if (tile.seq < 0) return;                            // the whole cluster
+    const SeqRange qr = seq_range(cu_q, tile.seq, sh.total_q, status), kr = seq_range(cu_k, tile.seq, sh.total_k, status);
+    const int key0 = 128 * tile.tile;
     const int rows = tok_per_tile * group;               // rows of a block in use
     // first query token that sees key0, and the blocks from its on
     const int tok_first = causal ? max(0, key0 + qr.len - kr.len) : 0;
-    const int b0 = tok_first / tok_per_tile;
-    const int n = warp_uniform(max(0, (qr.len + tok_per_tile - 1) / tok_per_tile - b0));
+    const int all = max(0, (qr.len + tok_per_tile - 1) / tok_per_tile - tok_first / tok_per_tile);
+    const int per = (all + shares - 1) / shares;
+    const int b0 = tok_first / tok_per_tile + min(all, share * per);
+    const int n = warp_uniform(min(per, all - min(all, share * per)));
     uint8_t* sK = smem;
     uint8_t* sV = smem + C::TILE;
     uint8_t* sQ = smem + 2 * C::TILE;                    // 2 slots
@@ -571,11 +590,39 @@ packed_dkdv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
         if (!ok) fail();
         if (ok) {
             tc_fence_after();
-            const bool valid = key < kr.len;
-            const long long row = (long long)kr.begin + key;
-            store_grad<D>(tDV + lane_base + hf * (D / 2), n > 0, 1.f, dv + row * dv_stride + (long long)kvh * D + hf * (D / 2), valid);
-            store_grad<D>(tDK + lane_base + hf * (D / 2), n > 0, scale, dk + row * dk_stride + (long long)kvh * D + hf * (D / 2), valid);
+            if (shares == 1) {
+                const long long row = (long long)kr.begin + key;
+                const QuadRows at_v(key < kr.len ? row * dv_stride + (long long)kvh * D : -1);
+                const QuadRows at_k(key < kr.len ? row * dk_stride + (long long)kvh * D : -1);
+                store_grad<D>(tDV + lane_base + hf * (D / 2), n > 0, 1.f, dv + hf * (D / 2), at_v);
+                store_grad<D>(tDK + lane_base + hf * (D / 2), n > 0, scale, dk + hf * (D / 2), at_k);
+            } else {
+                // every product has finished: the operands' places hold the CTA's sums for the cluster
+                share_grad<D>(tDV + lane_base + hf * (D / 2), n > 0, reinterpret_cast<float*>(smem), r, hf);
+                share_grad<D>(tDK + lane_base + hf * (D / 2), n > 0, reinterpret_cast<float*>(smem) + 128 * D, r, hf);
+            }
         }
+    }
+    if (shares > 1) {
+        // each CTA adds up its part of the rows, share after share (a fixed order)
+        __syncwarp();
+        cluster_sync();
+        const int count = 128 / shares, row0 = share * count;
+        for (int u = tid; u < 2 * count * (D / 4); u += C::THREADS) {
+            const int unit = u % (D / 4), row = row0 + u / (D / 4) % count, which = u / (D / 4) / count;
+            const float* p = reinterpret_cast<const float*>(smem) + which * 128 * D + row * D + (unit ^ (row & 7)) * 4;
+            float4 sum = cluster_load(p, 0);
+            for (int x = 1; x < shares; ++x) {
+                const float4 y = cluster_load(p, x);
+                sum.x += y.x; sum.y += y.y; sum.z += y.z; sum.w += y.w;
+            }
+            if (key0 + row >= kr.len) continue;
+            const float f = which ? scale : 1.f;
+            __nv_bfloat16* dst = (which ? dk + ((long long)kr.begin + key0 + row) * dk_stride : dv + ((long long)kr.begin + key0 + row) * dv_stride) +
+                                 (long long)kvh * D + unit * 4;
+            *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(sum.x * f, sum.y * f), pack_bf16x2(sum.z * f, sum.w * f));
+        }
+        cluster_sync();                                  // the others have read this CTA's sums
     }
     tc_fence_before();
     __syncthreads();
@@ -584,9 +631,30 @@ packed_dkdv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
 }
 
 // --------------------------------------------------------------------- launch
+static long long key_items(const PackedShape& s) { return ((long long)s.total_k / 128 + s.n_seq) * s.heads_kv; }
+
+// CTAs that share a tile of keys in dK/dV: as many as make its rounds shortest,
+// in units of one row block (1.2 us), 4 of them for a CTA's start and end and 2
+// for adding up.  A tile's longest chain of blocks (all rows of a sequence, 2.5
+// times the average one at most) bounds the time from below: few kv heads and a
+// large group make long chains and few of them.  Packed training batch (4128
+// tokens, 16 heads on 4, d 64): 1 share 94 us, 4 shares 44 us.
+static int key_shares(const PackedShape& s, int causal) {
+    const double per_seq = (double)s.total_q / s.n_seq / (128 / s.group());
+    const double longest = std::min(s.n_seq == 1 ? 1.0 : 2.5, (double)s.n_seq) * per_seq, mean = causal ? 0.5 * per_seq : per_seq;
+    const double items = (double)key_items(s);
+    int best = 1;
+    double best_cost = 1e300;
+    for (int n = 1; n <= 8; n *= 2) {
+        const double cost = std::max(std::max(1.0, items * n / 148) * (mean / n + 4), longest / n + 4) + (n > 1 ? 2 : 0);
+        if (cost < best_cost) { best_cost = cost; best = n; }
+    }
+    return best;
+}
+
 long long packed_bwd_work_items(const PackedShape& s) {
-    const long long q = (long long)s.total_q / (128 / s.group()) + s.n_seq, k = (long long)s.total_k / 128 + s.n_seq;
-    return std::max(std::max(q, k) * s.heads_kv, ((long long)s.total_q * s.heads_q * s.d + 2047) / 2048);
+    const long long q = (long long)s.total_q / (128 / s.group()) + s.n_seq;
+    return std::max(std::max(q * s.heads_kv, 8 * key_items(s)), ((long long)s.total_q * s.heads_q * s.d + 2047) / 2048);
 }
 
 size_t packed_bwd_scratch_bytes(const PackedShape& s) {
@@ -625,11 +693,10 @@ static cudaError_t launch_packed_bwd_impl(const PackedArgs& a, cudaStream_t stre
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
     if (s.total_k) {
-        const int tiles = s.total_k / 128 + s.n_seq;
-        packed_dkdv_kernel<D><<<(unsigned)(tiles * s.heads_kv), C::THREADS, C::SMEM, stream>>>(
-            mq, mk, mv, mg, s, tok, a.cu_q, a.cu_k, a.causal, scale_log2, scale, terms,
-            static_cast<__nv_bfloat16*>(a.dk.p), a.dk.stride, static_cast<__nv_bfloat16*>(a.dv.p), a.dv.stride, a.status);
-        e = cudaGetLastError();
+        const int shares = key_shares(s, a.causal);
+        e = launch_clusters(packed_dkdv_kernel<D>, shares, dim3((unsigned)(key_items(s) * shares)), C::THREADS, C::SMEM, stream,
+                            mq, mk, mv, mg, s, tok, shares, a.cu_q, a.cu_k, a.causal, scale_log2, scale, terms,
+                            static_cast<__nv_bfloat16*>(a.dk.p), a.dk.stride, static_cast<__nv_bfloat16*>(a.dv.p), a.dv.stride, a.status);
     }
     return e;
 }

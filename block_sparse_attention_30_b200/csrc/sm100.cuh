@@ -153,6 +153,27 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
 __device__ __forceinline__ void grid_dependents_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// --------------------------------------------------------------------- clusters
+
+// Every thread of the cluster has arrived, and what each wrote before is
+// visible to all (all threads of all CTAs).
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// 16 bytes at `local`'s place in the shared memory of the cluster's CTA `rank`.
+__device__ __forceinline__ float4 cluster_load(const void* local, uint32_t rank) {
+    float4 v;
+    asm volatile(
+        "{\n\t.reg .b32 a;\n\t"
+        "mapa.shared::cluster.u32 a, %4, %5;\n\t"
+        "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n\t}"
+        : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+        : "r"(smem_u32(local)), "r"(rank)
+        : "memory");
+    return v;
+}
+
 // ------------------------------------------------------ cluster launch control
 
 // Ask for a CTA of this grid that has not started yet: 16 bytes of answer in
