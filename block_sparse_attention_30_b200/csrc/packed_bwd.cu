@@ -12,7 +12,8 @@
 //   row_terms_kernel  (lse, D) of every packed row, D from the forward's fp32
 //                  output (the bf16 one's rounding would enter dQ as
 //                  -dD sum_j P_j k_j, which does not shrink with dQ when the
-//                  keys share a large common component);
+//                  keys share a large common component); rows whose keys are
+//                  all in one block get a better D in the next kernel;
 //   dq_kernel      one CTA per 128 rows of one kv head ((token, head of the
 //                  group) pairs, as in the forward), walking its key blocks:
 //                  S = Q K^T, dP = dO V^T, dQ += dS K;
@@ -92,7 +93,8 @@ struct PackBwdCfg {
     static constexpr int CHUNK = 128 * 128;
     static constexpr int TILE = NCH * CHUNK;
     static constexpr int BAR_OFF = 7 * TILE;             // (dK/dV uses 6 tiles; its row terms lie in the 7th)
-    static constexpr int SMEM = BAR_OFF + 512;
+    static constexpr int DELTA_OFF = BAR_OFF + 512;      // dQ: D of 128 rows, one half of the columns each
+    static constexpr int SMEM = DELTA_OFF + 1024;
     static constexpr int THREADS = 320;                  // 8 elementwise warps, loads, MMAs
 };
 static_assert(PackBwdCfg<128>::SMEM <= 232448, "shared memory");
@@ -108,7 +110,7 @@ struct PackBwdBars {
     uint64_t own_full;                   // the CTA's own tiles
     uint64_t x_full[3], x_empty[3];      // K blocks | Q blocks (2)
     uint64_t y_full[2], y_empty[2];      // V blocks | dO blocks
-    uint64_t s_full[2], dp_full, p_ready, ds_ready, mma_done;
+    uint64_t s_full[2], dp_full, p_ready, ds_ready, mma_done, delta_ready;
     uint32_t tmem_base;
     int abort;
 };
@@ -122,6 +124,7 @@ __device__ __forceinline__ void bwd_bars_init(PackBwdBars* b) {
     mbar_init(&b->p_ready, 256);
     mbar_init(&b->ds_ready, 256);
     mbar_init(&b->mma_done, 1);
+    mbar_init(&b->delta_ready, 256);
     fence_barrier_init();
 }
 
@@ -208,7 +211,7 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                  const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mg, const PackedShape sh,
                  const int tok_per_tile, const int tiles, const int32_t* __restrict__ cu_q,
                  const int32_t* __restrict__ cu_k, const int causal, const float scale_log2, const float scale,
-                 const float2* __restrict__ terms, __nv_bfloat16* __restrict__ dq, const long long dq_stride,
+                 float2* __restrict__ terms, __nv_bfloat16* __restrict__ dq, const long long dq_stride,
                  int* status) {
     using C = PackBwdCfg<D>;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -311,7 +314,8 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
         const int lim_min = seen_keys(tok0, qr.len, kr.len, causal);
         const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
         float2 ld = make_float2(0.f, 0.f);
-        if (valid) ld = __ldg(terms + ((long long)kvh * sh.total_q + qr.begin + tok) * group + r % group);
+        float2* term = terms + ((long long)kvh * sh.total_q + qr.begin + tok) * group + r % group;
+        if (valid) ld = *term;
         bool ok = true;
         for (int t = 0; t < n; ++t) {
             if (128 * t + 128 > kr.len) {                // the last, partial block: K's rows behind the sequence
@@ -337,6 +341,28 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
             if (!__all_sync(0xffffffffu, mbar_wait(&bars->dp_full, t & 1, abort_flag))) { ok = false; break; }
             tc_fence_after();
             const bool masked = 128 * t + 128 > lim_min;
+            if (n == 1) {
+                // all keys of these rows are here: D = sum_j P_j dP_j from the
+                // fp32 weights.  (The forward's output, with its weights rounded
+                // to bf16, is as good where rows see many keys; where they see
+                // few, its error is felt in every dS of the row.)
+                float part = 0.f;
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float dp[32];
+                    tmem_ld_32x32b_x32(tDP + lane_base + 64 * hf + 32 * c, dp);
+                    tmem_wait_ld();
+                    const int seen = lim - 64 * hf - 32 * c;
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) part = fmaf(p[32 * c + e], e < seen ? dp[e] : 0.f, part);
+                }
+                float* half = reinterpret_cast<float*>(smem + C::DELTA_OFF);
+                half[128 * hf + r] = part;
+                mbar_arrive(&bars->delta_ready);
+                if (!__all_sync(0xffffffffu, mbar_wait(&bars->delta_ready, 0, abort_flag))) { ok = false; break; }
+                ld.y = half[r] + half[128 + r];
+                if (valid && hf == 0) term->y = ld.y;    // for dK and dV
+            }
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 float dp[32];
@@ -638,7 +664,8 @@ static long long key_items(const PackedShape& s) { return ((long long)s.total_k 
 // for adding up.  A tile's longest chain of blocks (all rows of a sequence, 2.5
 // times the average one at most) bounds the time from below: few kv heads and a
 // large group make long chains and few of them.  Packed training batch (4128
-// tokens, 16 heads on 4, d 64): 1 share 94 us, 4 shares 44 us.
+// tokens, 16 heads on 4, d 64): 1 share 94 us, 4 shares 84 us; 4000 tokens, 5
+// heads on 1, d 128, with dQ: 304 and 129 us.
 static int key_shares(const PackedShape& s, int causal) {
     const double per_seq = (double)s.total_q / s.n_seq / (128 / s.group());
     const double longest = std::min(s.n_seq == 1 ? 1.0 : 2.5, (double)s.n_seq) * per_seq, mean = causal ? 0.5 * per_seq : per_seq;
