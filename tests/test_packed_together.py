@@ -1,0 +1,108 @@
+"""The operators over packed sequences as a model uses them together: a softmax
+branch and a linear branch with decays over the same packed batch, one
+workspace for all calls, for training and for generating token by token."""
+import pytest
+import torch
+
+from decay_ref import decay_attention
+from packed_ref import attention, check, cu_of
+from test_packed_attn import ops, randn  # noqa: F401  (ops is a fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+def bf16(shape):
+    return torch.full(shape, 7.0, dtype=torch.bfloat16, device="cuda")
+
+
+def workspace(ops, total_q, total_k, n_seq, hq, hk, d):  # noqa: F811
+    return ops.new_workspace_bytes(max(ops.vsa_packed_attn_workspace_bytes(total_q, total_k, n_seq, hq, hk, d),
+                                       ops.vsa_decay_attn_workspace_bytes(total_k, n_seq, hk, d)))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_training_step_of_both_branches(ops, d):  # noqa: F811
+    """Slices of one projection feed both branches (the linear one takes the kv heads' queries); eager, and captured
+    with the calls of both branches interleaved on one workspace: the same bits."""
+    lens, hq, hk = [150, 0, 333, 7], 4, 2
+    n = sum(lens)
+    x, g, gl = randn(1, n, hq + 2 * hk, d), randn(2, n, hq, d), randn(3, n, hk, d)
+    q, k, v, ql = x[:, :hq], x[:, hq:hq + hk], x[:, hq + hk:], x[:, :hk]
+    ld, cu = torch.tensor([-0.01, -0.2]).cuda(), cu_of(lens).cuda()
+    ws = workspace(ops, n, n, len(lens), hq, hk, d)
+    soft = dict(out=bf16(q.shape), dq=bf16(q.shape), dk=bf16(k.shape), dv=bf16(k.shape))
+    lin = dict(out=bf16(ql.shape), dq=bf16(ql.shape), dk=bf16(ql.shape), dv=bf16(ql.shape))
+    out32, lse = torch.empty(n, hq, d, device="cuda"), torch.empty(hq, n, device="cuda")
+
+    def step():
+        ops.vsa_packed_attn_fwd(q, k, v, cu, cu, soft["out"], ws, out_f32=out32, lse=lse)
+        ops.vsa_decay_attn_fwd(ql, k, v, ld, cu, lin["out"], ws)
+        ops.vsa_decay_attn_bwd(ql, k, v, gl, ld, cu, lin["dq"], lin["dk"], lin["dv"], ws)
+        ops.vsa_packed_attn_bwd(q, k, v, out32, g, cu, cu, lse, soft["dq"], soft["dk"], soft["dv"], ws)
+
+    step()
+    assert ops.vsa_device_status(ws) == 0
+    rs = attention(q.cpu(), k.cpu(), v.cpu(), cu.cpu(), cu.cpu(), True, g.cpu())
+    rl = decay_attention(ql.cpu(), k.cpu(), v.cpu(), ld.cpu(), cu.cpu(), d ** -0.5, None, gl.cpu())
+    for got, r in ((soft, rs), (lin, rl)):
+        for name in got:
+            check(got[name], r[name], r[name + "_tol"], name)
+    want = [t.clone() for r in (soft, lin) for t in r.values()]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        step()
+    for _ in range(3):
+        for r in (soft, lin):
+            for t in r.values():
+                t.fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip([t for r in (soft, lin) for t in r.values()], want))
+    assert ops.vsa_device_status(ws) == 0
+
+
+def test_generation_with_a_cache_and_a_state(ops):  # noqa: F811
+    """Prompts, then a piece of several tokens, then single tokens: the softmax branch reads a cache of keys and values
+    that grows in place (a slice of a larger buffer, sequence after sequence), the linear branch carries its state."""
+    hq, hk, d, prompt, piece, singles = 6, 2, 64, [200, 1, 77], 5, 3
+    n_seq, room = len(prompt), 300
+    whole = [p + piece + singles for p in prompt]
+    x = randn(1, sum(whole), hq + 2 * hk, d)
+    start = [sum(whole[:i]) for i in range(n_seq)]
+    ld = torch.tensor([-0.02, -0.5]).cuda()
+    cache_k, cache_v = bf16((n_seq, room, hk, d)), bf16((n_seq, room, hk, d))
+    state = torch.zeros(n_seq, hk, d, d, device="cuda")
+    ws = workspace(ops, sum(whole), sum(whole), n_seq, hq, hk, d)
+    outs = []
+    done = [0] * n_seq
+    for count in [prompt, [piece] * n_seq] + [[1] * n_seq] * singles:
+        rows = torch.cat([torch.arange(s + a, s + a + c) for s, a, c in zip(start, done, count)]).cuda()
+        q, k, v = x[rows, :hq], x[rows, hq:hq + hk].contiguous(), x[rows, hq + hk:].contiguous()
+        at = 0
+        for i, c in enumerate(count):
+            cache_k[i, done[i]:done[i] + c], cache_v[i, done[i]:done[i] + c] = k[at:at + c], v[at:at + c]
+            at += c
+        done = [a + c for a, c in zip(done, count)]
+        keys = torch.cat([cache_k[i, :done[i]] for i in range(n_seq)])
+        values = torch.cat([cache_v[i, :done[i]] for i in range(n_seq)])
+        cu_q, cu_k = cu_of(count).cuda(), cu_of(done).cuda()
+        soft, lin, new = bf16(q.shape), bf16(k.shape), torch.empty_like(state)
+        ops.vsa_packed_attn_fwd(q, keys, values, cu_q, cu_k, soft, ws)
+        if max(count) > 1:
+            ops.vsa_decay_attn_fwd(q[:, :hk], k, v, ld, cu_q, lin, ws, state_in=state, state_out=new)
+            state = new
+        else:
+            ops.vsa_decay_attn_step(q[:, :hk], k, v, ld, state, lin)
+        assert ops.vsa_device_status(ws) == 0
+        outs.append((rows.cpu(), soft, lin))
+    cu = cu_of(whole)
+    q, k, v = x[:, :hq].cpu(), x[:, hq:hq + hk].cpu(), x[:, hq + hk:].cpu()
+    rs = attention(q, k, v, cu, cu, True)
+    rl = decay_attention(q[:, :hk], k, v, ld.cpu(), cu, d ** -0.5)
+    for rows, soft, lin in outs:
+        check(soft, rs["out"][rows], rs["out_tol"][rows], "softmax branch")
+        # pieces are chunked otherwise than the whole: both roundings (scores, state) at most, so twice the bound
+        check(lin, rl["out"][rows], 2 * rl["out_tol"][rows], "linear branch")
+    check(state, rl["state_out"], 2 * rl["state_out_tol"], "state")
