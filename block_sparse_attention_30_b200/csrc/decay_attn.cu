@@ -89,7 +89,7 @@ __device__ __forceinline__ Piece find_piece(const int32_t* __restrict__ cu, cons
     Piece g{-1, 0, 0, 0, 0};
     const SeqTile at = find_tile(cu, s.n_seq, s.total, len, t, status, 1);
     if (at.seq < 0) return g;
-    const SeqRange r = seq_range(cu, at.seq, s.total, status);
+    const SeqRange r = at.a;
     g.seq = at.seq;
     g.off = at.tile * len;
     g.rest = r.len - g.off;

@@ -33,24 +33,33 @@ __device__ __forceinline__ int seen_keys(int i, int nq, int nk, int causal) {
 struct SeqTile {
     int seq;     // -1: past the last tile
     int tile;    // tile within the sequence
+    SeqRange a, b;
 };
 
-// Tile t of the tiles of `len` rows that the sequences are cut into (`least`
-// for an empty one), sequence after sequence (whole warp; every lane gets the
-// result).  Four sequences per lane and step: one round trip to L2 covers 128
-// sequences.
+// Tile t of the tiles of `len` rows that the sequences of `cu` are cut into
+// (`least` for an empty one), sequence after sequence, with the sequence's rows
+// by `cu` and by `cu_b` (may be null) (whole warp; every lane gets the result).
+// Four sequences per lane and step, all their borders loaded together: one round
+// trip to L2 covers 128 sequences.
 __device__ __forceinline__ SeqTile find_tile(const int32_t* __restrict__ cu, int n_seq, int total, int len, int t,
-                                             int* status, int least = 0) {
+                                             int* status, int least = 0, const int32_t* __restrict__ cu_b = nullptr,
+                                             int total_b = 0) {
     const int lane = threadIdx.x & 31;
     long long base = 0;            // 64 bits: borders that overlap can sum to more than the rows
     for (int s0 = 0; s0 < n_seq; s0 += 128) {
+        SeqRange a[4], b[4];
         int cnt[4];
         long long sum = 0;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int s = s0 + 4 * lane + e;
+            a[e] = b[e] = {0, 0};
             cnt[e] = 0;
-            if (s < n_seq) cnt[e] = max(least, (seq_range(cu, s, total, status).len + len - 1) / len);
+            if (s < n_seq) {
+                a[e] = seq_range(cu, s, total, status);
+                if (cu_b) b[e] = seq_range(cu_b, s, total_b, status);
+                cnt[e] = max(least, (a[e].len + len - 1) / len);
+            }
             sum += cnt[e];
         }
         long long incl = sum;
@@ -62,20 +71,20 @@ __device__ __forceinline__ SeqTile find_tile(const int32_t* __restrict__ cu, int
         const unsigned hit = __ballot_sync(0xffffffffu, base + incl > t);
         if (hit) {
             const int src = __ffs(hit) - 1;
-            SeqTile r{-1, 0};
+            SeqTile r{-1, 0, {0, 0}, {0, 0}};
             long long at = base + incl - sum;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                if (r.seq < 0 && t < at + cnt[e]) { r.seq = s0 + 4 * lane + e; r.tile = (int)(t - at); }
+                if (r.seq < 0 && t < at + cnt[e]) r = {s0 + 4 * lane + e, (int)(t - at), a[e], b[e]};
                 at += cnt[e];
             }
-            r.seq = __shfl_sync(0xffffffffu, r.seq, src);
-            r.tile = __shfl_sync(0xffffffffu, r.tile, src);
+            auto from = [&](int& x) { x = __shfl_sync(0xffffffffu, x, src); };
+            from(r.seq); from(r.tile); from(r.a.begin); from(r.a.len); from(r.b.begin); from(r.b.len);
             return r;
         }
         base += __shfl_sync(0xffffffffu, incl, 31);
     }
-    return {-1, 0};
+    return {-1, 0, {0, 0}, {0, 0}};
 }
 
 // Four lanes with four 16-byte units of a row each -> unit (lane & 3) of each

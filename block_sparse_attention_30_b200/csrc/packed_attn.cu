@@ -98,10 +98,10 @@ __device__ __forceinline__ PackWork pack_work(const int32_t* __restrict__ cu_q, 
     w.split = id % n_splits;
     id /= n_splits;
     w.kvh = id % s.heads_kv;
-    const SeqTile at = find_tile(cu_q, s.n_seq, s.total_q, nt * tok_per_tile, tiles - 1 - id / s.heads_kv, status);
+    const SeqTile at = find_tile(cu_q, s.n_seq, s.total_q, nt * tok_per_tile, tiles - 1 - id / s.heads_kv, status, 0, cu_k, s.total_k);
     w.seq = at.seq;
     if (at.seq < 0) return w;
-    const SeqRange q = seq_range(cu_q, at.seq, s.total_q, status), k = seq_range(cu_k, at.seq, s.total_k, status);
+    const SeqRange q = at.a, k = at.b;
     w.q0 = q.begin; w.nq = q.len; w.k0 = k.begin; w.nk = k.len;
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
@@ -137,6 +137,7 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
     uint8_t* ring = smem + NT * C::TILE;
     PackBars<D, NT>* bars = reinterpret_cast<PackBars<D, NT>*>(smem + C::BAR_OFF);
     volatile int* abort_flag = &bars->abort;
+    if (tid == 32) { tma_prefetch_desc(&mq); tma_prefetch_desc(&mk); tma_prefetch_desc(&mv); }
     if (tid == 0) {
         bars->abort = 0;
         queue_init(&bars->queue, 4 * NT + 2);
@@ -478,7 +479,7 @@ packed_combine_kernel(const PackedShape sh, const int tok_per_cta, const int til
     const int kvh = blockIdx.x % sh.heads_kv;
     const SeqTile at = find_tile(cu_q, sh.n_seq, sh.total_q, tok_per_cta, tiles - 1 - blockIdx.x / sh.heads_kv, status);
     if (at.seq < 0) return;
-    const SeqRange q = seq_range(cu_q, at.seq, sh.total_q, status);
+    const SeqRange q = at.a;
     const int tok0 = at.tile * tok_per_cta;
     const int rows = min(tok_per_cta, q.len - tok0) * group;
     const int f = threadIdx.x % TPR * 4;

@@ -110,7 +110,7 @@ struct PackBwdBars {
     uint64_t own_full;                   // the CTA's own tiles
     uint64_t x_full[3], x_empty[3];      // K blocks | Q blocks (2)
     uint64_t y_full[2], y_empty[2];      // V blocks | dO blocks
-    uint64_t s_full[2], dp_full, p_ready, ds_ready, mma_done, delta_ready;
+    uint64_t s_full[2], dp_full[2], p_ready, ds_ready, mma_done, delta_ready;
     uint32_t tmem_base;
     int abort;
 };
@@ -119,8 +119,7 @@ __device__ __forceinline__ void bwd_bars_init(PackBwdBars* b) {
     b->abort = 0;
     mbar_init(&b->own_full, 1);
     for (int x = 0; x < 3; ++x) { mbar_init(&b->x_full[x], 1); mbar_init(&b->x_empty[x], 1); }
-    for (int x = 0; x < 2; ++x) { mbar_init(&b->y_full[x], 1); mbar_init(&b->y_empty[x], 1); mbar_init(&b->s_full[x], 1); }
-    mbar_init(&b->dp_full, 1);
+    for (int x = 0; x < 2; ++x) { mbar_init(&b->y_full[x], 1); mbar_init(&b->y_empty[x], 1); mbar_init(&b->s_full[x], 1); mbar_init(&b->dp_full[x], 1); }
     mbar_init(&b->p_ready, 256);
     mbar_init(&b->ds_ready, 256);
     mbar_init(&b->mma_done, 1);
@@ -220,26 +219,30 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
         return;
     }
     const int tid = threadIdx.x, warp = warp_uniform(tid >> 5), lane = tid & 31;
+    PackBwdBars* bars = reinterpret_cast<PackBwdBars*>(smem + C::BAR_OFF);
+    volatile int* abort_flag = &bars->abort;
+    if (tid == 0) bwd_bars_init(bars);
+    if (tid == 32) { tma_prefetch_desc(&mq); tma_prefetch_desc(&mk); tma_prefetch_desc(&mv); tma_prefetch_desc(&mg); }
+    if (warp == 9) { tmem_alloc(&bars->tmem_base, 512); tmem_relinquish(); }
     const int group = sh.heads_q / sh.heads_kv;
     const int kvh = blockIdx.x % sh.heads_kv;
     // the last tiles of a sequence see the most keys: they start first
-    const SeqTile tile = find_tile(cu_q, sh.n_seq, sh.total_q, tok_per_tile, tiles - 1 - blockIdx.x / sh.heads_kv, status);
-    if (tile.seq < 0) return;
-    const SeqRange qr = seq_range(cu_q, tile.seq, sh.total_q, status), kr = seq_range(cu_k, tile.seq, sh.total_k, status);
+    const SeqTile tile = find_tile(cu_q, sh.n_seq, sh.total_q, tok_per_tile, tiles - 1 - blockIdx.x / sh.heads_kv, status, 0, cu_k, sh.total_k);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tbase = warp_uniform(bars->tmem_base);
+    if (tile.seq < 0) {
+        if (warp == 9) tmem_dealloc(tbase, 512);
+        return;
+    }
+    const SeqRange qr = tile.a, kr = tile.b;
     const int tok0 = tile.tile * tok_per_tile;
     const int n = warp_uniform((seen_keys(min(tok0 + tok_per_tile, qr.len) - 1, qr.len, kr.len, causal) + 127) / 128);   // key blocks
     uint8_t* sQ = smem;
     uint8_t* sG = smem + C::TILE;
     uint8_t* sK = smem + 2 * C::TILE;                    // 3 slots: a K block is read by S and, two steps later, by dQ
     uint8_t* sV = smem + 5 * C::TILE;                    // 2 slots
-    PackBwdBars* bars = reinterpret_cast<PackBwdBars*>(smem + C::BAR_OFF);
-    volatile int* abort_flag = &bars->abort;
-    if (tid == 0) bwd_bars_init(bars);
-    if (warp == 9) { tmem_alloc(&bars->tmem_base, 512); tmem_relinquish(); }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tbase = warp_uniform(bars->tmem_base);
     const uint32_t tDP = tbase + 256, tAcc = tbase + 384;     // S of block j at 128 (j & 1)
     auto fail = [&]() { *abort_flag = 1; report(status, kStatusTimeout); };
 
@@ -291,7 +294,7 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
             };
             auto issue_dp = [&](int t) {
                 if (!wait(&bars->y_full[t & 1], (t / 2) & 1)) return false;
-                mma_scores<D>(tDP, g, desc_add(v, (t & 1) * C::TILE), &bars->dp_full, &bars->y_empty[t & 1]);
+                mma_scores<D>(tDP, g, desc_add(v, (t & 1) * C::TILE), &bars->dp_full[0], &bars->y_empty[t & 1]);
                 return true;
             };
             bool ok = wait(&bars->own_full, 0) && issue_s(0) && issue_dp(0) && (n < 2 || issue_s(1));
@@ -338,7 +341,7 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
 #pragma unroll
                 for (int e = 0; e < 64; ++e) p[e] = ex2(fmaf(p[e], scale_log2, -ld.x));
             }
-            if (!__all_sync(0xffffffffu, mbar_wait(&bars->dp_full, t & 1, abort_flag))) { ok = false; break; }
+            if (!__all_sync(0xffffffffu, mbar_wait(&bars->dp_full[0], t & 1, abort_flag))) { ok = false; break; }
             tc_fence_after();
             const bool masked = 128 * t + 128 > lim_min;
             if (n == 1) {
@@ -415,16 +418,34 @@ packed_dkdv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
         return;
     }
     const int tid = threadIdx.x, warp = warp_uniform(tid >> 5), lane = tid & 31;
-    const int group = sh.heads_q / sh.heads_kv;
+    PackBwdBars* bars = reinterpret_cast<PackBwdBars*>(smem + C::BAR_OFF);
+    volatile int* abort_flag = &bars->abort;
+    if (tid == 0) bwd_bars_init(bars);
+    if (tid == 32) { tma_prefetch_desc(&mq); tma_prefetch_desc(&mk); tma_prefetch_desc(&mv); tma_prefetch_desc(&mg); }
+    if (warp == 9) { tmem_alloc(&bars->tmem_base, 512); tmem_relinquish(); }
+    const int group = sh.heads_q / sh.heads_kv, rows = tok_per_tile * group;   // rows of a block in use
+    uint8_t* sQ = smem + 2 * C::TILE;                    // 2 slots
+    uint8_t* sG = smem + 4 * C::TILE;                    // 2 slots
+    if (rows < 128 && tid < 256) {
+        // rows that no load writes (a group that does not divide 128): zeros
+        for (int x = 0; x < 4; ++x) zero_rows<D>(sQ + x * C::TILE, rows, tid);
+        fence_proxy_async_smem();
+    }
     // a cluster of `shares` CTAs per tile of keys, each with its share of the row blocks
     const int share = blockIdx.x % shares, item = blockIdx.x / shares;
     const int kvh = item % sh.heads_kv;
     // the first tiles of a sequence are seen by the most queries: they start first
-    const SeqTile tile = find_tile(cu_k, sh.n_seq, sh.total_k, 128, item / sh.heads_kv, status);
-    if (tile.seq < 0) return;                            // the whole cluster
-    const SeqRange qr = seq_range(cu_q, tile.seq, sh.total_q, status), kr = seq_range(cu_k, tile.seq, sh.total_k, status);
+    const SeqTile tile = find_tile(cu_k, sh.n_seq, sh.total_k, 128, item / sh.heads_kv, status, 0, cu_q, sh.total_q);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tbase = warp_uniform(bars->tmem_base);
+    if (tile.seq < 0) {                                  // the whole cluster
+        if (warp == 9) tmem_dealloc(tbase, 512);
+        return;
+    }
+    const SeqRange qr = tile.b, kr = tile.a;
     const int key0 = 128 * tile.tile;
-    const int rows = tok_per_tile * group;               // rows of a block in use
     // first query token that sees key0, and the blocks from its on
     const int tok_first = causal ? max(0, key0 + qr.len - kr.len) : 0;
     const int all = max(0, (qr.len + tok_per_tile - 1) / tok_per_tile - tok_first / tok_per_tile);
@@ -433,23 +454,12 @@ packed_dkdv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
     const int n = warp_uniform(min(per, all - min(all, share * per)));
     uint8_t* sK = smem;
     uint8_t* sV = smem + C::TILE;
-    uint8_t* sQ = smem + 2 * C::TILE;                    // 2 slots
-    uint8_t* sG = smem + 4 * C::TILE;                    // 2 slots
     RowTerms* sT = reinterpret_cast<RowTerms*>(smem + 6 * C::TILE);   // of the even and the odd blocks
-    PackBwdBars* bars = reinterpret_cast<PackBwdBars*>(smem + C::BAR_OFF);
-    volatile int* abort_flag = &bars->abort;
-    if (tid == 0) bwd_bars_init(bars);
-    if (warp == 9) { tmem_alloc(&bars->tmem_base, 512); tmem_relinquish(); }
-    if (rows < 128 && tid < 256) {
-        // rows that no load writes (a group that does not divide 128): zeros
-        for (int x = 0; x < 4; ++x) zero_rows<D>(sQ + x * C::TILE, rows, tid);
-        fence_proxy_async_smem();
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tbase = warp_uniform(bars->tmem_base);
-    const uint32_t tS = tbase, tDP = tbase + 128, tDV = tbase + 256, tDK = tbase + 384;
+    // at d = 64 there is room for two dP, so that the next block's does not
+    // wait for this one's dS to be used up
+    constexpr int NDP = D == 64 ? 2 : 1;
+    const uint32_t tS = tbase, tDV = tbase + 256, tDK = tbase + 256 + D;
+    auto tDP = [&](int t) { return tbase + 128 + (t % NDP) * 256; };
     auto fail = [&]() { *abort_flag = 1; report(status, kStatusTimeout); };
 
     if (warp == 8) {
@@ -498,17 +508,17 @@ packed_dkdv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
             };
             auto issue_dp = [&](int t) {
                 if (!wait(&bars->y_full[t & 1], (t / 2) & 1)) return false;
-                mma_scores<D>(tDP, v, desc_add(g, (t & 1) * C::TILE), &bars->dp_full);
+                mma_scores<D>(tDP(t), v, desc_add(g, (t & 1) * C::TILE), &bars->dp_full[t % NDP]);
                 return true;
             };
             bool ok = wait(&bars->own_full, 0) && issue_s(0) && issue_dp(0);
             for (int t = 0; t < n && ok; ++t) {
                 if (!(ok = wait(&bars->p_ready, t & 1))) break;
                 mma_weighted<D>(tDV, tS, desc_add(g_mn, (t & 1) * C::TILE), t > 0, nullptr);
-                if (t + 1 < n && !(ok = issue_s(t + 1))) break;
+                if (t + 1 < n && !(ok = issue_s(t + 1) && (NDP == 1 || issue_dp(t + 1)))) break;
                 if (!(ok = wait(&bars->ds_ready, t & 1))) break;
-                mma_weighted<D>(tDK, tDP, desc_add(q_mn, (t & 1) * C::TILE), t > 0, &bars->x_empty[t & 1]);
-                if (t + 1 < n) ok = issue_dp(t + 1);
+                mma_weighted<D>(tDK, tDP(t), desc_add(q_mn, (t & 1) * C::TILE), t > 0, &bars->x_empty[t & 1]);
+                if (NDP == 1 && t + 1 < n) ok = issue_dp(t + 1);
             }
             if (!ok) fail();
             if (elect_one()) mma_commit(&bars->mma_done);
@@ -584,12 +594,12 @@ packed_dkdv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
             tmem_wait_st();
             tc_fence_before();
             mbar_arrive(&bars->p_ready);
-            if (!__all_sync(0xffffffffu, mbar_wait(&bars->dp_full, t & 1, abort_flag))) { ok = false; continue; }
+            if (!__all_sync(0xffffffffu, mbar_wait(&bars->dp_full[t % NDP], (t / NDP) & 1, abort_flag))) { ok = false; continue; }
             tc_fence_after();
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 float dp[32];
-                tmem_ld_32x32b_x32(tDP + lane_base + 64 * hf + 32 * c, dp);
+                tmem_ld_32x32b_x32(tDP(t) + lane_base + 64 * hf + 32 * c, dp);
                 tmem_wait_ld();
 #pragma unroll
                 for (int e = 0; e < 32; e += 4) {
@@ -606,7 +616,7 @@ packed_dkdv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
                 uint32_t pk[16];
 #pragma unroll
                 for (int e = 0; e < 16; ++e) pk[e] = pack_bf16x2(dp[2 * e], dp[2 * e + 1]);
-                tmem_st_32x32b_x16(tDP + lane_base + 64 * hf + 16 * c, pk);
+                tmem_st_32x32b_x16(tDP(t) + lane_base + 64 * hf + 16 * c, pk);
             }
             tmem_wait_st();
             tc_fence_before();
@@ -634,19 +644,31 @@ packed_dkdv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
         __syncwarp();
         cluster_sync();
         const int count = 128 / shares, row0 = share * count;
-        for (int u = tid; u < 2 * count * (D / 4); u += C::THREADS) {
-            const int unit = u % (D / 4), row = row0 + u / (D / 4) % count, which = u / (D / 4) / count;
-            const float* p = reinterpret_cast<const float*>(smem) + which * 128 * D + row * D + (unit ^ (row & 7)) * 4;
-            float4 sum = cluster_load(p, 0);
-            for (int x = 1; x < shares; ++x) {
-                const float4 y = cluster_load(p, x);
-                sum.x += y.x; sum.y += y.y; sum.z += y.z; sum.w += y.w;
+        constexpr int PER = C::THREADS / (D / 4);        // rows per pass
+        const int unit = tid % (D / 4);
+        for (int at = tid / (D / 4); at < 2 * count; at += 2 * PER) {
+            float4 sum[2], y[2];
+            for (int x = 0; x < shares; ++x) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int u = min(at + i * PER, 2 * count - 1), which = u >= count, row = row0 + u - which * count;
+                    y[i] = cluster_load(reinterpret_cast<const float*>(smem) + which * 128 * D + row * D + (unit ^ (row & 7)) * 4, x);
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if (x == 0) sum[i] = y[i];
+                    else { sum[i].x += y[i].x; sum[i].y += y[i].y; sum[i].z += y[i].z; sum[i].w += y[i].w; }
+                }
             }
-            if (key0 + row >= kr.len) continue;
-            const float f = which ? scale : 1.f;
-            __nv_bfloat16* dst = (which ? dk + ((long long)kr.begin + key0 + row) * dk_stride : dv + ((long long)kr.begin + key0 + row) * dv_stride) +
-                                 (long long)kvh * D + unit * 4;
-            *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(sum.x * f, sum.y * f), pack_bf16x2(sum.z * f, sum.w * f));
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int u = at + i * PER, which = u >= count, row = row0 + u - which * count;
+                if (u >= 2 * count || key0 + row >= kr.len) continue;
+                const float f = which ? scale : 1.f;
+                __nv_bfloat16* dst = (which ? dk + ((long long)kr.begin + key0 + row) * dk_stride : dv + ((long long)kr.begin + key0 + row) * dv_stride) +
+                                     (long long)kvh * D + unit * 4;
+                *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(sum[i].x * f, sum[i].y * f), pack_bf16x2(sum[i].z * f, sum[i].w * f));
+            }
         }
         cluster_sync();                                  // the others have read this CTA's sums
     }
@@ -660,11 +682,11 @@ packed_dkdv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
 static long long key_items(const PackedShape& s) { return ((long long)s.total_k / 128 + s.n_seq) * s.heads_kv; }
 
 // CTAs that share a tile of keys in dK/dV: as many as make its rounds shortest,
-// in units of one row block (1.2 us), 4 of them for a CTA's start and end and 2
-// for adding up.  A tile's longest chain of blocks (all rows of a sequence, 2.5
+// in units of one row block (1.5 us), 10 of them for a CTA's start and end and
+// 0.75 for each share to add up.  A tile's longest chain of blocks (all rows of a sequence, 2.5
 // times the average one at most) bounds the time from below: few kv heads and a
 // large group make long chains and few of them.  Packed training batch (4128
-// tokens, 16 heads on 4, d 64): 1 share 94 us, 4 shares 84 us; 4000 tokens, 5
+// tokens, 16 heads on 4, d 64): 1 share 94 us, 2 shares 66 us, 4 shares 80 us; 4000 tokens, 5
 // heads on 1, d 128, with dQ: 304 and 129 us.
 static int key_shares(const PackedShape& s, int causal) {
     const double per_seq = (double)s.total_q / s.n_seq / (128 / s.group());
@@ -673,7 +695,7 @@ static int key_shares(const PackedShape& s, int causal) {
     int best = 1;
     double best_cost = 1e300;
     for (int n = 1; n <= 8; n *= 2) {
-        const double cost = std::max(std::max(1.0, items * n / 148) * (mean / n + 4), longest / n + 4) + (n > 1 ? 2 : 0);
+        const double cost = std::max(std::ceil(items * n / 148) * (mean / n + 10), longest / n + 10) + (n > 1 ? 0.75 * n : 0);
         if (cost < best_cost) { best_cost = cost; best = n; }
     }
     return best;
