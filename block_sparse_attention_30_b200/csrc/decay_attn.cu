@@ -468,7 +468,7 @@ decay_scan_kernel(const __grid_constant__ DecayScanArgs args, const DecayShape s
         float4 u[AHEAD];
 #pragma unroll
         for (int j = 0; j < AHEAD; ++j)
-            if (i0 + j < n) u[j] = *reinterpret_cast<const float4*>(base + (back ? b0 - i0 - j : i0 + j) * step);
+            if (i0 + j < n) u[j] = __ldcg(reinterpret_cast<const float4*>(base + (back ? b0 - i0 - j : i0 + j) * step));
 #pragma unroll
         for (int j = 0; j < AHEAD; ++j) {
             if (i0 + j >= n) break;
@@ -483,7 +483,7 @@ decay_scan_kernel(const __grid_constant__ DecayScanArgs args, const DecayShape s
             // the walk's last part: forward the sequence's last, backwards its first (the only one, or a full one);
             // before it n = 0 borders mean that it is the first of the walk as well
             const float f = ex2((float)(back ? min(r.len, sh.part) : tail) * l2);
-            const float4 u = *p;
+            const float4 u = __ldcg(p);
             s.x = fmaf(f, s.x, u.x); s.y = fmaf(f, s.y, u.y); s.z = fmaf(f, s.z, u.z); s.w = fmaf(f, s.w, u.w);
         }
         *p = s;                                          // (an empty sequence's state goes through)
@@ -912,17 +912,17 @@ decay_out_kernel(const __grid_constant__ DecayPasses passes, const int n_passes,
             float x[D / 2];
 #pragma unroll
             for (int c = 0; c < D / 2; ++c) x[c] = 0.f;
-            if (x0 && row < D) {                         // (whole warps)
+            if (x0 && row < D) {                         // (whole warps; from L2: the scan may have run beside this kernel's start)
                 if (ps.trans) {
 #pragma unroll
-                    for (int c = 0; c < D / 2; ++c) x[c] = __ldg(x0 + (long long)(hf * (D / 2) + c) * D + feat);
+                    for (int c = 0; c < D / 2; ++c) x[c] = __ldcg(x0 + (long long)(hf * (D / 2) + c) * D + feat);
                 } else {
 #pragma unroll
                     for (int c = 0; c < D / 2; c += 16) {
                         uint4 u[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            u[e] = __ldg(reinterpret_cast<const uint4*>(x0 + (long long)((feat & ~3) + e) * D + hf * (D / 2) + c + (lane & 3) * 4));
+                            u[e] = __ldcg(reinterpret_cast<const uint4*>(x0 + (long long)((feat & ~3) + e) * D + hf * (D / 2) + c + (lane & 3) * 4));
                         transpose_units(u, lane);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {

@@ -137,6 +137,7 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
     uint8_t* ring = smem + NT * C::TILE;
     PackBars<D, NT>* bars = reinterpret_cast<PackBars<D, NT>*>(smem + C::BAR_OFF);
     volatile int* abort_flag = &bars->abort;
+    if (NT == 1 && n_splits > 1) grid_dependents_launch();   // the joining kernel may start: it waits for the shares itself
     if (tid == 32) { tma_prefetch_desc(&mq); tma_prefetch_desc(&mk); tma_prefetch_desc(&mv); }
     if (tid == 0) {
         bars->abort = 0;
@@ -471,30 +472,33 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
 template <int D>
 __global__ void __launch_bounds__(256)
 packed_combine_kernel(const PackedShape sh, const int tok_per_cta, const int tiles, const int32_t* __restrict__ cu_q,
-                      const int n_splits, const float* __restrict__ part_o, const float* __restrict__ part_lse,
-                      __nv_bfloat16* __restrict__ out, const long long out_stride, float* __restrict__ out32,
-                      float* __restrict__ lse, int* status) {
+                      const int n_splits, const float* part_o, const float* part_lse, __nv_bfloat16* __restrict__ out,
+                      const long long out_stride, float* __restrict__ out32, float* __restrict__ lse, int* status) {
     constexpr int TPR = D / 4;
     const int group = sh.heads_q / sh.heads_kv;
     const int kvh = blockIdx.x % sh.heads_kv;
     const SeqTile at = find_tile(cu_q, sh.n_seq, sh.total_q, tok_per_cta, tiles - 1 - blockIdx.x / sh.heads_kv, status);
-    if (at.seq < 0) return;
+    if (at.seq < 0) {
+        grid_dependency_wait();                          // (by every CTA, so that what follows in the stream follows both launches)
+        return;
+    }
     const SeqRange q = at.a;
     const int tok0 = at.tile * tok_per_cta;
     const int rows = min(tok_per_cta, q.len - tok0) * group;
+    grid_dependency_wait();                              // (and from L2: the shares may have been written beside this kernel's start)
     const int f = threadIdx.x % TPR * 4;
     for (int r = threadIdx.x / TPR + blockIdx.y * (256 / TPR); r < rows; r += 256 / TPR * gridDim.y) {
         const long long row = (long long)q.begin + tok0 + r / group;
         const int head = kvh * group + r % group;
         float m = -CUDART_INF_F;
-        for (int s = 0; s < n_splits; ++s) m = fmaxf(m, __ldg(part_lse + ((long long)s * sh.heads_q + head) * sh.total_q + row));
+        for (int s = 0; s < n_splits; ++s) m = fmaxf(m, __ldcg(part_lse + ((long long)s * sh.heads_q + head) * sh.total_q + row));
         float sum = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int s = 0; s < n_splits; ++s) {
-            const float l = __ldg(part_lse + ((long long)s * sh.heads_q + head) * sh.total_q + row);
+            const float l = __ldcg(part_lse + ((long long)s * sh.heads_q + head) * sh.total_q + row);
             if (l == -CUDART_INF_F) continue;            // the share saw no key: its O was not written
             const float w = ex2(l - m);
-            const float4 p = __ldg(reinterpret_cast<const float4*>(part_o + (((long long)s * sh.total_q + row) * sh.heads_q + head) * D + f));
+            const float4 p = __ldcg(reinterpret_cast<const float4*>(part_o + (((long long)s * sh.total_q + row) * sh.heads_q + head) * D + f));
             sum += w;
             o.x = fmaf(w, p.x, o.x); o.y = fmaf(w, p.y, o.y); o.z = fmaf(w, p.z, o.z); o.w = fmaf(w, p.w, o.w);
         }
@@ -580,9 +584,9 @@ static cudaError_t launch_packed_fwd_impl(const PackedArgs& a, cudaStream_t stre
         // rows of an average sequence's share of a CTA
         const long long rows = std::min<long long>(NT * tok, (a.s.total_q + a.s.n_seq - 1) / a.s.n_seq) * group, per = 256 / (D / 4);
         const int gy = (int)std::min((rows + per - 1) / per, 8ll);
-        packed_combine_kernel<D><<<dim3((unsigned)(tiles * a.s.heads_kv), gy), 256, 0, stream>>>(
-            a.s, NT * tok, (int)tiles, a.cu_q, n, part_o, part_lse, static_cast<__nv_bfloat16*>(a.out.p), a.out.stride,
-            a.out32, a.lse, a.status);
+        return launch_overlapped(packed_combine_kernel<D>, dim3((unsigned)(tiles * a.s.heads_kv), gy), 256, 0, stream, a.s, NT * tok,
+                                 (int)tiles, a.cu_q, n, part_o, part_lse, static_cast<__nv_bfloat16*>(a.out.p), a.out.stride, a.out32,
+                                 a.lse, a.status);
     }
     return cudaGetLastError();
 }
