@@ -159,6 +159,10 @@ __device__ __forceinline__ void store_rows(float* p, const QuadRows& rows, const
 // here while another SM runs dry).  Two CTAs on an SM hide each other's latency
 // instead.
 // W is a plain struct with an int `seq`, -1 for the end.
+//
+// A warp may wait here for as long as a piece takes, so that these waits give
+// up later than those within a piece.
+constexpr unsigned long long kQueueWait = 16ull * VSA_WAIT_LIMIT_CYCLES;
 template <typename W>
 struct WorkQueue {
     uint4 answer;
@@ -187,7 +191,7 @@ __device__ __forceinline__ bool queue_produce(WorkQueue<W>* q, const volatile in
     const int lane = threadIdx.x & 31;
     int k = 0;
     auto put = [&](const W& w) {
-        if (k >= 2 && !__all_sync(0xffffffffu, sm100::mbar_wait(&q->empty[k & 1], (k / 2 - 1) & 1, abort))) return false;
+        if (k >= 2 && !__all_sync(0xffffffffu, sm100::mbar_wait_for(&q->empty[k & 1], (k / 2 - 1) & 1, abort, kQueueWait))) return false;
         if (lane == 0) {
             q->slot[k & 1] = w;
             sm100::mbar_arrive(&q->full[k & 1]);
@@ -201,7 +205,7 @@ __device__ __forceinline__ bool queue_produce(WorkQueue<W>* q, const volatile in
         const W w = make(id);
         if (w.seq >= 0) {
             if (!put(w)) return false;
-            if (TAKE_OVER && !__all_sync(0xffffffffu, sm100::mbar_wait(&q->ending, (k - 1) & 1, abort))) return false;
+            if (TAKE_OVER && !__all_sync(0xffffffffu, sm100::mbar_wait_for(&q->ending, (k - 1) & 1, abort, kQueueWait))) return false;
         }
         if (!TAKE_OVER) break;
         if (lane == 0) {
@@ -223,7 +227,7 @@ __device__ __forceinline__ bool queue_produce(WorkQueue<W>* q, const volatile in
 // Piece k of the queue (whole warp); false: a wait gave up.
 template <typename W>
 __device__ __forceinline__ bool queue_get(WorkQueue<W>* q, int k, const volatile int* abort, W& w) {
-    if (!__all_sync(0xffffffffu, sm100::mbar_wait(&q->full[k & 1], (k / 2) & 1, abort))) return false;
+    if (!__all_sync(0xffffffffu, sm100::mbar_wait_for(&q->full[k & 1], (k / 2) & 1, abort, kQueueWait))) return false;
     w = q->slot[k & 1];
     __syncwarp();
     if ((threadIdx.x & 31) == 0) sm100::mbar_arrive(&q->empty[k & 1]);

@@ -292,8 +292,13 @@ vsa_status vsa_sparse_linear_attn_fwd_e4m3(const uint8_t* q8, const uint8_t* k8,
  *    are (NaN and Inf too).  Within a sequence the products run over tiles
  *    of 128 tokens, so a NaN or Inf in k or v (in any tensor, for the
  *    gradients) may also reach results that the mask hides it from.
- *  - total below 2^30, n_seq below 2^24, heads below 2^16.  A tensor without
- *    rows (total == 0) may be NULL.
+ *  - total below 2^30, n_seq below 2^24, heads below 2^16, and no launch may
+ *    need more than 2^31 - 1 CTAs (VSA_ERR_UNSUPPORTED).  A tensor without rows
+ *    (total == 0) may be NULL.
+ *  - Outputs must not overlap the inputs or one another, except where stated.
+ *  - The host never reads the borders: how the work is cut follows from the
+ *    totals and the number of sequences, so that a captured call can be
+ *    replayed with other borders.
  * ------------------------------------------------------------------------- */
 
 /* Bytes of workspace vsa_packed_attn_fwd and vsa_packed_attn_bwd need for
@@ -327,7 +332,7 @@ vsa_status vsa_packed_attn_fwd(const vsa_bf16* q, long long q_stride, const vsa_
  *     dq_i = sum_j ds_ij k_j / sqrt(d),  dk_j = sum_i ds_ij q_i / sqrt(d),
  * dk and dv summed over the query heads of a group too (in fp32, in a fixed
  * order: the same call gives the same bits).  p and ds are rounded to bf16
- * for the products.  dq, dk, dv must not overlap the inputs or one another. */
+ * for the products. */
 vsa_status vsa_packed_attn_bwd(const vsa_bf16* q, long long q_stride, const vsa_bf16* k, long long k_stride,
                                const vsa_bf16* v, long long v_stride, const float* out_f32, const vsa_bf16* dout,
                                long long dout_stride, const int32_t* cu_q, const int32_t* cu_k, const float* lse,
@@ -349,10 +354,11 @@ size_t vsa_decay_attn_workspace_bytes(int total, int n_seq, int heads, int head_
  * state_in, state_out: fp32 [n_seq][heads][d][d] (row: feature of k, column:
  * feature of v), the states before each sequence's first and after its last
  * token; either may be NULL (zeros; not written); they must not overlap.  A
- * sequence without tokens passes its state through.  States are fp32
- * throughout (their update splits k, times its decay, into bf16 hi + lo);
- * scores times their decays, and the state as the operand of q S, are rounded
- * to bf16. */
+ * sequence without tokens passes its state through.  States that leave the
+ * library are good to fp32 (k times its decay enters the products in three
+ * bf16 parts, summed in fp32); for out, the state is updated in fp32 with two
+ * parts and rounded to bf16 as the operand of q S, as are the scores times
+ * their decays. */
 vsa_status vsa_decay_attn_fwd(const vsa_bf16* q, long long q_stride, const vsa_bf16* k, long long k_stride,
                               const vsa_bf16* v, long long v_stride, const float* log_decay, const int32_t* cu,
                               const float* state_in, float* state_out, vsa_bf16* out, long long out_stride,
@@ -365,8 +371,7 @@ vsa_status vsa_decay_attn_fwd(const vsa_bf16* q, long long q_stride, const vsa_b
  * in time R_t = lam R_(t+1) + scale q_t^T dout_t (R_last = dstate_out + its term),
  *     dq_t = scale S_t dout_t,  dk_t = R_t v_t,  dv_t = k_t R_t,
  *     dstate_in = lam R_first (dstate_out, for a sequence without tokens).
- * Sums are fp32 in a fixed order: the same call gives the same bits.  dq, dk,
- * dv, dstate_in must not overlap the inputs or one another. */
+ * Sums are fp32 in a fixed order: the same call gives the same bits. */
 vsa_status vsa_decay_attn_bwd(const vsa_bf16* q, long long q_stride, const vsa_bf16* k, long long k_stride,
                               const vsa_bf16* v, long long v_stride, const vsa_bf16* dout, long long dout_stride,
                               const float* log_decay, const int32_t* cu, const float* state_in,

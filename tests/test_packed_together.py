@@ -106,3 +106,42 @@ def test_generation_with_a_cache_and_a_state(ops):  # noqa: F811
         # pieces are chunked otherwise than the whole: both roundings (scores, state) at most, so twice the bound
         check(lin, rl["out"][rows], 2 * rl["out_tol"][rows], "linear branch")
     check(state, rl["state_out"], 2 * rl["state_out_tol"], "state")
+
+
+def test_long_strides(ops):  # noqa: F811
+    """Row offsets past 2^32 bytes in every tensor of both branches: all of them are slices of one buffer whose rows lie
+    2 MB apart; the same bits as from dense copies."""
+    n, d, lens = 2400, 64, [100, 2200, 100]
+    big = torch.empty(n, 1 << 20, dtype=torch.bfloat16, device="cuda")           # 5 GB
+    at = iter(range(0, 1 << 14, 128))
+
+    def part(heads, seed=None):
+        c = next(at) * 8
+        x = big[:, c:c + heads * d].unflatten(1, (heads, d))
+        x.copy_(randn(seed, n, heads, d)) if seed else x.fill_(7)
+        return x
+
+    q, k, v, g, ql, gl = part(2, 1), part(1, 2), part(1, 3), part(2, 4), part(1, 5), part(1, 6)
+    ld, cu = torch.tensor([-0.03]).cuda(), cu_of(lens).cuda()
+    ws = workspace(ops, n, n, len(lens), 2, 1, d)
+    out32, lse = torch.empty(n, 2, d, device="cuda"), torch.empty(2, n, device="cuda")
+
+    def run(q, k, v, g, ql, gl, new):
+        r = [new(2), new(2), new(1), new(1), new(1), new(1), new(1), new(1)]
+        ops.vsa_packed_attn_fwd(q, k, v, cu, cu, r[0], ws, out_f32=out32, lse=lse)
+        ops.vsa_packed_attn_bwd(q, k, v, out32, g, cu, cu, lse, *r[1:4], ws)
+        ops.vsa_decay_attn_fwd(ql, k, v, ld, cu, r[4], ws)
+        ops.vsa_decay_attn_bwd(ql, k, v, gl, ld, cu, *r[5:], ws)
+        assert ops.vsa_device_status(ws) == 0
+        return r
+
+    far = run(q, k, v, g, ql, gl, part)
+    near = run(*[x.contiguous() for x in (q, k, v, g, ql, gl)], lambda h: bf16((n, h, d)))
+    assert all(torch.equal(a, b) for a, b in zip(far, near))
+    step = part(1), part(1)
+    state = torch.randn(n, 1, d, d, device="cuda")
+    a, b = state.clone(), state.clone()
+    ops.vsa_decay_attn_step(ql, k, v, ld, a, step[0])
+    dense = bf16((n, 1, d))
+    ops.vsa_decay_attn_step(ql.contiguous(), k.contiguous(), v.contiguous(), ld, b, dense)
+    assert torch.equal(step[0], dense) and torch.equal(a, b)
