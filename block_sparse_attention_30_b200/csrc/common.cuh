@@ -134,35 +134,6 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
     return d;
 }
 
-// 2^x of two floats on the FMA pipe, for kernels that the MUFU unit (16
-// results per SM and cycle) holds up.  Range reduction as in Cody and Waite
-// (Software Manual for the Elementary Functions, 1980): x = n + f with n the
-// nearest integer (by adding and subtracting 1.5 * 2^23) and |f| <= 1/2; 2^f
-// by the polynomial of degree 5 with the smallest largest relative error there
-// (7.5e-8, found by a Remez exchange; 2.1e-7 with its fp32 roundings); n is
-// added to the exponent.  Arguments below -126 give 2^-126, those up to 127
-// are meant; NaN stays NaN.
-__device__ __forceinline__ void exp2_poly(uint64_t x, float& p0, float& p1) {
-    float x0, x1, r0, r1;
-    unf32x2(x, x0, x1);
-    asm("max.NaN.f32 %0, %1, 0fC2FC0000;" : "=f"(x0) : "f"(x0));   // -126
-    asm("max.NaN.f32 %0, %1, 0fC2FC0000;" : "=f"(x1) : "f"(x1));
-    x = f32x2(x0, x1);
-    const uint64_t r = add_f32x2(x, f32x2(12582912.f, 12582912.f));
-    const uint64_t n = add_f32x2(r, f32x2(-12582912.f, -12582912.f));
-    const uint64_t f = fma_f32x2(n, f32x2(-1.f, -1.f), x);
-    uint64_t p = f32x2(0.0013276472f, 0.0013276472f);
-    p = fma_f32x2(p, f, f32x2(0.00967554133f, 0.00967554133f));
-    p = fma_f32x2(p, f, f32x2(0.0555071327f, 0.0555071327f));
-    p = fma_f32x2(p, f, f32x2(0.240221197f, 0.240221197f));
-    p = fma_f32x2(p, f, f32x2(0.693146967f, 0.693146967f));
-    p = fma_f32x2(p, f, f32x2(1.00000007f, 1.00000007f));
-    unf32x2(p, p0, p1);
-    unf32x2(r, r0, r1);
-    p0 = __int_as_float(__float_as_int(p0) + (__float_as_int(r0) << 23));
-    p1 = __int_as_float(__float_as_int(p1) + (__float_as_int(r1) << 23));
-}
-
 // Fire-and-forget vector add of four floats into global memory (16-byte aligned).
 __device__ __forceinline__ void red_add_v4(float* p, float a, float b, float c, float d) {
     asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(a), "f"(b), "f"(c),

@@ -10,38 +10,31 @@
 
 namespace vsa {
 
+// Launch a kernel in clusters of n CTAs (n divides the grid).  `overlapped`: it
+// may start before the one before it in the stream has ended; it waits
+// (grid_dependency_wait) before it touches what that writes.
 template <typename... P, typename... A>
-cudaError_t launch_with(const cudaLaunchAttribute& at, void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem,
+cudaError_t launch_with(void (*kernel)(P...), unsigned n, bool overlapped, dim3 grid, unsigned threads, size_t smem,
                         cudaStream_t stream, A&&... args) {
-    cudaLaunchAttribute attr = at;
+    cudaLaunchAttribute at[2] = {};
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = n;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t c{};
     c.gridDim = grid;
     c.blockDim = dim3(threads);
     c.dynamicSmemBytes = smem;
     c.stream = stream;
-    c.attrs = &attr;
-    c.numAttrs = 1;
+    c.attrs = n > 1 ? at : at + 1;
+    c.numAttrs = (n > 1 ? 1 : 0) + (overlapped ? 1 : 0);
     return cudaLaunchKernelEx(&c, kernel, static_cast<P>(args)...);
 }
 
-// Launch a kernel that may start before the one before it in the stream has
-// ended; it waits (grid_dependency_wait) before it touches what that writes.
 template <typename... P, typename... A>
 cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t stream, A&&... args) {
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    return launch_with(at, kernel, grid, threads, smem, stream, static_cast<A&&>(args)...);
-}
-
-// Launch a kernel in clusters of n CTAs (n divides the grid).
-template <typename... P, typename... A>
-cudaError_t launch_clusters(void (*kernel)(P...), unsigned n, dim3 grid, unsigned threads, size_t smem, cudaStream_t stream, A&&... args) {
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = n;
-    at.val.clusterDim.y = at.val.clusterDim.z = 1;
-    return launch_with(at, kernel, grid, threads, smem, stream, static_cast<A&&>(args)...);
+    return launch_with(kernel, 1, true, grid, threads, smem, stream, static_cast<A&&>(args)...);
 }
 
 // One bf16 tensor [rows][heads][d]: heads and features contiguous, rows

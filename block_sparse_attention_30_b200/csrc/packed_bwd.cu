@@ -8,7 +8,9 @@
 //     dK_j = sum_i dS_ij q_i / sqrt(d),
 // the sums over i running over every query head of the group as well.
 //
-// Three launches, no atomics (the same call gives the same bits):
+// Three launches, no atomics (the same call gives the same bits); each may
+// start while the last CTAs of the one before end, and waits for it before the
+// terms are read:
 //   row_terms_kernel  (lse, D) of every packed row, D from the forward's fp32
 //                  output (the bf16 one's rounding would enter dQ as
 //                  -dD sum_j P_j k_j, which does not shrink with dQ when the
@@ -17,22 +19,31 @@
 //   dq_kernel      one CTA per 128 rows of one kv head ((token, head of the
 //                  group) pairs, as in the forward), walking its key blocks:
 //                  S = Q K^T, dP = dO V^T, dQ += dS K;
-//   dkdv_kernel    one CTA per 128 keys of one kv head, walking the blocks of
-//                  128 rows that see them: S^T = K Q^T, dP^T = V dO^T,
-//                  dV += P^T dO, dK += dS^T Q.  The rows of a block include
-//                  the group's heads, so the sum over shared heads is part of
-//                  the products.
+//   dkdv_kernel    one CTA, or a cluster of them that share the walk and add
+//                  their sums at its end (key_shares), per 128 keys of one kv
+//                  head, walking the blocks of 128 rows that see them:
+//                  S^T = K Q^T, dP^T = V dO^T, dV += P^T dO, dK += dS^T Q.  The
+//                  rows of a block include the group's heads, so the sum over
+//                  shared heads is part of the products.
 // 7 products instead of the 5 of a single kernel, which would have to add dQ
 // with atomics.  P and dS are rounded to bf16 for the products (2^-8 relative
 // at most per weight); everything else, sums included, is fp32.
 //
-// TMEM holds S twice (dQ) or once (dK/dV), dP once and the accumulators: 512
-// columns.  The tensor cores always have a product that does not wait for the
-// softmax of the current block: dQ alternates dP of block j+1, dQ of block j
-// and S of block j+2; dK/dV runs dV of block j and S^T of block j+1 while dS
-// is formed, and dK of block j and dP^T of block j+1 while the next weights
-// are.  Eight warps do the elementwise part, each row shared by two threads
-// (64 columns each).
+// TMEM holds S twice (dQ) or once (dK/dV), dP once (dK/dV at d = 64: twice) and
+// the accumulators: 512 columns.  The tensor cores always have a product that
+// does not wait for the softmax of the current block: dQ alternates dP of block
+// j+1, dQ of block j and S of block j+2; dK/dV runs dV of block j and S^T of
+// block j+1 while dS is formed, and dK of block j and dP^T of block j+1 while
+// the next weights are.  Eight warps do the elementwise part, each row shared
+// by two threads (64 columns each); warp 8 loads, warp 9 issues the products.
+//
+// 8192 tokens of one sequence, 12 heads, d 128, causal: 16 us for the terms
+// (0.54 of the copy rate), 285 us for dQ (tensor pipe busy 58 % of the time) and
+// 331 us for dK and dV (67 %).  The 7 products alone would take 440 us at the
+// rate of a large library product; the rest is the start and end of a CTA's
+// walk (it holds the whole SM: nothing covers its first loads and its epilogue)
+// and, at d = 128, where TMEM has room for one dP, the wait for the elementwise
+// part.
 // Rows of a tile behind the sequence's end are masked by selection in the
 // scores and overwritten with zeros in shared memory before they enter a
 // product as its inner dimension (0 x NaN would not be 0).
@@ -60,6 +71,7 @@ __global__ void __launch_bounds__(256)
 row_terms_kernel(const float* __restrict__ o, const __nv_bfloat16* __restrict__ dout, const long long dout_stride,
                  const float* __restrict__ lse, const int total, const int heads, const int group,
                  float2* __restrict__ terms) {
+    grid_dependents_launch();                            // the next kernel may start: it waits for the terms itself
     constexpr int TPR = D / 8;
     const long long id = (long long)blockIdx.x * (256 / TPR) + threadIdx.x / TPR;
     const int f = threadIdx.x % TPR * 8;
@@ -210,7 +222,7 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                  const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mg, const PackedShape sh,
                  const int tok_per_tile, const int tiles, const int32_t* __restrict__ cu_q,
                  const int32_t* __restrict__ cu_k, const int causal, const float scale_log2, const float scale,
-                 float2* __restrict__ terms, __nv_bfloat16* __restrict__ dq, const long long dq_stride,
+                 float2* terms, __nv_bfloat16* __restrict__ dq, const long long dq_stride,
                  int* status) {
     using C = PackBwdCfg<D>;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -221,6 +233,7 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
     const int tid = threadIdx.x, warp = warp_uniform(tid >> 5), lane = tid & 31;
     PackBwdBars* bars = reinterpret_cast<PackBwdBars*>(smem + C::BAR_OFF);
     volatile int* abort_flag = &bars->abort;
+    grid_dependents_launch();
     if (tid == 0) bwd_bars_init(bars);
     if (tid == 32) { tma_prefetch_desc(&mq); tma_prefetch_desc(&mk); tma_prefetch_desc(&mv); tma_prefetch_desc(&mg); }
     if (warp == 9) { tmem_alloc(&bars->tmem_base, 512); tmem_relinquish(); }
@@ -233,6 +246,7 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
     tc_fence_after();
     const uint32_t tbase = warp_uniform(bars->tmem_base);
     if (tile.seq < 0) {
+        grid_dependency_wait();                          // (by every CTA, so that the next launch's wait covers the one before this)
         if (warp == 9) tmem_dealloc(tbase, 512);
         return;
     }
@@ -318,7 +332,8 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
         const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
         float2 ld = make_float2(0.f, 0.f);
         float2* term = terms + ((long long)kvh * sh.total_q + qr.begin + tok) * group + r % group;
-        if (valid) ld = *term;
+        grid_dependency_wait();
+        if (valid) ld = __ldcg(term);
         bool ok = true;
         for (int t = 0; t < n; ++t) {
             if (128 * t + 128 > kr.len) {                // the last, partial block: K's rows behind the sequence
@@ -408,7 +423,7 @@ __global__ void __launch_bounds__(PackBwdCfg<D>::THREADS, 1)
 packed_dkdv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                    const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mg, const PackedShape sh,
                    const int tok_per_tile, const int shares, const int32_t* __restrict__ cu_q, const int32_t* __restrict__ cu_k,
-                   const int causal, const float scale_log2, const float scale, const float2* __restrict__ terms,
+                   const int causal, const float scale_log2, const float scale, const float2* terms,
                    __nv_bfloat16* __restrict__ dk, const long long dk_stride, __nv_bfloat16* __restrict__ dv,
                    const long long dv_stride, int* status) {
     using C = PackBwdCfg<D>;
@@ -441,6 +456,7 @@ packed_dkdv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
     tc_fence_after();
     const uint32_t tbase = warp_uniform(bars->tmem_base);
     if (tile.seq < 0) {                                  // the whole cluster
+        grid_dependency_wait();
         if (warp == 9) tmem_dealloc(tbase, 512);
         return;
     }
@@ -536,12 +552,13 @@ packed_dkdv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
             const int tok = (b0 + t) * tok_per_tile + tid / group;
             row_lse = CUDART_INF_F; row_delta = 0.f; row_last = -1;
             if (tid < rows && tok < qr.len) {
-                const float2 ld = __ldg(terms + ((long long)kvh * sh.total_q + qr.begin + tok) * group + tid % group);
+                const float2 ld = __ldcg(terms + ((long long)kvh * sh.total_q + qr.begin + tok) * group + tid % group);
                 row_lse = ld.x;
                 row_delta = ld.y;
                 row_last = seen_keys(tok, qr.len, kr.len, causal) - 1;
             }
         };
+        grid_dependency_wait();                          // for the terms; the operands were there before
         if (tid < 128 && n > 0) fetch(0);
         bool ok = true;
         // A wait that gave up leaves `ok` false in its warp, which then walks on
@@ -736,16 +753,17 @@ static cudaError_t launch_packed_bwd_impl(const PackedArgs& a, cudaStream_t stre
             a.out32, static_cast<const __nv_bfloat16*>(a.dout.p), a.dout.stride, a.lse, s.total_q, s.heads_q, group, terms);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
         const int tiles = s.total_q / tok + s.n_seq;
-        packed_dq_kernel<D><<<(unsigned)(tiles * s.heads_kv), C::THREADS, C::SMEM, stream>>>(
-            mq, mk, mv, mg, s, tok, tiles, a.cu_q, a.cu_k, a.causal, scale_log2, scale, terms,
-            static_cast<__nv_bfloat16*>(a.dq.p), a.dq.stride, a.status);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        e = launch_overlapped(packed_dq_kernel<D>, dim3((unsigned)(tiles * s.heads_kv)), C::THREADS, C::SMEM, stream, mq, mk, mv, mg, s,
+                              tok, tiles, a.cu_q, a.cu_k, a.causal, scale_log2, scale, terms, static_cast<__nv_bfloat16*>(a.dq.p),
+                              a.dq.stride, a.status);
+        if (e != cudaSuccess) return e;
     }
     if (s.total_k) {
         const int shares = key_shares(s, a.causal);
-        e = launch_clusters(packed_dkdv_kernel<D>, shares, dim3((unsigned)(key_items(s) * shares)), C::THREADS, C::SMEM, stream,
-                            mq, mk, mv, mg, s, tok, shares, a.cu_q, a.cu_k, a.causal, scale_log2, scale, terms,
-                            static_cast<__nv_bfloat16*>(a.dk.p), a.dk.stride, static_cast<__nv_bfloat16*>(a.dv.p), a.dv.stride, a.status);
+        // after dQ (without queries there is none: then nothing to overlap with)
+        e = launch_with(packed_dkdv_kernel<D>, shares, s.total_q > 0, dim3((unsigned)(key_items(s) * shares)), C::THREADS, C::SMEM, stream,
+                        mq, mk, mv, mg, s, tok, shares, a.cu_q, a.cu_k, a.causal, scale_log2, scale, terms,
+                        static_cast<__nv_bfloat16*>(a.dk.p), a.dk.stride, static_cast<__nv_bfloat16*>(a.dv.p), a.dv.stride, a.status);
     }
     return e;
 }
