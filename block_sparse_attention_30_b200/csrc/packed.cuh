@@ -1,6 +1,6 @@
 // packed.cuh -- where a tile of packed sequences lies.  The borders `cu` are
 // device data, so the host only knows an upper bound of the number of tiles;
-// every warp finds its tile by a scan over the sequences' tile counts.
+// every warp finds its tile by a search over the borders.
 #pragma once
 #include <cstdint>
 
@@ -31,60 +31,59 @@ __device__ __forceinline__ int seen_keys(int i, int nq, int nk, int causal) {
 }
 
 struct SeqTile {
-    int seq;     // -1: past the last tile
+    int seq;     // -1: none
     int tile;    // tile within the sequence
     SeqRange a, b;
 };
 
-// Tile t of the tiles of `len` rows that the sequences of `cu` are cut into
-// (`least` for an empty one), sequence after sequence, with the sequence's rows
-// by `cu` and by `cu_b` (may be null) (whole warp; every lane gets the result).
-// Four sequences per lane and step, all their borders loaded together: one round
-// trip to L2 covers 128 sequences.
+// What is at place t when each sequence is cut into tiles of `len` rows (an
+// empty one into `least`, 0 or 1), with the sequence's rows by `cu` and by `cu_b`
+// (may be null).  Sequence s takes the places from cu[s] / len + s on: that is
+// total / len + n_seq places at most, and never two sequences' (n rows have
+// n / len + 1 tiles at most, divided as those are); the places between are
+// empty.  So the whole warp finds a place's sequence by a search in 32 parts at
+// a time, one round trip for 32 sequences and two for 1024, where adding up the
+// tiles before it (dense places) reads all borders before it: 4096 sequences of
+// 16 tokens, 8 heads, d 64: 3860 against 1000 us for the softmax branch, 7490
+// against 1280 for the one with decays; 16 of 300 tokens: 26.6 and 24.6, 25.6
+// and 23.8 us.
+// Borders that do not ascend mislead the search; every place checks the borders
+// of its own number, so that they are always reported.
 __device__ __forceinline__ SeqTile find_tile(const int32_t* __restrict__ cu, int n_seq, int total, int len, int t,
                                              int* status, int least = 0, const int32_t* __restrict__ cu_b = nullptr,
                                              int total_b = 0) {
     const int lane = threadIdx.x & 31;
-    long long base = 0;            // 64 bits: borders that overlap can sum to more than the rows
-    for (int s0 = 0; s0 < n_seq; s0 += 128) {
-        SeqRange a[4], b[4];
-        int cnt[4];
-        long long sum = 0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int s = s0 + 4 * lane + e;
-            a[e] = b[e] = {0, 0};
-            cnt[e] = 0;
-            if (s < n_seq) {
-                a[e] = seq_range(cu, s, total, status);
-                if (cu_b) b[e] = seq_range(cu_b, s, total_b, status);
-                cnt[e] = max(least, (a[e].len + len - 1) / len);
-            }
-            sum += cnt[e];
+    SeqTile r{-1, 0, {0, 0}, {0, 0}};
+    int lo = 0, step = 1;
+    if (n_seq > 32) {                    // (below, the last step reads them all)
+        if (t < n_seq && lane == 0) {
+            seq_range(cu, t, total, status);
+            if (cu_b) seq_range(cu_b, t, total_b, status);
         }
-        long long incl = sum;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, incl, d);
-            if (lane >= d) incl += y;
-        }
-        const unsigned hit = __ballot_sync(0xffffffffu, base + incl > t);
-        if (hit) {
-            const int src = __ffs(hit) - 1;
-            SeqTile r{-1, 0, {0, 0}, {0, 0}};
-            long long at = base + incl - sum;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if (r.seq < 0 && t < at + cnt[e]) r = {s0 + 4 * lane + e, (int)(t - at), a[e], b[e]};
-                at += cnt[e];
-            }
-            auto from = [&](int& x) { x = __shfl_sync(0xffffffffu, x, src); };
-            from(r.seq); from(r.tile); from(r.a.begin); from(r.a.len); from(r.b.begin); from(r.b.len);
-            return r;
-        }
-        base += __shfl_sync(0xffffffffu, incl, 31);
+        while (32 * step < n_seq) step *= 32;
     }
-    return {-1, 0, {0, 0}, {0, 0}};
+    for (;; step /= 32) {
+        // of the sequences lo, lo + step, ... the last one that starts at or before t
+        const int s = lo + lane * step;
+        const int tile = s < n_seq ? t - s - max(0, min(total, __ldg(cu + s))) / len : -1;
+        const unsigned hit = __ballot_sync(0xffffffffu, tile >= 0);
+        if (!hit) return r;
+        const int src = 31 - __clz(hit);
+        auto from = [&](int& x) { x = __shfl_sync(0xffffffffu, x, src); };
+        if (step > 1) {
+            lo = s;
+            from(lo);
+            continue;
+        }
+        if (s < n_seq) {
+            r.a = seq_range(cu, s, total, status);
+            if (cu_b) r.b = seq_range(cu_b, s, total_b, status);
+            r.tile = tile;
+            if (tile < least || (long long)tile * len < r.a.len) r.seq = s;
+        }
+        from(r.seq); from(r.tile); from(r.a.begin); from(r.a.len); from(r.b.begin); from(r.b.len);
+        return r;
+    }
 }
 
 // Four lanes with four 16-byte units of a row each -> unit (lane & 3) of each

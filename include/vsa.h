@@ -286,8 +286,8 @@ vsa_status vsa_sparse_linear_attn_fwd_e4m3(const uint8_t* q8, const uint8_t* k8,
  *    Rows before cu[0] and from cu[n_seq] on belong to no sequence: they are
  *    not read into any result, and outputs there are left as they were.
  *    Borders that do not ascend within [0, total] are recorded as
- *    VSA_ERR_DEVICE_CHECK, and a sequence between two such borders is taken
- *    as empty.
+ *    VSA_ERR_DEVICE_CHECK; the outputs of such a call mean nothing, but no row
+ *    outside the tensors is read or written.
  *  - One sequence's values never reach another one's results, whatever they
  *    are (NaN and Inf too).  Within a sequence the products run over tiles
  *    of 128 tokens, so a NaN or Inf in k or v (in any tensor, for the

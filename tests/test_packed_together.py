@@ -145,3 +145,57 @@ def test_long_strides(ops):  # noqa: F811
     dense = bf16((n, 1, d))
     ops.vsa_decay_attn_step(ql.contiguous(), k.contiguous(), v.contiguous(), ld, b, dense)
     assert torch.equal(step[0], dense) and torch.equal(a, b)
+
+
+def many_borders():
+    lens = torch.tensor([0, 0, 1, 2, 3, 5])[torch.randint(6, (1100,), generator=torch.Generator().manual_seed(3))]
+    lens[::97] = 131
+    return cu_of(lens.tolist(), first=4)
+
+
+def test_many_short_sequences(ops):  # noqa: F811
+    """More sequences than two steps of the search for a tile cover, with runs of empty ones, and rows of none."""
+    cu = many_borders().cuda()
+    n, d = int(cu[-1]) + 3, 64
+    q, g, k, v = randn(1, n, 2, d), randn(2, n, 2, d), randn(3, n, 1, d), randn(4, n, 1, d)
+    ws = workspace(ops, n, n, 1100, 2, 1, d)
+    ld = torch.tensor([-0.1]).cuda()
+    soft = dict(out=bf16(q.shape), dq=bf16(q.shape), dk=bf16(k.shape), dv=bf16(k.shape))
+    lin = dict(out=bf16(k.shape), dq=bf16(k.shape), dk=bf16(k.shape), dv=bf16(k.shape))
+    out32, lse = torch.empty(n, 2, d, device="cuda"), torch.empty(2, n, device="cuda")
+    ops.vsa_packed_attn_fwd(q, k, v, cu, cu, soft["out"], ws, out_f32=out32, lse=lse)
+    ops.vsa_packed_attn_bwd(q, k, v, out32, g, cu, cu, lse, soft["dq"], soft["dk"], soft["dv"], ws)
+    ops.vsa_decay_attn_fwd(q[:, :1], k, v, ld, cu, lin["out"], ws)
+    ops.vsa_decay_attn_bwd(q[:, :1], k, v, g[:, :1], ld, cu, lin["dq"], lin["dk"], lin["dv"], ws)
+    assert ops.vsa_device_status(ws) == 0
+    rs = attention(q.cpu(), k.cpu(), v.cpu(), cu.cpu(), cu.cpu(), True, g.cpu())
+    rl = decay_attention(q[:, :1].cpu(), k.cpu(), v.cpu(), ld.cpu(), cu.cpu(), d ** -0.5, None, g[:, :1].cpu())
+    for got, r in ((soft, rs), (lin, rl)):
+        for name in got:
+            check(got[name], r[name], r[name + "_tol"], name)
+            assert (got[name].cpu()[torch.isnan(r[name])] == 7).all(), name
+
+
+def test_bad_borders_among_many_are_reported(ops):  # noqa: F811
+    good = many_borders()
+    n, d = int(good[-1]) + 3, 64
+    q, k, v = randn(1, n, 2, d), randn(3, n, 1, d), randn(4, n, 1, d)
+    ws = workspace(ops, n, n, 1100, 2, 1, d)
+    ld, out32, lse = torch.tensor([-0.1]).cuda(), torch.zeros(n, 2, d, device="cuda"), torch.zeros(2, n, device="cuda")
+    o, b = torch.empty_like(q), [torch.empty_like(t) for t in (q, k, v)]
+    good_d = good.cuda()
+    for at, x in ((1, 2 ** 31 - 1), (778, -2 ** 31), (778, int(good[778]) + 200), (1100, n + 1)):
+        bad = good.clone()
+        bad[at] = x
+        bad_d = bad.cuda()
+        for cq, ck in ((bad_d, good_d), (good_d, bad_d)):
+            ops.vsa_packed_attn_fwd(q, k, v, cq, ck, o, ws)
+            assert ops.vsa_device_status(ws) == 6              # VSA_ERR_DEVICE_CHECK
+            ops.vsa_packed_attn_bwd(q, k, v, out32, q, cq, ck, lse, *b, ws)
+            assert ops.vsa_device_status(ws) == 6
+        ops.vsa_decay_attn_fwd(q[:, :1], k, v, ld, bad_d, o[:, :1], ws)
+        assert ops.vsa_device_status(ws) == 6
+        ops.vsa_decay_attn_bwd(q[:, :1], k, v, q[:, 1:], ld, bad_d, *[t[:, :1] for t in b], ws)
+        assert ops.vsa_device_status(ws) == 6
+    ops.vsa_packed_attn_fwd(q, k, v, good_d, good_d, o, ws)
+    assert ops.vsa_device_status(ws) == 0
