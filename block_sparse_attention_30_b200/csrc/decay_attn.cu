@@ -77,7 +77,9 @@ struct DecayPasses {
 
 struct DecayShape {
     int n_seq, total, heads;
-    int seg, part;               // tokens of a segment and of a part of it (multiples of 128)
+    Divisor seg, part;           // tokens of a segment and of a part of it (multiples of 128)
+    Divisor n_heads;
+    int per;                     // parts of a segment
 };
 
 // log2(lam); below 2^-1024 a decay is a plain 0 (and lam^0 stays 1)
@@ -94,16 +96,42 @@ struct Piece {
     int off, rest;               // tokens of the sequence before it and from its first on
 };
 
-__device__ __forceinline__ Piece find_piece(const int32_t* __restrict__ cu, const DecayShape& s, int len, int t, int* status) {
+__device__ __forceinline__ Piece find_piece(const int32_t* __restrict__ cu, const DecayShape& s, const Divisor& len, int t, int* status) {
     Piece g{-1, 0, 0, 0, 0};
     const SeqTile at = find_tile(cu, s.n_seq, s.total, len, t, status, 1);
     if (at.seq < 0) return g;
     const SeqRange r = at.a;
     g.seq = at.seq;
-    g.off = at.tile * len;
+    g.off = at.tile * len.n;
     g.rest = r.len - g.off;
     g.begin = r.begin + g.off;
-    g.len = min(len, g.rest);
+    g.len = min(len.n, g.rest);
+    return g;
+}
+
+// The sequence that has the last of the rows len j .. len j + len - 1 (whole
+// warp; -1 if none).  Whatever piece of len rows starts among them has that row.
+__device__ __forceinline__ int find_row(const int32_t* __restrict__ cu, const DecayShape& s, int len, int j, SeqRange& r, int* status) {
+    const int row = len * j + len - 1;
+    const int seq = find_last(s.n_seq, [&](int i) { return row - border(cu, i, s.total); });
+    if (seq < 0) return -1;
+    r = seq_range(cu, seq, s.total, status);
+    return row - r.begin < r.len ? seq : -1;
+}
+
+// The part before border j (or behind it) of a sequence that has one there.
+__device__ __forceinline__ Piece find_border(const int32_t* __restrict__ cu, const DecayShape& s, int j, bool behind, int* status) {
+    Piece g{-1, 0, 0, 0, 0};
+    SeqRange r;
+    const int seq = find_row(cu, s, s.part.n, j, r, status);
+    if (seq < 0) return g;
+    const int off = (s.part.n * j + s.part.n - 1 - r.begin) / s.part * s.part.n;
+    if (off + s.part.n >= r.len) return g;               // no border: the sequence ends first
+    g.seq = seq;
+    g.off = behind ? off + s.part.n : off;
+    g.rest = r.len - g.off;
+    g.begin = r.begin + g.off;
+    g.len = min(s.part.n, g.rest);
     return g;
 }
 
@@ -186,12 +214,14 @@ struct DecayStateArgs {
     float* last[2];              // [n_seq][heads][d][d]: the walk's last part, for the scan to finish; or null
     int back[2];
     float w_scale[2];
+    int ends;                    // some `last` is wanted
 };
 
 // grid (kinds of state x parts x heads), from a queue per CTA.  Forward in time
 // the sum of part p goes to the border behind it, backwards that of part p + 1;
 // the walk's last part's to `last`, and without that the parts of its last
-// segment are not needed.  Steps of 64 tokens are counted on from part to part.
+// segment are not needed, and the places are the borders' (total / part, however
+// many sequences are too short to have one).  Steps of 64 tokens are counted on from part to part.
 //
 // Where states leave the library (`last`) the sums are good to fp32: the
 // weighted operand is split into three bf16 parts (all 24 bits) instead of two,
@@ -201,7 +231,7 @@ struct DecayStateArgs {
 // those, one of two accumulators being read while the other is filled.
 template <int D>
 __global__ void __launch_bounds__(DecStateCfg<D>::THREADS, 1)
-decay_state_kernel(const __grid_constant__ DecayStateArgs args, const int kinds, const DecayShape sh,
+decay_state_kernel(const __grid_constant__ DecayStateArgs args, const Divisor kinds, const DecayShape sh,
                    const int32_t* __restrict__ cu, const float* __restrict__ log_decay, int* status) {
     using C = DecStateCfg<D>;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -245,13 +275,15 @@ decay_state_kernel(const __grid_constant__ DecayStateArgs args, const int kinds,
         const bool ok = queue_produce<true>(&bars->queue, abort_flag, [&](int id) {
             DecayPart w{};
             w.kind = id % kinds;
-            id /= kinds;
-            w.head = id % sh.heads;
-            const Piece g = find_piece(cu, sh, sh.part, id / sh.heads, status);
-            const bool needed = args.last[w.kind] ? g.len > 0 : args.back[w.kind] ? g.off >= sh.seg : g.rest > sh.seg - g.off % sh.seg;
+            id = id / kinds;
+            w.head = id % sh.n_heads;
+            id = id / sh.n_heads;
+            const bool back = args.back[w.kind];
+            const Piece g = args.ends ? find_piece(cu, sh, sh.part, id, status) : find_border(cu, sh, id, back, status);
+            const bool needed = args.last[w.kind] ? g.len > 0 : back ? g.off >= sh.seg.n : g.rest > sh.seg.n - g.off % sh.seg;
             w.seq = needed ? g.seq : -1;
             w.begin = g.begin; w.len = g.len;
-            w.ends = args.back[w.kind] ? g.off == 0 : g.rest <= sh.part;
+            w.ends = back ? g.off == 0 : g.rest <= sh.part.n;
             return w;
         });
         if (!ok) fail();
@@ -406,7 +438,7 @@ decay_state_kernel(const __grid_constant__ DecayStateArgs args, const int kinds,
                 mbar_arrive(&bars->sum_free[group & 1]);
             }
             if (!ok) break;
-            const long long slot = (args.back[w.kind] ? w.begin - sh.part : w.begin) / sh.part;
+            const long long slot = (args.back[w.kind] ? w.begin - sh.part.n : w.begin) / sh.part;
             float* dst = w.ends ? args.last[w.kind] + ((long long)w.seq * sh.heads + w.head) * D * D
                                 : args.border[w.kind] + (slot * sh.heads + w.head) * D * D;
             const QuadRows at((long long)feat * D);
@@ -444,34 +476,46 @@ struct DecayScanArgs {
     const float* first[2];
     float* last[2];              // or null
     int back[2];
+    int ends;                    // some `last` is wanted
 };
 
 // Border sums -> states at the borders, in place, and the last part's sum in
 // `last` -> the state that the walk ends with.  grid (sequences x heads,
-// D^2 / 1024, kinds of state), 4 elements per thread.
+// D^2 / 1024, kinds of state), 4 elements per thread; without `last` the places
+// of first segments instead of the sequences: total / seg, one for each that is
+// longer than a segment.
 template <int D>
 __global__ void __launch_bounds__(256)
 decay_scan_kernel(const __grid_constant__ DecayScanArgs args, const DecayShape sh, const int32_t* __restrict__ cu,
                   const float* __restrict__ log_decay, int* status) {
     grid_dependents_launch();                            // decay_out_kernel may start: it waits for the borders itself
-    const int head = blockIdx.x % sh.heads, seq = blockIdx.x / sh.heads, kind = blockIdx.z;
-    const SeqRange r = seq_range(cu, seq, sh.total, status);
+    const int id = blockIdx.x, head = id % sh.n_heads, kind = blockIdx.z;
+    int seq = id / sh.n_heads;
+    SeqRange r{0, 0};
+    if (args.ends) {
+        r = seq_range(cu, seq, sh.total, status);
+    } else {
+        const int j = seq;
+        seq = find_row(cu, sh, sh.seg.n, j, r, status);
+        if (seq < 0 || r.begin / sh.seg != j) r.len = 0;
+    }
+    const int per = sh.per, parts = (r.len + sh.part.n - 1) / sh.part, full_segs = max(0, r.len - 1) / sh.seg;
+    const int slot0 = r.begin / sh.part;
     grid_dependency_wait();                              // (by every CTA: so decay_out_kernel's wait covers the sums' launch too)
     float* last = args.last[kind];
-    if (r.len <= sh.seg && !last) return;
+    if (r.len <= sh.seg.n && !last) return;
     const int back = args.back[kind];
-    const int per = sh.seg / sh.part, parts = (r.len + sh.part - 1) / sh.part;
     // border b lies behind part b; without `last`, forward those up to the last
     // segment's, backwards from the last one down to the first segment's
-    const int n = last ? max(0, parts - 1) : back ? parts - per : (r.len - 1) / sh.seg * per, b0 = back ? parts - 2 : 0;
+    const int n = last ? max(0, parts - 1) : back ? parts - per : full_segs * per, b0 = back ? parts - 2 : 0;
     const int e = (blockIdx.y * 256 + threadIdx.x) * 4;
     const float l2 = decay_log2(log_decay, head);
-    const float full = ex2((float)sh.part * l2);
+    const float full = ex2((float)sh.part.n * l2);
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
     if (args.first[kind]) s = __ldg(reinterpret_cast<const float4*>(args.first[kind] + ((long long)seq * sh.heads + head) * D * D + e));
-    const int tail = r.len - (parts - 1) * sh.part;      // tokens of the last part
+    const int tail = r.len - (parts - 1) * sh.part.n;      // tokens of the last part
     const long long step = (long long)sh.heads * D * D;
-    float* base = args.border[kind] + (r.begin / sh.part) * step + (long long)head * D * D + e;   // border 0
+    float* base = args.border[kind] + slot0 * step + (long long)head * D * D + e;   // border 0
     constexpr int AHEAD = 12;
     for (int i0 = 0; i0 < n; i0 += AHEAD) {
         float4 u[AHEAD];
@@ -491,7 +535,7 @@ decay_scan_kernel(const __grid_constant__ DecayScanArgs args, const DecayShape s
         if (r.len > 0) {
             // the walk's last part: forward the sequence's last, backwards its first (the only one, or a full one);
             // before it n = 0 borders mean that it is the first of the walk as well
-            const float f = ex2((float)(back ? min(r.len, sh.part) : tail) * l2);
+            const float f = ex2((float)(back ? min(r.len, sh.part.n) : tail) * l2);
             const float4 u = __ldcg(p);
             s.x = fmaf(f, s.x, u.x); s.y = fmaf(f, s.y, u.y); s.z = fmaf(f, s.z, u.z); s.w = fmaf(f, s.w, u.w);
         }
@@ -548,7 +592,7 @@ static_assert(sizeof(DecOutBars<64>) <= 512 && sizeof(DecOutBars<128>) <= 512, "
 // CTA's queue; steps (chunks), items and phases are counted on from walk to walk.
 template <int D>
 __global__ void __launch_bounds__(DecOutCfg<D>::THREADS, 1)
-decay_out_kernel(const __grid_constant__ DecayPasses passes, const int n_passes, const DecayShape sh,
+decay_out_kernel(const __grid_constant__ DecayPasses passes, const Divisor n_passes, const DecayShape sh,
                  const int32_t* __restrict__ cu, const float* __restrict__ log_decay, int* status) {
     using C = DecOutCfg<D>;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -618,9 +662,9 @@ decay_out_kernel(const __grid_constant__ DecayPasses passes, const int n_passes,
         const bool ok = queue_produce<true>(&bars->queue, abort_flag, [&](int id) {
             DecayWork w{};
             w.pass = id % n_passes;
-            id /= n_passes;
-            w.head = id % sh.heads;
-            const Piece g = find_piece(cu, sh, sh.seg, id / sh.heads, status);
+            id = id / n_passes;
+            w.head = id % sh.n_heads;
+            const Piece g = find_piece(cu, sh, sh.seg, id / sh.n_heads, status);
             w.seq = g.len > 0 ? g.seq : -1;
             w.begin = g.begin; w.len = g.len; w.off = g.off; w.rest = g.rest;
             return w;
@@ -916,8 +960,8 @@ decay_out_kernel(const __grid_constant__ DecayPasses passes, const int n_passes,
             const float l2 = decay_log2(log_decay, w.head);
             const int n = chunks(w);
             const float* x0;                             // the state before step 0, or null: zeros
-            if (back ? w.rest <= sh.seg : w.off == 0) x0 = ps.first ? ps.first + ((long long)w.seq * sh.heads + w.head) * D * D : nullptr;
-            else x0 = ps.border + ((long long)((back ? w.begin + sh.seg : w.begin) - sh.part) / sh.part * sh.heads + w.head) * D * D;
+            if (back ? w.rest <= sh.seg.n : w.off == 0) x0 = ps.first ? ps.first + ((long long)w.seq * sh.heads + w.head) * D * D : nullptr;
+            else x0 = ps.border + ((long long)(((back ? w.begin + sh.seg.n : w.begin) - sh.part.n) / sh.part) * sh.heads + w.head) * D * D;
             float x[D / 2];
 #pragma unroll
             for (int c = 0; c < D / 2; ++c) x[c] = 0.f;
@@ -1035,10 +1079,10 @@ static DecayShape decay_shape(int n_seq, int total, int heads, int d, int passes
         const double cost = std::ceil(cuts * i * sums / 148) * (len + 1.0);
         if (cost < best_cost) { best_cost = cost; part = len; k = i; }
     }
-    return {n_seq, total, heads, (int)(128 * part * k), (int)(128 * part)};
+    return {n_seq, total, heads, divisor(128 * part * k), divisor(128 * part), divisor(heads), (int)k};
 }
 
-static size_t border_bytes(const DecayShape& s, int d) { return (size_t)(s.total / s.part) * s.heads * d * d * sizeof(float); }
+static size_t border_bytes(const DecayShape& s, int d) { return (size_t)(s.total / s.part.n) * s.heads * d * d * sizeof(float); }
 
 long long decay_work_items(int n_seq, int total, int heads) { return 3 * ((long long)total / 128 + n_seq) * heads; }
 
@@ -1053,22 +1097,24 @@ static bool decay_map(CUtensorMap* m, const PackedTensor& t, const DecayArgs& a,
 template <int D>
 static cudaError_t launch_decay(const DecayArgs& a, const DecayShape& sh, const DecayPasses& passes, int n_passes,
                                 const DecayStateArgs& st, const DecayScanArgs& sc, int kinds, cudaStream_t stream) {
-    const unsigned segs = (unsigned)(((long long)sh.total / sh.seg + sh.n_seq) * a.heads);
-    const unsigned parts = (unsigned)(((long long)sh.total / sh.part + sh.n_seq) * a.heads);
+    const unsigned segs = (unsigned)(((long long)sh.total / sh.seg.n + sh.n_seq) * a.heads);
+    // places of the sums and of the scan: every part and sequence, or those with borders
+    const unsigned parts = (unsigned)(((long long)sh.total / sh.part.n + (st.ends ? sh.n_seq : 0)) * a.heads);
+    const unsigned scans = (unsigned)((long long)(st.ends ? sh.n_seq : sh.total / sh.seg.n) * a.heads);
     cudaError_t e = cudaFuncSetAttribute(decay_out_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, DecOutCfg<D>::SMEM);
     if (e != cudaSuccess) return e;
-    if (a.total > sh.seg || st.last[0] || st.last[1]) {  // some sequence may have several segments, or states are wanted
+    if (a.total > sh.seg.n || st.ends) {  // some sequence may have several segments, or states are wanted
         e = cudaFuncSetAttribute(decay_state_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, DecStateCfg<D>::SMEM);
         if (e != cudaSuccess) return e;
-        decay_state_kernel<D><<<parts * kinds, DecStateCfg<D>::THREADS, DecStateCfg<D>::SMEM, stream>>>(st, kinds, sh, a.cu, a.log_decay, a.status);
+        decay_state_kernel<D><<<parts * kinds, DecStateCfg<D>::THREADS, DecStateCfg<D>::SMEM, stream>>>(st, divisor(kinds), sh, a.cu, a.log_decay, a.status);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
-        e = launch_overlapped(decay_scan_kernel<D>, dim3((unsigned)((long long)a.n_seq * a.heads), D * D / 1024, kinds), 256, 0, stream,
+        e = launch_overlapped(decay_scan_kernel<D>, dim3(scans, D * D / 1024, kinds), 256, 0, stream,
                               sc, sh, a.cu, a.log_decay, a.status);
         if (e != cudaSuccess) return e;
         return launch_overlapped(decay_out_kernel<D>, dim3(segs * n_passes), DecOutCfg<D>::THREADS, DecOutCfg<D>::SMEM, stream, passes,
-                                 n_passes, sh, a.cu, a.log_decay, a.status);
+                                 divisor(n_passes), sh, a.cu, a.log_decay, a.status);
     }
-    decay_out_kernel<D><<<segs * n_passes, DecOutCfg<D>::THREADS, DecOutCfg<D>::SMEM, stream>>>(passes, n_passes, sh, a.cu, a.log_decay, a.status);
+    decay_out_kernel<D><<<segs * n_passes, DecOutCfg<D>::THREADS, DecOutCfg<D>::SMEM, stream>>>(passes, divisor(n_passes), sh, a.cu, a.log_decay, a.status);
     return cudaGetLastError();
 }
 
@@ -1093,6 +1139,7 @@ cudaError_t launch_decay_fwd(const DecayArgs& a, cudaStream_t stream) {
     DecayScanArgs sc{};
     sc.border[0] = border;
     sc.last[0] = a.state_out;
+    st.ends = sc.ends = a.state_out != nullptr;
     sc.first[0] = a.state_in;
     return a.d == 128 ? launch_decay<128>(a, sh, ps, 1, st, sc, 1, stream) : launch_decay<64>(a, sh, ps, 1, st, sc, 1, stream);
 }
@@ -1131,6 +1178,7 @@ cudaError_t launch_decay_bwd(const DecayArgs& a, cudaStream_t stream) {
     sc.first[0] = a.state_in;
     sc.first[1] = a.dstate_out;
     st.last[1] = sc.last[1] = a.dstate_in;
+    st.ends = sc.ends = a.dstate_in != nullptr;
     for (int i = 0; i < 2; ++i) st.border[i] = sc.border[i] = border[i], st.back[i] = sc.back[i] = i;
     return a.d == 128 ? launch_decay<128>(a, sh, ps, 3, st, sc, 2, stream) : launch_decay<64>(a, sh, ps, 3, st, sc, 2, stream);
 }

@@ -5,6 +5,7 @@
 #include <cstdint>
 
 #include "common.cuh"
+#include "packed.h"
 #include "sm100.cuh"
 
 namespace vsa {
@@ -36,54 +37,53 @@ struct SeqTile {
     SeqRange a, b;
 };
 
+// The last of the sequences 0 .. n_seq - 1 for which left(s), which descends, is
+// not below 0, or -1 (whole warp): 32 parts at a time.
+template <typename F>
+__device__ __forceinline__ int find_last(int n_seq, F left) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, step = 1;
+    while (32 * step < n_seq) step *= 32;
+    for (;; step /= 32) {
+        const int s = lo + lane * step;
+        const unsigned hit = __ballot_sync(0xffffffffu, s < n_seq && left(s) >= 0);
+        if (!hit) return -1;
+        lo += (31 - __clz(hit)) * step;
+        if (step == 1) return lo;
+    }
+}
+
+// A border that is within the rows, whatever the memory holds.
+__device__ __forceinline__ int border(const int32_t* __restrict__ cu, int s, int total) { return max(0, min(total, __ldg(cu + s))); }
+
 // What is at place t when each sequence is cut into tiles of `len` rows (an
 // empty one into `least`, 0 or 1), with the sequence's rows by `cu` and by `cu_b`
 // (may be null).  Sequence s takes the places from cu[s] / len + s on: that is
 // total / len + n_seq places at most, and never two sequences' (n rows have
 // n / len + 1 tiles at most, divided as those are); the places between are
-// empty.  So the whole warp finds a place's sequence by a search in 32 parts at
-// a time, one round trip for 32 sequences and two for 1024, where adding up the
-// tiles before it (dense places) reads all borders before it: 4096 sequences of
-// 16 tokens, 8 heads, d 64: 3860 against 1000 us for the softmax branch, 7490
-// against 1280 for the one with decays; 16 of 300 tokens: 26.6 and 24.6, 25.6
-// and 23.8 us.
+// empty.  So the whole warp finds a place's sequence by a search, one round trip
+// for 32 sequences and two for 1024, where adding up the tiles before it (dense
+// places) reads all borders before it: 4096 sequences of 16 tokens, 8 heads,
+// d 64: 3860 against 940 us for the softmax branch, 7490 against 650 for the one
+// with decays; 16 of 300 tokens: 26.6 and 22.5, 25.6 and 20.6 us.
 // Borders that do not ascend mislead the search; every place checks the borders
 // of its own number, so that they are always reported.
-__device__ __forceinline__ SeqTile find_tile(const int32_t* __restrict__ cu, int n_seq, int total, int len, int t,
+__device__ __forceinline__ SeqTile find_tile(const int32_t* __restrict__ cu, int n_seq, int total, const Divisor& len, int t,
                                              int* status, int least = 0, const int32_t* __restrict__ cu_b = nullptr,
                                              int total_b = 0) {
-    const int lane = threadIdx.x & 31;
     SeqTile r{-1, 0, {0, 0}, {0, 0}};
-    int lo = 0, step = 1;
-    if (n_seq > 32) {                    // (below, the last step reads them all)
-        if (t < n_seq && lane == 0) {
-            seq_range(cu, t, total, status);
-            if (cu_b) seq_range(cu_b, t, total_b, status);
-        }
-        while (32 * step < n_seq) step *= 32;
+    if (t < n_seq) {
+        seq_range(cu, t, total, status);
+        if (cu_b) seq_range(cu_b, t, total_b, status);
     }
-    for (;; step /= 32) {
-        // of the sequences lo, lo + step, ... the last one that starts at or before t
-        const int s = lo + lane * step;
-        const int tile = s < n_seq ? t - s - max(0, min(total, __ldg(cu + s))) / len : -1;
-        const unsigned hit = __ballot_sync(0xffffffffu, tile >= 0);
-        if (!hit) return r;
-        const int src = 31 - __clz(hit);
-        auto from = [&](int& x) { x = __shfl_sync(0xffffffffu, x, src); };
-        if (step > 1) {
-            lo = s;
-            from(lo);
-            continue;
-        }
-        if (s < n_seq) {
-            r.a = seq_range(cu, s, total, status);
-            if (cu_b) r.b = seq_range(cu_b, s, total_b, status);
-            r.tile = tile;
-            if (tile < least || (long long)tile * len < r.a.len) r.seq = s;
-        }
-        from(r.seq); from(r.tile); from(r.a.begin); from(r.a.len); from(r.b.begin); from(r.b.len);
-        return r;
-    }
+    auto tile = [&](int s) { return t - s - border(cu, s, total) / len; };
+    const int s = find_last(n_seq, tile);
+    if (s < 0) return r;
+    r.tile = tile(s);
+    r.a = seq_range(cu, s, total, status);
+    if (cu_b) r.b = seq_range(cu_b, s, total_b, status);
+    if (r.tile < least || (long long)r.tile * len.n < r.a.len) r.seq = s;
+    return r;
 }
 
 // Four lanes with four 16-byte units of a row each -> unit (lane & 3) of each

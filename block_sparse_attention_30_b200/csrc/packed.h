@@ -37,6 +37,21 @@ cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, unsigned threads,
     return launch_with(kernel, 1, true, grid, threads, smem, stream, static_cast<A&&>(args)...);
 }
 
+// Division by a number that the host knows, of 0 <= x < 2^31: one high product
+// and a correction (magic = floor((2^32 - 1) / n), so the quotient is at most 1
+// too small) instead of some 100 cycles; finding a piece of work takes several
+// in a row.
+struct Divisor {
+    int n;
+    unsigned magic;
+};
+inline Divisor divisor(long long n) { return {(int)n, 0xffffffffu / (unsigned)n}; }
+__device__ __forceinline__ int operator/(int x, const Divisor& d) {
+    const unsigned q = __umulhi((unsigned)x, d.magic);
+    return (int)(q + ((unsigned)x - q * (unsigned)d.n >= (unsigned)d.n));
+}
+__device__ __forceinline__ int operator%(int x, const Divisor& d) { return x - x / d * d.n; }
+
 // One bf16 tensor [rows][heads][d]: heads and features contiguous, rows
 // `stride` elements apart.
 struct PackedTensor {
@@ -47,6 +62,15 @@ struct PackedTensor {
 struct PackedShape {
     int n_seq, total_q, total_k, heads_q, heads_kv, d;
     int group() const { return heads_q / heads_kv; }
+};
+
+// How the rows of the packed tensors are handed to CTAs.
+struct PackedCut {
+    Divisor group;               // query heads per kv head
+    Divisor tok;                 // tokens of a tile of 128 rows
+    Divisor cta;                 // tokens of a CTA
+    Divisor heads;               // kv heads
+    Divisor shares;              // of the other axis
 };
 
 struct PackedArgs {

@@ -104,14 +104,15 @@ struct PackBars {
 static_assert(sizeof(PackBars<64, 2>) <= 1024, "barrier block");
 
 __device__ __forceinline__ PackWork pack_work(const int32_t* __restrict__ cu_q, const int32_t* __restrict__ cu_k,
-                                              const PackedShape& s, int nt, int tok_per_tile, int tiles, int id,
-                                              int causal, int n_splits, int* status) {
+                                              const PackedShape& s, int nt, const PackedCut& cut, int tiles, int id,
+                                              int causal, int* status) {
     PackWork w{};
     // the shares of a tile start together, so that long sequences come first as a whole
-    w.split = id % n_splits;
-    id /= n_splits;
-    w.kvh = id % s.heads_kv;
-    const SeqTile at = find_tile(cu_q, s.n_seq, s.total_q, nt * tok_per_tile, tiles - 1 - id / s.heads_kv, status, 0, cu_k, s.total_k);
+    w.split = id % cut.shares;
+    id = id / cut.shares;
+    w.kvh = id % cut.heads;
+    const int tok_per_tile = cut.tok.n;
+    const SeqTile at = find_tile(cu_q, s.n_seq, s.total_q, cut.cta, tiles - 1 - id / cut.heads, status, 0, cu_k, s.total_k);
     w.seq = at.seq;
     if (at.seq < 0) return w;
     const SeqRange q = at.a, k = at.b;
@@ -124,7 +125,7 @@ __device__ __forceinline__ PackWork pack_work(const int32_t* __restrict__ cu_q, 
         w.nb[x] = x < nt && w.tok[x] < w.nq ? (seen_keys(last, w.nq, w.nk, causal) + 127) / 128 : 0;
     }
     const int nb = max(w.nb[0], w.nb[1]);
-    const int per = (nb + n_splits - 1) / n_splits;
+    const int per = (nb + cut.shares.n - 1) / cut.shares;
     w.lo = min(nb, w.split * per);
     w.hi = min(nb, w.lo + per);
     return w;
@@ -133,11 +134,11 @@ __device__ __forceinline__ PackWork pack_work(const int32_t* __restrict__ cu_q, 
 template <int D, int NT>
 __global__ void __launch_bounds__(PackCfg<D, NT>::THREADS, 3 - NT)
 packed_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-                  const __grid_constant__ CUtensorMap mv, const PackedShape sh, const int tok_per_tile,
+                  const __grid_constant__ CUtensorMap mv, const PackedShape sh, const PackedCut cut,
                   const int tiles, const int32_t* __restrict__ cu_q, const int32_t* __restrict__ cu_k,
                   const int causal, const float scale_log2, __nv_bfloat16* __restrict__ out,
                   const long long out_stride, float* __restrict__ out32, float* __restrict__ lse,
-                  const int n_splits, float* __restrict__ part_o, float* __restrict__ part_lse, int* status) {
+                  float* __restrict__ part_o, float* __restrict__ part_lse, int* status) {
     using C = PackCfg<D, NT>;
     extern __shared__ __align__(1024) uint8_t smem[];
     if (smem_u32(smem) & 1023) {
@@ -145,7 +146,7 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
         return;
     }
     const int tid = threadIdx.x, warp = warp_uniform(tid >> 5), lane = tid & 31;
-    const int group = sh.heads_q / sh.heads_kv;
+    const int group = cut.group.n, tok_per_tile = cut.tok.n, n_splits = cut.shares.n;
     uint8_t* sQ = smem;
     uint8_t* ring = smem + NT * C::TILE;
     PackBars<D, NT>* bars = reinterpret_cast<PackBars<D, NT>*>(smem + C::BAR_OFF);
@@ -184,7 +185,7 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
       reg_dec<C::REG_LOAD>();
       if (warp == 4 * NT + 2) {
         if (!queue_produce<NT == 2>(&bars->queue, abort_flag, [&](int id) {
-                return pack_work(cu_q, cu_k, sh, NT, tok_per_tile, tiles, id, causal, n_splits, status);
+                return pack_work(cu_q, cu_k, sh, NT, cut, tiles, id, causal, status);
             }))
             fail();
       } else if (warp == 4 * NT) {
@@ -332,9 +333,9 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
             PackWork w;
             if (!(ok = queue_get(&bars->queue, k, abort_flag, w)) || w.seq < 0) break;
             const int n = w.hi - w.lo, f = first_step(w, x);
-            const int tok = w.tok[x] + r / group;        // token within the sequence
+            const int tok = w.tok[x] + r / cut.group;    // token within the sequence
             const bool valid = r < tok_per_tile * group && tok < w.nq;
-            const int head = w.kvh * group + r % group;
+            const int head = w.kvh * group + r % cut.group;
             const int lim = valid ? seen_keys(tok, w.nq, w.nk, causal) : 0;
             const int lim_min = seen_keys(w.tok[x], w.nq, w.nk, causal);   // of the tile's first token: the smallest
             float m_run = -CUDART_INF_F, l_run = 0.f;
@@ -484,13 +485,13 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant_
 // One CTA per `tok_per_cta` tokens and kv head as in the kernel before it, D / 4 threads per row.
 template <int D>
 __global__ void __launch_bounds__(256)
-packed_combine_kernel(const PackedShape sh, const int tok_per_cta, const int tiles, const int32_t* __restrict__ cu_q,
-                      const int n_splits, const float* part_o, const float* part_lse, __nv_bfloat16* __restrict__ out,
+packed_combine_kernel(const PackedShape sh, const PackedCut cut, const int tiles, const int32_t* __restrict__ cu_q,
+                      const float* part_o, const float* part_lse, __nv_bfloat16* __restrict__ out,
                       const long long out_stride, float* __restrict__ out32, float* __restrict__ lse, int* status) {
     constexpr int TPR = D / 4;
-    const int group = sh.heads_q / sh.heads_kv;
-    const int kvh = blockIdx.x % sh.heads_kv;
-    const SeqTile at = find_tile(cu_q, sh.n_seq, sh.total_q, tok_per_cta, tiles - 1 - blockIdx.x / sh.heads_kv, status);
+    const int group = cut.group.n, tok_per_cta = cut.cta.n, n_splits = cut.shares.n, id = blockIdx.x;
+    const int kvh = id % cut.heads;
+    const SeqTile at = find_tile(cu_q, sh.n_seq, sh.total_q, cut.cta, tiles - 1 - id / cut.heads, status);
     if (at.seq < 0) {
         grid_dependency_wait();                          // (by every CTA, so that what follows in the stream follows both launches)
         return;
@@ -501,8 +502,8 @@ packed_combine_kernel(const PackedShape sh, const int tok_per_cta, const int til
     grid_dependency_wait();                              // (and from L2: the shares may have been written beside this kernel's start)
     const int f = threadIdx.x % TPR * 4;
     for (int r = threadIdx.x / TPR + blockIdx.y * (256 / TPR); r < rows; r += 256 / TPR * gridDim.y) {
-        const long long row = (long long)q.begin + tok0 + r / group;
-        const int head = kvh * group + r % group;
+        const long long row = (long long)q.begin + tok0 + r / cut.group;
+        const int head = kvh * group + r % cut.group;
         float m = -CUDART_INF_F;
         for (int s = 0; s < n_splits; ++s) m = fmaxf(m, __ldcg(part_lse + ((long long)s * sh.heads_q + head) * sh.total_q + row));
         float sum = 0.f;
@@ -585,20 +586,21 @@ static cudaError_t launch_packed_fwd_impl(const PackedArgs& a, cudaStream_t stre
         !encode_packed_map(&mv, vv, std::max(1, a.s.total_k), a.s.heads_kv, D, 1, 128, a.enc))
         return cudaErrorInvalidValue;
     const int n = packed_splits(a.s);
+    const PackedCut cut{divisor(group), divisor(tok), divisor(NT * tok), divisor(a.s.heads_kv), divisor(n)};
     float* part_o = reinterpret_cast<float*>(a.scratch);
     float* part_lse = part_o + (size_t)n * a.s.total_q * a.s.heads_q * D;
     const float scale_log2 = 1.4426950408889634f / sqrtf((float)D);
     packed_fwd_kernel<D, NT><<<(unsigned)(tiles * a.s.heads_kv * n), C::THREADS, C::SMEM, stream>>>(
-        mq, mk, mv, a.s, tok, (int)tiles, a.cu_q, a.cu_k, a.causal, scale_log2,
-        static_cast<__nv_bfloat16*>(a.out.p), a.out.stride, a.out32, a.lse, n, part_o, part_lse, a.status);
+        mq, mk, mv, a.s, cut, (int)tiles, a.cu_q, a.cu_k, a.causal, scale_log2,
+        static_cast<__nv_bfloat16*>(a.out.p), a.out.stride, a.out32, a.lse, part_o, part_lse, a.status);
     if (n > 1) {
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
         // rows of an average sequence's share of a CTA
         const long long rows = std::min<long long>(NT * tok, (a.s.total_q + a.s.n_seq - 1) / a.s.n_seq) * group, per = 256 / (D / 4);
         const int gy = (int)std::min((rows + per - 1) / per, 8ll);
-        return launch_overlapped(packed_combine_kernel<D>, dim3((unsigned)(tiles * a.s.heads_kv), gy), 256, 0, stream, a.s, NT * tok,
-                                 (int)tiles, a.cu_q, n, part_o, part_lse, static_cast<__nv_bfloat16*>(a.out.p), a.out.stride, a.out32,
+        return launch_overlapped(packed_combine_kernel<D>, dim3((unsigned)(tiles * a.s.heads_kv), gy), 256, 0, stream, a.s, cut,
+                                 (int)tiles, a.cu_q, part_o, part_lse, static_cast<__nv_bfloat16*>(a.out.p), a.out.stride, a.out32,
                                  a.lse, a.status);
     }
     return cudaGetLastError();

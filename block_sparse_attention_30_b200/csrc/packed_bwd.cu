@@ -220,7 +220,7 @@ template <int D>
 __global__ void __launch_bounds__(PackBwdCfg<D>::THREADS, 1)
 packed_dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                  const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mg, const PackedShape sh,
-                 const int tok_per_tile, const int tiles, const int32_t* __restrict__ cu_q,
+                 const PackedCut cut, const int tiles, const int32_t* __restrict__ cu_q,
                  const int32_t* __restrict__ cu_k, const int causal, const float scale_log2, const float scale,
                  float2* terms, __nv_bfloat16* __restrict__ dq, const long long dq_stride,
                  int* status) {
@@ -237,10 +237,10 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
     if (tid == 0) bwd_bars_init(bars);
     if (tid == 32) { tma_prefetch_desc(&mq); tma_prefetch_desc(&mk); tma_prefetch_desc(&mv); tma_prefetch_desc(&mg); }
     if (warp == 9) { tmem_alloc(&bars->tmem_base, 512); tmem_relinquish(); }
-    const int group = sh.heads_q / sh.heads_kv;
-    const int kvh = blockIdx.x % sh.heads_kv;
+    const int group = cut.group.n, tok_per_tile = cut.tok.n, id = blockIdx.x;
+    const int kvh = id % cut.heads;
     // the last tiles of a sequence see the most keys: they start first
-    const SeqTile tile = find_tile(cu_q, sh.n_seq, sh.total_q, tok_per_tile, tiles - 1 - blockIdx.x / sh.heads_kv, status, 0, cu_k, sh.total_k);
+    const SeqTile tile = find_tile(cu_q, sh.n_seq, sh.total_q, cut.cta, tiles - 1 - id / cut.heads, status, 0, cu_k, sh.total_k);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -325,13 +325,13 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
         }
     } else {
         const int r = 32 * (warp & 3) + lane, hf = warp >> 2;     // row, half of the columns
-        const int tok = tok0 + r / group;
+        const int tok = tok0 + r / cut.group;
         const bool valid = r < tok_per_tile * group && tok < qr.len;
         const int lim = valid ? seen_keys(tok, qr.len, kr.len, causal) : 0;
         const int lim_min = seen_keys(tok0, qr.len, kr.len, causal);
         const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
         float2 ld = make_float2(0.f, 0.f);
-        float2* term = terms + ((long long)kvh * sh.total_q + qr.begin + tok) * group + r % group;
+        float2* term = terms + ((long long)kvh * sh.total_q + qr.begin + tok) * group + r % cut.group;
         grid_dependency_wait();
         if (valid) ld = __ldcg(term);
         bool ok = true;
@@ -407,7 +407,7 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
         if (!ok) fail();
         if (ok) {
             tc_fence_after();
-            const QuadRows at(valid ? ((long long)qr.begin + tok) * dq_stride + (long long)(kvh * group + r % group) * D : -1);
+            const QuadRows at(valid ? ((long long)qr.begin + tok) * dq_stride + (long long)(kvh * group + r % cut.group) * D : -1);
             store_grad<D>(tAcc + lane_base + hf * (D / 2), n > 0, scale, dq + hf * (D / 2), at);
         }
     }
@@ -422,7 +422,7 @@ template <int D>
 __global__ void __launch_bounds__(PackBwdCfg<D>::THREADS, 1)
 packed_dkdv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                    const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mg, const PackedShape sh,
-                   const int tok_per_tile, const int shares, const int32_t* __restrict__ cu_q, const int32_t* __restrict__ cu_k,
+                   const PackedCut cut, const int32_t* __restrict__ cu_q, const int32_t* __restrict__ cu_k,
                    const int causal, const float scale_log2, const float scale, const float2* terms,
                    __nv_bfloat16* __restrict__ dk, const long long dk_stride, __nv_bfloat16* __restrict__ dv,
                    const long long dv_stride, int* status) {
@@ -438,7 +438,7 @@ packed_dkdv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
     if (tid == 0) bwd_bars_init(bars);
     if (tid == 32) { tma_prefetch_desc(&mq); tma_prefetch_desc(&mk); tma_prefetch_desc(&mv); tma_prefetch_desc(&mg); }
     if (warp == 9) { tmem_alloc(&bars->tmem_base, 512); tmem_relinquish(); }
-    const int group = sh.heads_q / sh.heads_kv, rows = tok_per_tile * group;   // rows of a block in use
+    const int group = cut.group.n, tok_per_tile = cut.tok.n, shares = cut.shares.n, rows = tok_per_tile * group;   // rows of a block in use
     uint8_t* sQ = smem + 2 * C::TILE;                    // 2 slots
     uint8_t* sG = smem + 4 * C::TILE;                    // 2 slots
     if (rows < 128 && tid < 256) {
@@ -447,10 +447,10 @@ packed_dkdv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
         fence_proxy_async_smem();
     }
     // a cluster of `shares` CTAs per tile of keys, each with its share of the row blocks
-    const int share = blockIdx.x % shares, item = blockIdx.x / shares;
-    const int kvh = item % sh.heads_kv;
+    const int id = blockIdx.x, share = id % cut.shares, item = id / cut.shares;
+    const int kvh = item % cut.heads;
     // the first tiles of a sequence are seen by the most queries: they start first
-    const SeqTile tile = find_tile(cu_k, sh.n_seq, sh.total_k, 128, item / sh.heads_kv, status, 0, cu_q, sh.total_q);
+    const SeqTile tile = find_tile(cu_k, sh.n_seq, sh.total_k, cut.cta, item / cut.heads, status, 0, cu_q, sh.total_q);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -464,9 +464,9 @@ packed_dkdv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
     const int key0 = 128 * tile.tile;
     // first query token that sees key0, and the blocks from its on
     const int tok_first = causal ? max(0, key0 + qr.len - kr.len) : 0;
-    const int all = max(0, (qr.len + tok_per_tile - 1) / tok_per_tile - tok_first / tok_per_tile);
-    const int per = (all + shares - 1) / shares;
-    const int b0 = tok_first / tok_per_tile + min(all, share * per);
+    const int all = max(0, (qr.len + tok_per_tile - 1) / cut.tok - tok_first / cut.tok);
+    const int per = (all + shares - 1) / cut.shares;
+    const int b0 = tok_first / cut.tok + min(all, share * per);
     const int n = warp_uniform(min(per, all - min(all, share * per)));
     uint8_t* sK = smem;
     uint8_t* sV = smem + C::TILE;
@@ -549,10 +549,10 @@ packed_dkdv_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
         float row_lse = CUDART_INF_F, row_delta = 0.f;
         int row_last = -1;
         auto fetch = [&](int t) {
-            const int tok = (b0 + t) * tok_per_tile + tid / group;
+            const int tok = (b0 + t) * tok_per_tile + tid / cut.group;
             row_lse = CUDART_INF_F; row_delta = 0.f; row_last = -1;
             if (tid < rows && tok < qr.len) {
-                const float2 ld = __ldcg(terms + ((long long)kvh * sh.total_q + qr.begin + tok) * group + tid % group);
+                const float2 ld = __ldcg(terms + ((long long)kvh * sh.total_q + qr.begin + tok) * group + tid % cut.group);
                 row_lse = ld.x;
                 row_delta = ld.y;
                 row_last = seen_keys(tok, qr.len, kr.len, causal) - 1;
@@ -753,16 +753,18 @@ static cudaError_t launch_packed_bwd_impl(const PackedArgs& a, cudaStream_t stre
             a.out32, static_cast<const __nv_bfloat16*>(a.dout.p), a.dout.stride, a.lse, s.total_q, s.heads_q, group, terms);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
         const int tiles = s.total_q / tok + s.n_seq;
+        const PackedCut cut{divisor(group), divisor(tok), divisor(tok), divisor(s.heads_kv), divisor(1)};
         e = launch_overlapped(packed_dq_kernel<D>, dim3((unsigned)(tiles * s.heads_kv)), C::THREADS, C::SMEM, stream, mq, mk, mv, mg, s,
-                              tok, tiles, a.cu_q, a.cu_k, a.causal, scale_log2, scale, terms, static_cast<__nv_bfloat16*>(a.dq.p),
+                              cut, tiles, a.cu_q, a.cu_k, a.causal, scale_log2, scale, terms, static_cast<__nv_bfloat16*>(a.dq.p),
                               a.dq.stride, a.status);
         if (e != cudaSuccess) return e;
     }
     if (s.total_k) {
         const int shares = key_shares(s, a.causal);
+        const PackedCut cut{divisor(group), divisor(tok), divisor(128), divisor(s.heads_kv), divisor(shares)};
         // after dQ (without queries there is none: then nothing to overlap with)
         e = launch_with(packed_dkdv_kernel<D>, shares, s.total_q > 0, dim3((unsigned)(key_items(s) * shares)), C::THREADS, C::SMEM, stream,
-                        mq, mk, mv, mg, s, tok, shares, a.cu_q, a.cu_k, a.causal, scale_log2, scale, terms,
+                        mq, mk, mv, mg, s, cut, a.cu_q, a.cu_k, a.causal, scale_log2, scale, terms,
                         static_cast<__nv_bfloat16*>(a.dk.p), a.dk.stride, static_cast<__nv_bfloat16*>(a.dv.p), a.dv.stride, a.status);
     }
     return e;
