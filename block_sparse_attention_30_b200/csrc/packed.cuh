@@ -64,8 +64,8 @@ __device__ __forceinline__ int border(const int32_t* __restrict__ cu, int s, int
 // empty.  So the whole warp finds a place's sequence by a search, one round trip
 // for 32 sequences and two for 1024, where adding up the tiles before it (dense
 // places) reads all borders before it: 4096 sequences of 16 tokens, 8 heads,
-// d 64: 3860 against 940 us for the softmax branch, 7490 against 650 for the one
-// with decays; 16 of 300 tokens: 26.6 and 22.5, 25.6 and 20.6 us.
+// d 64: 3860 against 1000 us for the softmax branch, 7490 against 1280 for the
+// one with decays; 16 of 300 tokens: 26.6 and 24.6, 25.6 and 23.8 us.
 // Borders that do not ascend mislead the search; every place checks the borders
 // of its own number, so that they are always reported.
 __device__ __forceinline__ SeqTile find_tile(const int32_t* __restrict__ cu, int n_seq, int total, const Divisor& len, int t,
