@@ -476,23 +476,22 @@ struct DecayScanArgs {
     const float* first[2];
     float* last[2];              // or null
     int back[2];
-    int ends;                    // some `last` is wanted
 };
 
 // Border sums -> states at the borders, in place, and the last part's sum in
 // `last` -> the state that the walk ends with.  grid (sequences x heads,
-// D^2 / 1024, kinds of state), 4 elements per thread; without `last` the places
-// of first segments instead of the sequences: total / seg, one for each that is
-// longer than a segment.
+// D^2 / 1024, kinds of state), 4 elements per thread.  Without `last` and where
+// there are more sequences than total / seg, that many places instead: a
+// sequence longer than a segment has one of them, where its first segment starts.
 template <int D>
 __global__ void __launch_bounds__(256)
-decay_scan_kernel(const __grid_constant__ DecayScanArgs args, const DecayShape sh, const int32_t* __restrict__ cu,
+decay_scan_kernel(const __grid_constant__ DecayScanArgs args, const int by_seq, const DecayShape sh, const int32_t* __restrict__ cu,
                   const float* __restrict__ log_decay, int* status) {
     grid_dependents_launch();                            // decay_out_kernel may start: it waits for the borders itself
     const int id = blockIdx.x, head = id % sh.n_heads, kind = blockIdx.z;
     int seq = id / sh.n_heads;
     SeqRange r{0, 0};
-    if (args.ends) {
+    if (by_seq) {
         r = seq_range(cu, seq, sh.total, status);
     } else {
         const int j = seq;
@@ -1100,7 +1099,8 @@ static cudaError_t launch_decay(const DecayArgs& a, const DecayShape& sh, const 
     const unsigned segs = (unsigned)(((long long)sh.total / sh.seg.n + sh.n_seq) * a.heads);
     // places of the sums and of the scan: every part and sequence, or those with borders
     const unsigned parts = (unsigned)(((long long)sh.total / sh.part.n + (st.ends ? sh.n_seq : 0)) * a.heads);
-    const unsigned scans = (unsigned)((long long)(st.ends ? sh.n_seq : sh.total / sh.seg.n) * a.heads);
+    const bool by_seq = st.ends || sh.n_seq <= sh.total / sh.seg.n;
+    const unsigned scans = (unsigned)((long long)(by_seq ? sh.n_seq : sh.total / sh.seg.n) * a.heads);
     cudaError_t e = cudaFuncSetAttribute(decay_out_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, DecOutCfg<D>::SMEM);
     if (e != cudaSuccess) return e;
     if (a.total > sh.seg.n || st.ends) {  // some sequence may have several segments, or states are wanted
@@ -1109,7 +1109,7 @@ static cudaError_t launch_decay(const DecayArgs& a, const DecayShape& sh, const 
         decay_state_kernel<D><<<parts * kinds, DecStateCfg<D>::THREADS, DecStateCfg<D>::SMEM, stream>>>(st, divisor(kinds), sh, a.cu, a.log_decay, a.status);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
         e = launch_overlapped(decay_scan_kernel<D>, dim3(scans, D * D / 1024, kinds), 256, 0, stream,
-                              sc, sh, a.cu, a.log_decay, a.status);
+                              sc, by_seq, sh, a.cu, a.log_decay, a.status);
         if (e != cudaSuccess) return e;
         return launch_overlapped(decay_out_kernel<D>, dim3(segs * n_passes), DecOutCfg<D>::THREADS, DecOutCfg<D>::SMEM, stream, passes,
                                  divisor(n_passes), sh, a.cu, a.log_decay, a.status);
@@ -1139,7 +1139,7 @@ cudaError_t launch_decay_fwd(const DecayArgs& a, cudaStream_t stream) {
     DecayScanArgs sc{};
     sc.border[0] = border;
     sc.last[0] = a.state_out;
-    st.ends = sc.ends = a.state_out != nullptr;
+    st.ends = a.state_out != nullptr;
     sc.first[0] = a.state_in;
     return a.d == 128 ? launch_decay<128>(a, sh, ps, 1, st, sc, 1, stream) : launch_decay<64>(a, sh, ps, 1, st, sc, 1, stream);
 }
@@ -1178,7 +1178,7 @@ cudaError_t launch_decay_bwd(const DecayArgs& a, cudaStream_t stream) {
     sc.first[0] = a.state_in;
     sc.first[1] = a.dstate_out;
     st.last[1] = sc.last[1] = a.dstate_in;
-    st.ends = sc.ends = a.dstate_in != nullptr;
+    st.ends = a.dstate_in != nullptr;
     for (int i = 0; i < 2; ++i) st.border[i] = sc.border[i] = border[i], st.back[i] = sc.back[i] = i;
     return a.d == 128 ? launch_decay<128>(a, sh, ps, 3, st, sc, 2, stream) : launch_decay<64>(a, sh, ps, 3, st, sc, 2, stream);
 }
