@@ -196,6 +196,7 @@ struct DecayPart {
     int seq, head, kind;
     int begin, len;
     int ends;                    // the walk's last part
+    bool alone;                  // the sequence is this part
 };
 
 template <int D>
@@ -211,7 +212,9 @@ static_assert(sizeof(DecStateBars<64>) <= 512, "barrier block");
 struct DecayStateArgs {
     CUtensorMap b[2], c[2];
     float* border[2];
-    float* last[2];              // [n_seq][heads][d][d]: the walk's last part, for the scan to finish; or null
+    float* last[2];              // [n_seq][heads][d][d]: the walk's last part, for the scan to finish (of a sequence of one
+                                 // part: the state after it); or null
+    const float* first[2];       // the states the walks start with, or null (zeros)
     int back[2];
     float w_scale[2];
     int ends;                    // some `last` is wanted
@@ -280,9 +283,10 @@ decay_state_kernel(const __grid_constant__ DecayStateArgs args, const Divisor ki
             id = id / sh.n_heads;
             const bool back = args.back[w.kind];
             const Piece g = args.ends ? find_piece(cu, sh, sh.part, id, status) : find_border(cu, sh, id, back, status);
-            const bool needed = args.last[w.kind] ? g.len > 0 : back ? g.off >= sh.seg.n : g.rest > sh.seg.n - g.off % sh.seg;
+            const bool needed = args.last[w.kind] ? true : back ? g.off >= sh.seg.n : g.rest > sh.seg.n - g.off % sh.seg;
             w.seq = needed ? g.seq : -1;
             w.begin = g.begin; w.len = g.len;
+            w.alone = g.off == 0 && g.rest <= sh.part.n;
             w.ends = back ? g.off == 0 : g.rest <= sh.part.n;
             return w;
         });
@@ -442,6 +446,8 @@ decay_state_kernel(const __grid_constant__ DecayStateArgs args, const Divisor ki
             float* dst = w.ends ? args.last[w.kind] + ((long long)w.seq * sh.heads + w.head) * D * D
                                 : args.border[w.kind] + (slot * sh.heads + w.head) * D * D;
             const QuadRows at((long long)feat * D);
+            const float* const first = w.ends && w.alone && args.first[w.kind] ? args.first[w.kind] + ((long long)w.seq * sh.heads + w.head) * D * D : nullptr;
+            const float f_first = ex2((float)w.len * decay_log2(log_decay, w.head));
 #pragma unroll
             for (int c = 0; c < D; c += 32) {
                 float(&v)[32] = *reinterpret_cast<float(*)[32]>(&x[c]);
@@ -460,7 +466,14 @@ decay_state_kernel(const __grid_constant__ DecayStateArgs args, const Divisor ki
                     }
                     ++exchanges;
                 }
-                if (row < D) store_rows(dst + c, at, v);
+                if (row >= D) continue;                  // (whole warps)
+                if (first) {
+                    float y[32];
+                    load_rows(first + c, at, y);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) v[e] = fmaf(f_first, y[e], v[e]);
+                }
+                store_rows(dst + c, at, v);
             }
         }
         if (!ok) fail();
@@ -480,12 +493,13 @@ struct DecayScanArgs {
 
 // Border sums -> states at the borders, in place, and the last part's sum in
 // `last` -> the state that the walk ends with.  grid (sequences x heads,
-// D^2 / 1024, kinds of state), 4 elements per thread.  Without `last` and where
-// there are more sequences than total / seg, that many places instead: a
-// sequence longer than a segment has one of them, where its first segment starts.
+// D^2 / 1024, kinds of state), 4 elements per thread.  Sequences without a border
+// (of one segment; where `last` is wanted, of one part) have nothing to do here;
+// where there are more sequences than total / that length, the grid has so many
+// places instead, and a sequence that is longer has the one where it starts.
 template <int D>
 __global__ void __launch_bounds__(256)
-decay_scan_kernel(const __grid_constant__ DecayScanArgs args, const int by_seq, const DecayShape sh, const int32_t* __restrict__ cu,
+decay_scan_kernel(const __grid_constant__ DecayScanArgs args, const int by_seq, const Divisor longer, const DecayShape sh, const int32_t* __restrict__ cu,
                   const float* __restrict__ log_decay, int* status) {
     grid_dependents_launch();                            // decay_out_kernel may start: it waits for the borders itself
     const int id = blockIdx.x, head = id % sh.n_heads, kind = blockIdx.z;
@@ -495,18 +509,18 @@ decay_scan_kernel(const __grid_constant__ DecayScanArgs args, const int by_seq, 
         r = seq_range(cu, seq, sh.total, status);
     } else {
         const int j = seq;
-        seq = find_row(cu, sh, sh.seg.n, j, r, status);
-        if (seq < 0 || r.begin / sh.seg != j) r.len = 0;
+        seq = find_row(cu, sh, longer.n, j, r, status);
+        if (seq < 0 || r.begin / longer != j) r.len = 0;
     }
     const int per = sh.per, parts = (r.len + sh.part.n - 1) / sh.part, full_segs = max(0, r.len - 1) / sh.seg;
     const int slot0 = r.begin / sh.part;
     grid_dependency_wait();                              // (by every CTA: so decay_out_kernel's wait covers the sums' launch too)
     float* last = args.last[kind];
-    if (r.len <= sh.seg.n && !last) return;
+    if (r.len <= (last ? sh.part.n : sh.seg.n)) return;
     const int back = args.back[kind];
     // border b lies behind part b; without `last`, forward those up to the last
     // segment's, backwards from the last one down to the first segment's
-    const int n = last ? max(0, parts - 1) : back ? parts - per : full_segs * per, b0 = back ? parts - 2 : 0;
+    const int n = last ? parts - 1 : back ? parts - per : full_segs * per, b0 = back ? parts - 2 : 0;
     const int e = (blockIdx.y * 256 + threadIdx.x) * 4;
     const float l2 = decay_log2(log_decay, head);
     const float full = ex2((float)sh.part.n * l2);
@@ -531,14 +545,11 @@ decay_scan_kernel(const __grid_constant__ DecayScanArgs args, const int by_seq, 
     }
     if (last) {
         float4* p = reinterpret_cast<float4*>(last + ((long long)seq * sh.heads + head) * D * D + e);
-        if (r.len > 0) {
-            // the walk's last part: forward the sequence's last, backwards its first (the only one, or a full one);
-            // before it n = 0 borders mean that it is the first of the walk as well
-            const float f = ex2((float)(back ? min(r.len, sh.part.n) : tail) * l2);
-            const float4 u = __ldcg(p);
-            s.x = fmaf(f, s.x, u.x); s.y = fmaf(f, s.y, u.y); s.z = fmaf(f, s.z, u.z); s.w = fmaf(f, s.w, u.w);
-        }
-        *p = s;                                          // (an empty sequence's state goes through)
+        // the walk's last part: forward the sequence's last, backwards its first, a full one
+        const float f = back ? full : ex2((float)tail * l2);
+        const float4 u = __ldcg(p);
+        s.x = fmaf(f, s.x, u.x); s.y = fmaf(f, s.y, u.y); s.z = fmaf(f, s.z, u.z); s.w = fmaf(f, s.w, u.w);
+        *p = s;
     }
 }
 
@@ -1099,8 +1110,9 @@ static cudaError_t launch_decay(const DecayArgs& a, const DecayShape& sh, const 
     const unsigned segs = (unsigned)(((long long)sh.total / sh.seg.n + sh.n_seq) * a.heads);
     // places of the sums and of the scan: every part and sequence, or those with borders
     const unsigned parts = (unsigned)(((long long)sh.total / sh.part.n + (st.ends ? sh.n_seq : 0)) * a.heads);
-    const bool by_seq = st.ends || sh.n_seq <= sh.total / sh.seg.n;
-    const unsigned scans = (unsigned)((long long)(by_seq ? sh.n_seq : sh.total / sh.seg.n) * a.heads);
+    const Divisor longer = st.ends ? sh.part : sh.seg;
+    const bool by_seq = sh.n_seq <= sh.total / longer.n;
+    const unsigned scans = (unsigned)((long long)(by_seq ? sh.n_seq : sh.total / longer.n) * a.heads);
     cudaError_t e = cudaFuncSetAttribute(decay_out_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, DecOutCfg<D>::SMEM);
     if (e != cudaSuccess) return e;
     if (a.total > sh.seg.n || st.ends) {  // some sequence may have several segments, or states are wanted
@@ -1108,8 +1120,8 @@ static cudaError_t launch_decay(const DecayArgs& a, const DecayShape& sh, const 
         if (e != cudaSuccess) return e;
         decay_state_kernel<D><<<parts * kinds, DecStateCfg<D>::THREADS, DecStateCfg<D>::SMEM, stream>>>(st, divisor(kinds), sh, a.cu, a.log_decay, a.status);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
-        e = launch_overlapped(decay_scan_kernel<D>, dim3(scans, D * D / 1024, kinds), 256, 0, stream,
-                              sc, by_seq, sh, a.cu, a.log_decay, a.status);
+        if (scans)
+            e = launch_overlapped(decay_scan_kernel<D>, dim3(scans, D * D / 1024, kinds), 256, 0, stream, sc, by_seq, longer, sh, a.cu, a.log_decay, a.status);
         if (e != cudaSuccess) return e;
         return launch_overlapped(decay_out_kernel<D>, dim3(segs * n_passes), DecOutCfg<D>::THREADS, DecOutCfg<D>::SMEM, stream, passes,
                                  divisor(n_passes), sh, a.cu, a.log_decay, a.status);
@@ -1135,6 +1147,7 @@ cudaError_t launch_decay_fwd(const DecayArgs& a, cudaStream_t stream) {
     p.p_scale = p.s_scale = a.scale;
     st.border[0] = border;
     st.last[0] = a.state_out;
+    st.first[0] = a.state_in;
     st.w_scale[0] = 1.f;
     DecayScanArgs sc{};
     sc.border[0] = border;
@@ -1177,6 +1190,7 @@ cudaError_t launch_decay_bwd(const DecayArgs& a, cudaStream_t stream) {
     DecayScanArgs sc{};
     sc.first[0] = a.state_in;
     sc.first[1] = a.dstate_out;
+    for (int i = 0; i < 2; ++i) st.first[i] = sc.first[i];
     st.last[1] = sc.last[1] = a.dstate_in;
     st.ends = a.dstate_in != nullptr;
     for (int i = 0; i < 2; ++i) st.border[i] = sc.border[i] = border[i], st.back[i] = sc.back[i] = i;

@@ -149,6 +149,24 @@ __device__ __forceinline__ void store_rows(float* p, const QuadRows& rows, const
     }
 }
 
+// 32 columns of every lane's row of fp32, read as store_rows writes them.
+__device__ __forceinline__ void load_rows(const float* __restrict__ p, const QuadRows& rows, float (&v)[32]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int h = 0; h < 32; h += 16) {
+        uint4 u[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            u[e] = rows.at[e] >= 0 ? __ldg(reinterpret_cast<const uint4*>(p + rows.at[e] + h + (lane & 3) * 4)) : make_uint4(0, 0, 0, 0);
+        transpose_units(u, lane);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            v[h + 4 * e] = __uint_as_float(u[e].x); v[h + 4 * e + 1] = __uint_as_float(u[e].y);
+            v[h + 4 * e + 2] = __uint_as_float(u[e].z); v[h + 4 * e + 3] = __uint_as_float(u[e].w);
+        }
+    }
+}
+
 // A CTA's queue of work: one warp finds what the CTA is to do and hands it to
 // the other warps.  Where a CTA has an SM to itself it then takes over CTAs that
 // have not started yet from the grid (cluster launch control): the latency of
