@@ -199,3 +199,45 @@ def test_bad_borders_among_many_are_reported(ops):  # noqa: F811
         assert ops.vsa_device_status(ws) == 6
     ops.vsa_packed_attn_fwd(q, k, v, good_d, good_d, o, ws)
     assert ops.vsa_device_status(ws) == 0
+
+
+def test_calls_at_once_on_two_streams(ops):  # noqa: F811
+    """Both branches' steps side by side on two streams, a workspace each (kernels of both share SMs): the same bits
+    as one after the other."""
+    lens, hq, hk, d = [300, 1, 0, 700, 64], 8, 2, 64
+    n = sum(lens)
+    q, k, v, g = randn(1, n, hq, d), randn(2, n, hk, d), randn(3, n, hk, d), randn(4, n, hq, d)
+    cu, ones = cu_of(lens).cuda(), cu_of([1] * len(lens)).cuda()
+    ld = torch.linspace(-0.3, -0.001, hq).cuda()
+    kq, vq = randn(5, n, hq, d), randn(6, n, hq, d)
+
+    def buffers():
+        f32 = lambda *s: torch.zeros(*s, device="cuda")  # noqa: E731
+        return dict(ws=workspace(ops, n, n, len(lens), hq, hq, d), out=bf16(q.shape), o32=f32(n, hq, d), lse=f32(hq, n),
+                    dq=bf16(q.shape), dk=bf16(k.shape), dv=bf16(k.shape), tok=bf16((len(lens), hq, d)), lin=bf16(q.shape),
+                    ldq=bf16(q.shape), ldk=bf16(q.shape), ldv=bf16(q.shape), state=f32(len(lens), hq, d, d))
+
+    def soft(b, s):
+        ops.vsa_packed_attn_fwd(q, k, v, cu, cu, b["out"], b["ws"], out_f32=b["o32"], lse=b["lse"], stream=s)
+        ops.vsa_packed_attn_bwd(q, k, v, b["o32"], g, cu, cu, b["lse"], b["dq"], b["dk"], b["dv"], b["ws"], stream=s)
+        ops.vsa_packed_attn_fwd(q[:len(lens)], k, v, ones, cu, b["tok"], b["ws"], stream=s)
+
+    def linear(b, s):
+        ops.vsa_decay_attn_fwd(q, kq, vq, ld, cu, b["lin"], b["ws"], state_out=b["state"], stream=s)
+        ops.vsa_decay_attn_bwd(q, kq, vq, g, ld, cu, b["ldq"], b["ldk"], b["ldv"], b["ws"], stream=s)
+
+    want, x, y = buffers(), buffers(), buffers()
+    soft(want, None)
+    linear(want, None)
+    torch.cuda.synchronize()
+    s, t = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(20):
+        soft(x, s)
+        linear(y, t)
+        linear(x, s)
+        soft(y, t)
+    torch.cuda.synchronize()
+    for b in (x, y):
+        assert ops.vsa_device_status(b["ws"]) == 0
+        for name in want:
+            assert name == "ws" or torch.equal(b[name], want[name]), name
