@@ -171,14 +171,22 @@ def new_workspace_bytes(nbytes, device="cuda", stream=None):
     return ws
 
 
-def _rows(x, shape):
+# A call's checks take longer than its launch, so each helper looks at a tensor
+# once: type, device, shape and layout, for the pointer that it returns.
+def _refuse(x, what, shape, dev):
+    raise AssertionError(f"expected a {what} tensor of shape {tuple(shape)} on CUDA device {dev}, "
+                         f"got {x.dtype} {tuple(x.shape)} on {x.device}")
+
+
+def _rows(x, shape, dev):
     """A packed bf16 [total, heads, d] tensor -> (pointer, row stride)."""
-    assert x.dtype == torch.bfloat16 and x.is_cuda, "expected a bf16 CUDA tensor"
-    assert x.shape == shape, f"expected a tensor of shape {tuple(shape)}, got {tuple(x.shape)}"
+    if x.dtype is not torch.bfloat16 or x.get_device() != dev or x.shape != shape:
+        _refuse(x, "bf16", shape, dev)
     t, h, n = shape
-    st = x.stride()
-    assert t == 0 or ((n == 1 or st[2] == 1) and (h == 1 or st[1] == n)), "heads and features must be contiguous"
-    return x.data_ptr(), st[0] if t > 1 else h * n
+    row, head, feature = x.stride()
+    assert (head == n and feature == 1) or t == 0 or ((n == 1 or feature == 1) and (h == 1 or head == n)), \
+        "heads and features must be contiguous"
+    return x.data_ptr(), row if t > 1 else h * n
 
 
 def _packed_shape(x):
@@ -186,32 +194,37 @@ def _packed_shape(x):
     return x.shape
 
 
-def _borders(cu):
-    assert cu.dtype == torch.int32 and cu.is_cuda and cu.dim() == 1 and cu.is_contiguous() and cu.numel() >= 2, \
-        "expected int32 [n_seq + 1] sequence borders"
+def _device(x):
+    dev = x.get_device()
+    assert dev >= 0, "expected CUDA tensors"
+    return dev
+
+
+def _borders(cu, dev=0):
+    assert cu.dtype is torch.int32 and cu.get_device() == dev and cu.dim() == 1 and cu.is_contiguous() and cu.numel() >= 2, \
+        f"expected int32 [n_seq + 1] sequence borders on CUDA device {dev}"
     return cu.numel() - 1
 
 
-def _f32(x, shape):
+def _f32(x, shape, dev):
     if x is None:
         return None
-    assert x.dtype == torch.float32 and x.is_cuda and x.is_contiguous() and x.shape == shape, \
-        f"expected a contiguous fp32 CUDA tensor of shape {tuple(shape)}"
+    if x.dtype is not torch.float32 or x.get_device() != dev or x.shape != shape or not x.is_contiguous():
+        _refuse(x, "contiguous fp32", shape, dev)
     return x.data_ptr()
 
 
-def _space(workspace):
-    assert workspace.dtype == torch.uint8 and workspace.is_cuda and workspace.is_contiguous(), "expected a uint8 CUDA workspace"
+def _space(workspace, dev):
+    assert workspace.dtype is torch.uint8 and workspace.get_device() == dev and workspace.is_contiguous(), \
+        f"expected a uint8 workspace on CUDA device {dev}"
     return workspace.data_ptr(), workspace.numel()
 
 
-def _run(name, stream, tensors, *args):
+def _run(name, stream, dev, *args):
     """Call an entry point on the tensors' device, on `stream` or that device's current stream."""
-    dev = tensors[0].get_device()
-    assert all(x is None or x.get_device() == dev for x in tensors), "tensors on several devices"
     raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
     f = getattr(_lib.lib(), name)
-    if torch.cuda.current_device() == dev:
+    if torch._C._cuda_getDevice() == dev:
         code = f(*args, raw)
     else:
         with torch.cuda.device(dev):
@@ -231,27 +244,28 @@ def vsa_packed_attn_fwd(q, k, v, cu_q, cu_k, out, workspace, causal=True, out_f3
     Query i of a sequence sees keys up to i + nk - nq (causal) or all of them.
     out_f32 [total_q, heads_q, d] and lse [heads_q, total_q] (fp32) are
     written if given; the backward needs both."""
-    (tq, hq, d), (tk, hk, _) = _packed_shape(q), _packed_shape(k)
-    n = _borders(cu_q)
-    assert _borders(cu_k) == n, "cu_q and cu_k describe different numbers of sequences"
+    x, (tk, hk, _), dev = _packed_shape(q), _packed_shape(k), _device(q)
+    tq, hq, d = x
+    n = _borders(cu_q, dev)
+    assert _borders(cu_k, dev) == n, "cu_q and cu_k describe different numbers of sequences"
     kv = (tk, hk, d)
-    _run("vsa_packed_attn_fwd", stream, (q, k, v, cu_q, cu_k, out, workspace, out_f32, lse),
-         *_rows(q, q.shape), *_rows(k, kv), *_rows(v, kv), cu_q.data_ptr(), cu_k.data_ptr(), *_rows(out, q.shape),
-         _f32(out_f32, q.shape), _f32(lse, (hq, tq)), tq, tk, n, hq, hk, d, int(bool(causal)),
-         *_space(workspace))
+    _run("vsa_packed_attn_fwd", stream, dev, *_rows(q, x, dev), *_rows(k, kv, dev), *_rows(v, kv, dev), cu_q.data_ptr(),
+         cu_k.data_ptr(), *_rows(out, x, dev), _f32(out_f32, x, dev), _f32(lse, (hq, tq), dev), tq, tk, n, hq, hk, d,
+         1 if causal else 0, *_space(workspace, dev))
 
 
 def vsa_packed_attn_bwd(q, k, v, out_f32, dout, cu_q, cu_k, lse, dq, dk, dv, workspace, causal=True, stream=None):
     """Gradients of vsa_packed_attn_fwd, written into dq, dk, dv (bf16, shaped
     as q, k, v; rows may be strided); out_f32 and lse are the forward's."""
-    (tq, hq, d), (tk, hk, _) = _packed_shape(q), _packed_shape(k)
-    n = _borders(cu_q)
-    assert _borders(cu_k) == n, "cu_q and cu_k describe different numbers of sequences"
+    x, (tk, hk, _), dev = _packed_shape(q), _packed_shape(k), _device(q)
+    tq, hq, d = x
+    n = _borders(cu_q, dev)
+    assert _borders(cu_k, dev) == n, "cu_q and cu_k describe different numbers of sequences"
     kv = (tk, hk, d)
-    _run("vsa_packed_attn_bwd", stream, (q, k, v, out_f32, dout, cu_q, cu_k, lse, dq, dk, dv, workspace),
-         *_rows(q, q.shape), *_rows(k, kv), *_rows(v, kv), _f32(out_f32, q.shape), *_rows(dout, q.shape),
-         cu_q.data_ptr(), cu_k.data_ptr(), _f32(lse, (hq, tq)), *_rows(dq, q.shape), *_rows(dk, kv), *_rows(dv, kv),
-         tq, tk, n, hq, hk, d, int(bool(causal)), *_space(workspace))
+    _run("vsa_packed_attn_bwd", stream, dev, *_rows(q, x, dev), *_rows(k, kv, dev), *_rows(v, kv, dev),
+         _f32(out_f32, x, dev), *_rows(dout, x, dev), cu_q.data_ptr(), cu_k.data_ptr(), _f32(lse, (hq, tq), dev),
+         *_rows(dq, x, dev), *_rows(dk, kv, dev), *_rows(dv, kv, dev), tq, tk, n, hq, hk, d, 1 if causal else 0,
+         *_space(workspace, dev))
 
 
 def vsa_decay_attn_workspace_bytes(total, n_seq, heads, head_dim) -> int:
@@ -266,12 +280,12 @@ def vsa_decay_attn_fwd(q, k, v, log_decay, cu, out, workspace, scale=None, state
     [heads]; cu: int32 borders; state_in, state_out (optional): fp32 [n_seq,
     heads, d, d], the states before and after each sequence.  scale: 1/sqrt(d)
     if not given."""
-    (t, h, d), n = _packed_shape(q), _borders(cu)
-    x, st = q.shape, (n, h, d, d)
-    _run("vsa_decay_attn_fwd", stream, (q, k, v, log_decay, cu, out, workspace, state_in, state_out),
-         *_rows(q, x), *_rows(k, x), *_rows(v, x), _f32(log_decay, (h,)), cu.data_ptr(), _f32(state_in, st),
-         _f32(state_out, st), *_rows(out, x), d ** -0.5 if scale is None else scale, t, n, h, d,
-         *_space(workspace))
+    x, dev = _packed_shape(q), _device(q)
+    (t, h, d), n = x, _borders(cu, dev)
+    st = (n, h, d, d)
+    _run("vsa_decay_attn_fwd", stream, dev, *_rows(q, x, dev), *_rows(k, x, dev), *_rows(v, x, dev),
+         _f32(log_decay, (h,), dev), cu.data_ptr(), _f32(state_in, st, dev), _f32(state_out, st, dev), *_rows(out, x, dev),
+         d ** -0.5 if scale is None else scale, t, n, h, d, *_space(workspace, dev))
 
 
 def vsa_decay_attn_bwd(q, k, v, dout, log_decay, cu, dq, dk, dv, workspace, scale=None, state_in=None, dstate_out=None,
@@ -279,23 +293,25 @@ def vsa_decay_attn_bwd(q, k, v, dout, log_decay, cu, dq, dk, dv, workspace, scal
     """Gradients of vsa_decay_attn_fwd, written into dq, dk, dv (bf16) and, if
     given, dstate_in (fp32); dstate_out: the gradient of the states after each
     sequence, if there is one.  The decays are constants."""
-    (t, h, d), n = _packed_shape(q), _borders(cu)
-    x, st = q.shape, (n, h, d, d)
-    _run("vsa_decay_attn_bwd", stream, (q, k, v, dout, log_decay, cu, dq, dk, dv, workspace, state_in, dstate_out, dstate_in),
-         *_rows(q, x), *_rows(k, x), *_rows(v, x), *_rows(dout, x), _f32(log_decay, (h,)), cu.data_ptr(),
-         _f32(state_in, st), _f32(dstate_out, st), *_rows(dq, x), *_rows(dk, x), *_rows(dv, x), _f32(dstate_in, st),
-         d ** -0.5 if scale is None else scale, t, n, h, d, *_space(workspace))
+    x, dev = _packed_shape(q), _device(q)
+    (t, h, d), n = x, _borders(cu, dev)
+    st = (n, h, d, d)
+    _run("vsa_decay_attn_bwd", stream, dev, *_rows(q, x, dev), *_rows(k, x, dev), *_rows(v, x, dev), *_rows(dout, x, dev),
+         _f32(log_decay, (h,), dev), cu.data_ptr(), _f32(state_in, st, dev), _f32(dstate_out, st, dev), *_rows(dq, x, dev),
+         *_rows(dk, x, dev), *_rows(dv, x, dev), _f32(dstate_in, st, dev), d ** -0.5 if scale is None else scale, t, n, h, d,
+         *_space(workspace, dev))
 
 
 def vsa_decay_attn_step(q, k, v, log_decay, state, out, scale=None, state_out=None, stream=None):
     """One new token for each of the sequences: q, k, v, out bf16 [batch, heads,
     d], state fp32 [batch, heads, d, d], updated in place or into state_out."""
-    n, h, d = _packed_shape(q)
-    x, st = q.shape, (n, h, d, d)
+    x, dev = _packed_shape(q), _device(q)
+    n, h, d = x
+    st = (n, h, d, d)
     state_out = state if state_out is None else state_out
-    _run("vsa_decay_attn_step", stream, (q, k, v, log_decay, state, state_out, out),
-         *_rows(q, x), *_rows(k, x), *_rows(v, x), _f32(log_decay, (h,)), _f32(state, st), _f32(state_out, st),
-         *_rows(out, x), d ** -0.5 if scale is None else scale, n, h, d)
+    _run("vsa_decay_attn_step", stream, dev, *_rows(q, x, dev), *_rows(k, x, dev), *_rows(v, x, dev),
+         _f32(log_decay, (h,), dev), _f32(state, st, dev), _f32(state_out, st, dev), *_rows(out, x, dev),
+         d ** -0.5 if scale is None else scale, n, h, d)
 
 
 def vsa_device_status(workspace, stream=None) -> int:
