@@ -591,7 +591,8 @@ struct DecOutBars {
     WorkQueue<DecayWork> queue;
     uint64_t b_full[DecOutCfg<D>::NB], ac_full[DecOutCfg<D>::NAC];
     uint64_t u_done[DecOutCfg<D>::NB];   // every product of a step in this slot of B
-    uint64_t s_full[2], p_ready[2], x_ready, w_ready, o_full, o_free, mma_done, pow_ready;
+    uint64_t s_full[2], p_ready[2], x_ready, w_ready, o_full, o_free, mma_done;
+    uint64_t pow_ready[2];               // of even and odd walks, as the tables
     uint32_t tmem_base;
     int abort;
 };
@@ -627,7 +628,7 @@ decay_out_kernel(const __grid_constant__ DecayPasses passes, const Divisor n_pas
         mbar_init(&bars->o_full, 1);
         mbar_init(&bars->o_free, 128);
         mbar_init(&bars->mma_done, 1);
-        mbar_init(&bars->pow_ready, 64);
+        for (int x = 0; x < 2; ++x) mbar_init(&bars->pow_ready[x], 64);
         fence_barrier_init();
     }
     if (warp == 21) { tmem_alloc(&bars->tmem_base, 512); tmem_relinquish(); }
@@ -851,9 +852,13 @@ decay_out_kernel(const __grid_constant__ DecayPasses passes, const Divisor n_pas
                 const float y = (back ? tid >= 32 : tid < 32) ? ex2((float)(back ? tid - 32 : 31 - tid) * l2) : 0.f;
                 sPow[tid] = y;
                 sPow[64 + 1 + tid] = y;                  // for pairs that start at an odd place
-                mbar_arrive(&bars->pow_ready);
+                mbar_arrive(&bars->pow_ready[k & 1]);
             }
-            if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bars->pow_ready, k & 1, abort_flag)))) break;
+            // (Two warps complete a phase and eight wait for it, so that those two
+            // may be a walk ahead of the others here, which one barrier would let
+            // them leave behind; not two, as the scores of the next walk follow
+            // the weights of all eight in this one.)
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bars->pow_ready[k & 1], (k >> 1) & 1, abort_flag)))) break;
             const int n = chunks(w);
             for (int t = 0; t < n; ++t) {
                 const int step = s0 + t, rows = min(128, w.len - token(w, back, t));
