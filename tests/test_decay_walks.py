@@ -108,3 +108,26 @@ def test_many_walks_of_one_chunk(ops, d):  # noqa: F811
     tol = HALF * (w.abs() @ c.abs() + state) + SLACK * ((a.abs() @ b.abs().transpose(-1, -2) * m) @ c.abs() + state)
     flat = lambda y: y.transpose(1, 2)[here]  # noqa: E731
     check(got["out"], flat(out), flat(tol + HALF * (out.abs() + tol)), "out of all")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+def test_states_of_long_sequences_among_many_short_ones(ops, d):  # noqa: F811
+    """More sequences than the rows have parts (the scan has a place per part's length, not per sequence), all their
+    states wanted, and some of several parts: the first one, one that starts with a part's length of rows, two in a row
+    and the last; the others of one part, of which two are full and one empty."""
+    lens, h = [2] * 150, 2
+    lens[0], lens[64], lens[80], lens[81], lens[149] = 300, 129, 515, 700, 257
+    lens[1], lens[2], lens[100], lens[101] = 128, 0, 127, 1
+    lens[63] = -sum(lens[:63]) % 128                     # sequence 64 starts at a multiple of 128
+    q, k, v, g, s0, r1 = inputs(lens, h, d, True)
+    ld, cu = decays(h), cu_of(lens).cuda()
+    # the workspace holds a state for every 128 rows, twice: that is the length of a part here
+    assert ops.vsa_decay_attn_workspace_bytes(sum(lens), len(lens), h, d) == 256 + 2 * (sum(lens) // 128) * h * d * d * 4
+    assert sum(lens) // 128 < len(lens)
+    got = run(ops, q, k, v, ld, cu, None, s0, g, r1)
+    want = decay_attention(*[x.cpu() for x in (q, k, v, ld, cu)], d ** -0.5, *[x.cpu() for x in (s0, g, r1)])
+    less = run(ops, q, k, v, ld, cu, None, s0, g, r1, want_states=False)   # and where no final states are wanted
+    for r in (got, less):
+        for x in r:
+            check(r[x], want[x], want[x + "_tol"], x)
