@@ -242,6 +242,8 @@ def vsa_packed_attn_fwd(q, k, v, cu_q, cu_k, out, workspace, causal=True, out_f3
     q, out: bf16 [total_q, heads_q, d]; k, v: bf16 [total_k, heads_kv, d] (rows
     may be strided: slices of a fused projection); cu_q, cu_k: int32 borders.
     Query i of a sequence sees keys up to i + nk - nq (causal) or all of them.
+    Room that a cache keeps behind a sequence's keys is passed as a sequence
+    without queries.
     out_f32 [total_q, heads_q, d] and lse [heads_q, total_q] (fp32) are
     written if given; the backward needs both."""
     x, (tk, hk, _), dev = _packed_shape(q), _packed_shape(k), _device(q)

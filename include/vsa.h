@@ -316,6 +316,10 @@ size_t vsa_packed_attn_workspace_bytes(int total_q, int total_k, int n_seq, int 
  * (causal == 0); fp32 online softmax, bf16 tensor-core products.  A query
  * that sees no key gives 0.  nq < nk is a continued prompt, nq == 1 a single
  * new token over a cache of keys.
+ * A cache of keys that is kept in place, with room to grow behind each
+ * sequence, needs no copy: what is not filled yet is passed as a sequence
+ * without queries, with borders cu_q = {0, 1, 1, 2, 2, ...} and
+ * cu_k = {0, n_0, room, room + n_1, 2 room, ...}; n_seq counts those too.
  * out_f32 ([total_q][heads_q][d]) and lse ([heads_q][total_q], log2 of the
  * normaliser of the scaled scores as in vsa_sparse_attn_fwd_train, -inf
  * for a query that sees no key) may be NULL; the backward needs both.
