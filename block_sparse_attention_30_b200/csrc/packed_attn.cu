@@ -30,15 +30,22 @@
 // With NT = 2 a CTA fills the SM, and warp 4 NT + 2 takes over CTAs of the grid
 // that have not started (cluster launch control), so that the set-up is paid
 // once and the next work's loads and products run under this one's last softmax
-// and its epilogue.  Longest works first.
+// and its epilogue.  With the causal mask the works with the most keys of a
+// sequence come first; from sequence to sequence the order is the batch's, the
+// last one first.
 // Few and long sequences (single tokens over a cache): the key axis is split
-// and packed_combine_kernel joins the shares.
+// and packed_combine_kernel joins the shares, as many for every sequence: the
+// host knows the average length only (one cache of 100000 keys among 23 of 100,
+// 40 heads on 8, d 128: 450 us, where alone it takes 105).
 //
 // Measured: one sequence of 8192 tokens, 12 heads, d 128: 203 us, tensor pipe
-// and the exponentials' unit busy 60 % of the time each (a row of 128 scores
-// takes 64 tensor cycles for its two products and as long on that unit, and
-// the two tiles' turns overlap in part); 23296 tokens: 1460 us, 1.14 PFLOP/s,
-// 0.70 of a large library product's rate, with the power cap active.  One token
+// and the exponentials' unit busy 60 % of the time each (at d 128 a block of 128
+// x 128 scores takes 1024 tensor cycles, 16 products of 64, and its 16384
+// exponentials as long at 16 a cycle; the two tiles' turns overlap in part);
+// 23296 tokens: 1460 us, 1.14 PFLOP/s, 0.70 of a large library product's rate,
+// with the power cap active.  At d 64 the products are half of that and the
+// exponentials as many: 163 us and 1046 us (d 128 in the same runs, one call at a
+// time: 214 and 1257).  One token
 // on each of 24 caches, 40 heads on 8 (394 MB): 85 us, 0.71 of the copy rate.
 // The rows of a K/V tile behind the sequence's last key belong to another
 // sequence.  Scores there are masked by selection, whatever they are; V rows

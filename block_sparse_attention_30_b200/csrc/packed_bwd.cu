@@ -700,11 +700,13 @@ static long long key_items(const PackedShape& s) { return ((long long)s.total_k 
 
 // CTAs that share a tile of keys in dK/dV: as many as make its rounds shortest,
 // in units of one row block (1.5 us), 10 of them for a CTA's start and end and
-// 0.75 for each share to add up.  A tile's longest chain of blocks (all rows of a sequence, 2.5
-// times the average one at most) bounds the time from below: few kv heads and a
+// 0.75 for each share to add up.  A tile's longest chain of blocks (all rows of a sequence, taken to
+// be 2.5 times the average one: the lengths are device data, and a longer one makes the estimate
+// worse, not the result) bounds the time from below: few kv heads and a
 // large group make long chains and few of them.  Packed training batch (4128
 // tokens, 16 heads on 4, d 64): 1 share 94 us, 2 shares 66 us, 4 shares 80 us; 4000 tokens, 5
-// heads on 1, d 128, with dQ: 304 and 129 us.
+// heads on 1, d 128, with dQ: 304 and 129 us.  One sequence of 8000 tokens among 15 of 20, 12 heads
+// on 4, d 128: 585 us, as long as alone.
 static int key_shares(const PackedShape& s, int causal) {
     const double per_seq = (double)s.total_q / s.n_seq / (128 / s.group());
     const double longest = std::min(s.n_seq == 1 ? 1.0 : 2.5, (double)s.n_seq) * per_seq, mean = causal ? 0.5 * per_seq : per_seq;
